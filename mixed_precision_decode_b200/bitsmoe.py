@@ -21,6 +21,9 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
 OK, EINVAL, EWIDTH, ESIZE, ECUDA, EFORMAT, ENOMEM = 0, -1, -2, -3, -4, -5, -6
 ST_NONFINITE, ST_BADSCALE, ST_BADEXPERT, ST_TIMEOUT, ST_PLANMISMATCH, ST_BOUNDS = 1, 2, 4, 8, 16, 32
 ST_NOCONVERGE = 64
+ST_BADGROUP = 128
+F32, F16, BF16 = 0, 1, 2  # element types
+SCORING = {"softmax": 0, "sigmoid": 1}
 
 # Every symbol include/bitsmoe.h declares.
 EXPORTS = (
@@ -32,6 +35,9 @@ EXPORTS = (
     "bitsmoe_ffn_down_launches", "bitsmoe_ffn_down", "bitsmoe_ffn_workspace_bytes", "bitsmoe_ffn_launches",
     "bitsmoe_ffn_forward", "bitsmoe_ssd_workspace_bytes", "bitsmoe_ssd_decompose", "bitsmoe_assign_widths",
     "bitsmoe_fqcm_eps", "bitsmoe_fqcm_beta", "bitsmoe_allocate_widths",
+    "bitsmoe_norm_residual", "bitsmoe_topk_route_workspace_bytes", "bitsmoe_topk_route", "bitsmoe_q4_bytes",
+    "bitsmoe_q4_pack", "bitsmoe_q4_unpack", "bitsmoe_ffn_down_q4_workspace_bytes", "bitsmoe_ffn_down_q4_launches",
+    "bitsmoe_ffn_down_q4", "bitsmoe_grouped_matmul",
     "bitsmoe_read_status", "bitsmoe_strerror", "bitsmoe_version",
 )
 
@@ -52,6 +58,12 @@ class FfnDims(ctypes.Structure):
                 ("top_k", ctypes.c_int32)]
 
 
+class GmmDims(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("n_a_rows", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("n_in", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("in_type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
+
+
 class ProjIO(ctypes.Structure):
     _fields_ = [("plan", ctypes.c_void_p), ("blob", ctypes.c_void_p), ("phi_t", ctypes.c_void_p),
                 ("Z", ctypes.c_void_p), ("Y_experts", ctypes.c_void_p), ("Y_sum", ctypes.c_void_p)]
@@ -69,6 +81,7 @@ def lib() -> ctypes.CDLL:
                                f" (checked=True for the bounds-checked build)")
         L = ctypes.CDLL(_LIB_PATH)
         vp, u64, i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int32
+        i64, f32 = ctypes.c_int64, ctypes.c_float
         sig = {
             "bitsmoe_pack_plan": ([ctypes.POINTER(Dims), vp, ctypes.POINTER(vp)], ctypes.c_int),
             "bitsmoe_plan_from_header": ([vp, u64, i32, i32, ctypes.POINTER(vp)], ctypes.c_int),
@@ -105,6 +118,20 @@ def lib() -> ctypes.CDLL:
             "bitsmoe_fqcm_eps": ([vp, i32, i32, i32, vp], ctypes.c_int),
             "bitsmoe_fqcm_beta": ([vp, vp, vp, i32, i32, i32, i32, vp], ctypes.c_int),
             "bitsmoe_allocate_widths": ([vp, vp, vp, i32, i32, i32, u64, vp, vp], ctypes.c_int),
+            "bitsmoe_norm_residual": ([i32, i32, vp, i32, i64, vp, i32, i64, vp, vp, i64, i32, f32, vp, i64, vp, vp, i32,
+                                       i64, f32, vp], ctypes.c_int),
+            "bitsmoe_topk_route_workspace_bytes": ([i32, i32, i32], u64),
+            "bitsmoe_topk_route": ([vp, i32, i64, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp, u64, vp, vp],
+                                   ctypes.c_int),
+            "bitsmoe_q4_bytes": ([i32, i32, i32, i32], u64),
+            "bitsmoe_q4_pack": ([vp, i32, i32, i32, i32, i32, vp, vp, vp], ctypes.c_int),
+            "bitsmoe_q4_unpack": ([vp, i32, i32, i32, i32, vp, vp], ctypes.c_int),
+            "bitsmoe_ffn_down_q4_workspace_bytes": ([ctypes.POINTER(FfnDims), i32, i32], u64),
+            "bitsmoe_ffn_down_q4_launches": ([ctypes.POINTER(FfnDims), i32, i32], ctypes.c_int),
+            "bitsmoe_ffn_down_q4": ([ctypes.POINTER(FfnDims), vp, i32, vp, vp, vp, vp, i32, vp, vp, u64, vp, vp],
+                                    ctypes.c_int),
+            "bitsmoe_grouped_matmul": ([ctypes.POINTER(GmmDims), vp, i64, vp, vp, vp, vp, i32, i32, vp, vp, vp],
+                                       ctypes.c_int),
             "bitsmoe_read_status": ([vp, vp, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
             "bitsmoe_strerror": ([ctypes.c_int], ctypes.c_char_p),
             "bitsmoe_version": ([], ctypes.c_int),
@@ -367,6 +394,201 @@ def allocate_widths(amps_host, beta_host, eps_host, d_out: int, budget_bits: int
     _check(lib().bitsmoe_allocate_widths(a.ctypes.data, b.ctypes.data, e.ctypes.data, E, r, d_out, int(budget_bits),
                                          w.ctypes.data, ctypes.byref(loss)), "allocate_widths")
     return w, float(loss.value)
+
+
+# ---- the block around the routed experts ----
+_TYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+
+def _refuse(what: str, why: str):
+    raise BitsMoEError(EINVAL, f"{what}: {why}")
+
+
+def _type(what: str, name: str, t: torch.Tensor) -> int:
+    code = _TYPE.get(t.dtype)
+    if code is None:
+        _refuse(what, f"{name} is {t.dtype}, not float32, float16 or bfloat16")
+    return code
+
+
+def _rows(what: str, name: str, t: torch.Tensor, shape: tuple) -> int:
+    """Row stride of a 2-D operand with unit column stride."""
+    if t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+        _refuse(what, f"{name} is not {list(shape)} with contiguous rows")
+    return t.stride(0)
+
+
+def _dense(what: str, name: str, t: torch.Tensor, dtype, shape: tuple) -> int:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(what, f"{name} is not a contiguous {dtype} tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _launch(what: str, call, tensors, args: tuple, stream):
+    """Calls the library on the device of the tensors, which they share; the stream
+    defaults to torch's current stream there."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (t.device != dev or not t.is_cuda):
+            _refuse(what, "the tensors are not on one GPU")
+    if dev.index == torch.cuda.current_device():
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = call(*args, _stream(stream))
+    if rc != 0:
+        raise BitsMoEError(rc, what)
+
+
+def norm_residual(h, y=None, w_pre=None, x=None, *, w_post=None, gate=None, alpha: float = 1.0, eps: float = 1e-6,
+                  h_out=None, stream=None):
+    """h' = h + alpha * gate * (y, or y normalised with w_post); x = h' normalised with w_pre.
+
+    h, y, x [T][d] in float32, float16 or bfloat16, any row stride; gate float32 [T or 1][d or 1];
+    w_pre, w_post [d] float32.  h' goes to h_out (default: h itself when y is given), x is written
+    when given."""
+    what = "norm_residual"
+    if h.dim() != 2:
+        _refuse(what, "h is not [T][d]")
+    T, d = shape = h.shape
+    if h_out is None and y is not None:
+        h_out = h
+    ht = _type(what, "h", h)
+    hs, yt, ys, hos, xt, xs, gs, gc = _rows(what, "h", h, shape), 0, 0, 0, 0, 0, 0, 0
+    if y is not None:
+        yt, ys = _type(what, "y", y), _rows(what, "y", y, shape)
+    if h_out is not None:
+        if h_out.dtype != h.dtype:
+            _refuse(what, "h_out has another type than h")
+        hos = _rows(what, "h_out", h_out, shape)
+    if x is not None:
+        xt, xs = _type(what, "x", x), _rows(what, "x", x, shape)
+        if w_pre is None:
+            _refuse(what, "x needs w_pre")
+    if gate is not None:
+        if (gate.dtype != torch.float32 or gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, d)
+                or (gate.shape[1] > 1 and gate.stride(1) != 1)):
+            _refuse(what, "gate is not float32 [T or 1][d or 1] with contiguous rows")
+        gs = gate.stride(0) if gate.shape[0] > 1 else 0
+        gc = gate.shape[1] > 1
+    wo = None if w_post is None else _dense(what, "w_post", w_post, torch.float32, (d,))
+    wi = None if w_pre is None else _dense(what, "w_pre", w_pre, torch.float32, (d,))
+    _launch(what, lib().bitsmoe_norm_residual, (h, y, w_post, gate, h_out, w_pre, x),
+            (T, d, h.data_ptr(), ht, hs, _ptr(y), yt, ys, wo, _ptr(gate), gs, gc, alpha, _ptr(h_out), hos, wi, _ptr(x), xt,
+             xs, eps), stream)
+
+
+def topk_route_workspace_bytes(T: int, n_experts: int, top_k: int) -> int:
+    return int(lib().bitsmoe_topk_route_workspace_bytes(T, n_experts, top_k))
+
+
+def topk_route(logits, topk_ids, gate_w, offsets=None, order=None, *, scoring: str = "softmax",
+               renormalise: bool = True, scale: float = 1.0, workspace=None, status=None, stream=None):
+    """The top_k largest logits [T][E] of every token into topk_ids [T][top_k] int32 and their weights
+    into gate_w [T][top_k] float32; with offsets [E+1] and order [T*top_k] (int32) also the pairs
+    t*top_k + slot grouped by expert."""
+    what = "topk_route"
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        _refuse(what, "logits or topk_ids is not 2-D")
+    T, E = shape = logits.shape
+    K = topk_ids.shape[1]
+    if scoring not in SCORING:
+        _refuse(what, f"scoring {scoring!r} is neither softmax nor sigmoid")
+    lt, ls = _type(what, "logits", logits), _rows(what, "logits", logits, shape)
+    ids = _dense(what, "topk_ids", topk_ids, torch.int32, (T, K))
+    gw = _dense(what, "gate_w", gate_w, torch.float32, (T, K))
+    off = None if offsets is None else _dense(what, "offsets", offsets, torch.int32, (E + 1,))
+    od = None if order is None else _dense(what, "order", order, torch.int32, (T * K,))
+    _launch(what, lib().bitsmoe_topk_route, (logits, topk_ids, gate_w, offsets, order, workspace, status),
+            (logits.data_ptr(), lt, ls, T, E, K, SCORING[scoring], renormalise, scale, ids, gw, off, od, _ptr(workspace),
+             0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status)), stream)
+
+
+def q4_bytes(n_experts: int, rows: int, cols: int, group: int) -> int:
+    return int(lib().bitsmoe_q4_bytes(n_experts, rows, cols, group))
+
+
+def q4_pack(W, group: int, blob, status=None, stream=None):
+    """W [E][rows][cols] (float32, float16 or bfloat16) into 4 bits with a scale per `group` columns."""
+    what = "q4_pack"
+    if W.dim() != 3 or not W.is_contiguous():
+        _refuse(what, "W is not a contiguous [E][rows][cols]")
+    E, rows, cols = W.shape
+    n = q4_bytes(E, rows, cols, group)
+    if n == 0:
+        _refuse(what, f"group {group} is not 32, 64 or 128, or W is empty")
+    if blob.dtype != torch.uint8 or not blob.is_contiguous() or blob.numel() < n:
+        raise BitsMoEError(ESIZE, f"{what}: blob is not {n} contiguous bytes")
+    _launch(what, lib().bitsmoe_q4_pack, (W, blob, status),
+            (W.data_ptr(), _type(what, "W", W), E, rows, cols, group, blob.data_ptr(), _ptr(status)), stream)
+
+
+def q4_unpack(blob, group: int, W, stream=None):
+    """The stored values of packed matrices into W [E][rows][cols] float32."""
+    what = "q4_unpack"
+    if W.dim() != 3:
+        _refuse(what, "W is not [E][rows][cols]")
+    E, rows, cols = W.shape
+    wp = _dense(what, "W", W, torch.float32, (E, rows, cols))
+    n = q4_bytes(E, rows, cols, group)
+    if n == 0 or blob.numel() < n:
+        raise BitsMoEError(ESIZE if n else EINVAL, f"{what}: blob of {blob.numel()} bytes, {n} needed")
+    _launch(what, lib().bitsmoe_q4_unpack, (blob, W), (blob.data_ptr(), E, rows, cols, group, wp), stream)
+
+
+def ffn_down_q4_workspace_bytes(dims: FfnDims, group: int, T: int) -> int:
+    return int(lib().bitsmoe_ffn_down_q4_workspace_bytes(ctypes.byref(dims), group, T))
+
+
+def ffn_down_q4_launches(dims: FfnDims, group: int, T: int) -> int:
+    n = int(lib().bitsmoe_ffn_down_q4_launches(ctypes.byref(dims), group, T))
+    if n < 0:
+        raise BitsMoEError(n, "ffn_down_q4_launches")
+    return n
+
+
+def ffn_down_q4(dims: FfnDims, blob, group: int, Y_gate, Y_up, topk_ids, gate_w, T: int, out, workspace=None,
+                workspace_bytes: int = 0, status=None, stream=None):
+    """ffn_down with the down matrices in 4 bits (q4_pack).  Y_up None: h = Y_gate, no activation."""
+    what = "ffn_down_q4"
+    K = dims.top_k
+    yg = _dense(what, "Y_gate", Y_gate, torch.float32, (T, K, dims.d_ff))
+    yu = None if Y_up is None else _dense(what, "Y_up", Y_up, torch.float32, (T, K, dims.d_ff))
+    ids = _dense(what, "topk_ids", topk_ids, torch.int32, (T, K))
+    gw = _dense(what, "gate_w", gate_w, torch.float32, (T, K))
+    op = _dense(what, "out", out, torch.float32, (T, dims.d_model))
+    n = q4_bytes(dims.n_experts, dims.d_model, dims.d_ff, group)
+    if n == 0 or blob.numel() < n:
+        raise BitsMoEError(ESIZE if n else EINVAL, f"{what}: blob of {blob.numel()} bytes, {n} needed")
+    _launch(what, lib().bitsmoe_ffn_down_q4, (blob, Y_gate, Y_up, topk_ids, gate_w, out, workspace, status),
+            (ctypes.byref(dims), blob.data_ptr(), group, yg, yu, ids, gw, T, op, _ptr(workspace), workspace_bytes,
+             _ptr(status)), stream)
+
+
+def grouped_matmul(A, W, offsets, out, *, W_up=None, rows=None, rows_per_a: int = 1, scatter: bool = False, status=None,
+                   stream=None):
+    """Sorted rows times their expert's matrix: out row i = W[e] a_i for offsets[e] <= i < offsets[e+1],
+    or SiLU(W[e] a_i) * (W_up[e] a_i) with W_up.
+
+    A [*][K] and W, W_up [E][N][K] float16 or bfloat16; out [n][N] of the same type or float32.
+    a_i is row i of A, or with rows [n] int32 row rows[i] // rows_per_a; with scatter the result
+    goes to row rows[i] of out."""
+    what = "grouped_matmul"
+    if A.dim() != 2 or W.dim() != 3 or out.dim() != 2:
+        _refuse(what, "A, W and out are not [*][K], [E][N][K] and [n][N]")
+    E, N, K = W.shape
+    n = out.shape[0]
+    it, ot = _type(what, "A", A), _type(what, "out", out)
+    ap = A.data_ptr()
+    lda = _rows(what, "A", A, (A.shape[0], K)) if A.shape[0] > 1 else K
+    wp = _dense(what, "W", W, A.dtype, (E, N, K))
+    up = None if W_up is None else _dense(what, "W_up", W_up, A.dtype, (E, N, K))
+    op = _dense(what, "out", out, out.dtype, (n, N))
+    off = _dense(what, "offsets", offsets, torch.int32, (E + 1,))
+    rp = None if rows is None else _dense(what, "rows", rows, torch.int32, (n,))
+    dims = GmmDims(n, A.shape[0], N, K, E, it, ot)
+    _launch(what, lib().bitsmoe_grouped_matmul, (A, W, W_up, offsets, rows, out, status),
+            (ctypes.byref(dims), ap, lda, wp, up, off, rp, rows_per_a, scatter, op, _ptr(status)), stream)
 
 
 def read_status(status, stream=None) -> int:

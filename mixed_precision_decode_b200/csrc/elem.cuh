@@ -1,0 +1,98 @@
+// elem.cuh -- element types of the block operators (norms, routing, grouped
+// products): loads and stores that convert between fp32 arithmetic and fp32, fp16
+// or bf16 memory, the type chosen at run time (uniform over a launch), and the
+// launch helper that lets a kernel's start overlap the end of the kernel before it.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace bitsmoe {
+
+__host__ __device__ constexpr int elem_bytes(int type) { return type == BITSMOE_F32 ? 4 : 2; }
+inline bool elem_ok(int type) { return type == BITSMOE_F32 || type == BITSMOE_F16 || type == BITSMOE_BF16; }
+
+__device__ __forceinline__ float half_bits(uint32_t b, int type) {
+    return type == BITSMOE_F16 ? __half2float(__ushort_as_half((unsigned short)b)) : __uint_as_float(b << 16);
+}
+__device__ __forceinline__ uint32_t to_half_bits(float v, int type) {
+    return type == BITSMOE_F16 ? (uint32_t)__half_as_ushort(__float2half_rn(v))
+                               : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
+    return to_half_bits(a, type) | (to_half_bits(b, type) << 16);
+}
+
+// V elements (8: 16-byte aligned; 1: any) from element i of p.
+template <int V>
+__device__ __forceinline__ void load_elems(const void* p, int type, int64_t i, float (&v)[V]) {
+    if constexpr (V == 8) {
+        if (type == BITSMOE_F32) {
+            const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+            const float4 a = f[0], b = f[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                v[2 * j] = half_bits(u[j] & 0xffffu, type);
+                v[2 * j + 1] = half_bits(u[j] >> 16, type);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            v[j] = type == BITSMOE_F32 ? static_cast<const float*>(p)[i + j]
+                                       : half_bits(static_cast<const uint16_t*>(p)[i + j], type);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_elems(void* p, int type, int64_t i, const float (&v)[V]) {
+    if constexpr (V == 8) {
+        if (type == BITSMOE_F32) {
+            float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+            f[0] = make_float4(v[0], v[1], v[2], v[3]);
+            f[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+                make_uint4(pack2(v[0], v[1], type), pack2(v[2], v[3], type), pack2(v[4], v[5], type),
+                           pack2(v[6], v[7], type));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            if (type == BITSMOE_F32)
+                static_cast<float*>(p)[i + j] = v[j];
+            else
+                static_cast<uint16_t*>(p)[i + j] = (uint16_t)to_half_bits(v[j], type);
+        }
+    }
+}
+
+// Programmatic dependent launch: the wait returns when every kernel before this one
+// in the stream has finished and its writes are visible; the trigger lets the next
+// kernel (if it was launched the same way) start its own pre-wait part.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... KArgs, typename... Args>
+inline int launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    return e == cudaSuccess ? BITSMOE_OK : set_cuda_error(e);
+}
+
+}  // namespace bitsmoe

@@ -1,0 +1,575 @@
+"""The operators around the routed experts -- the norms with the gated residual, the
+router with its grouped pairs, the 4-bit down projection and the products grouped by
+expert -- against plain implementations in 64 bits.
+
+Tolerances count roundings.  eps(t) / 2 of the value for one rounding to type t;
+2^-24 relative for an fp32 operation, 2^-23 for an addition inside a tensor-core
+instruction (it may truncate).  A sum of n terms v taken in N sequential additions is
+off by at most N 2^-23 sum|v|."""
+import numpy as np
+import pytest
+import torch
+
+from mixed_precision_decode_b200 import bitsmoe as B
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+U24, U23 = 2.0 ** -24, 2.0 ** -23
+TINY = {F32: 2.0 ** -149, F16: 2.0 ** -24, BF16: 2.0 ** -133}  # smallest subnormals
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def _rounding(ref, dtype):
+    """Bound of one rounding of ref to dtype."""
+    return ref.abs() * (torch.finfo(dtype).eps / 2) + TINY[dtype]
+
+
+def _within(got, ref, tol, what):
+    err = (got.double() - ref).abs()
+    bad = ~(err <= tol)
+    assert not bool(bad.any()), (what, int(bad.sum()), float((err / tol).nan_to_num(nan=np.inf).max()))
+
+
+# ---------------------------------------------------------------------------
+# norms and residual
+# ---------------------------------------------------------------------------
+def _norm_ref(h, y, w_pre, w_post, gate, alpha, eps):
+    """(h', x, bound of h' before rounding, bound of x before rounding), float64.  A row's sum of squares is
+    taken in at most 60 sequential additions, so its inverse root is off by 32 units, the factors by one each."""
+    c = 64 * U24
+    h = h.double()
+    v, size = h, h.abs()
+    if y is not None:
+        u = y.double()
+        if w_post is not None:
+            u = u / torch.sqrt(u.square().mean(1, keepdim=True) + eps) * w_post.double()
+        u = alpha * u * (gate.double() if gate is not None else 1.0)
+        v, size = h + u, h.abs() + u.abs()
+    x = None
+    if w_pre is not None:
+        r = 1.0 / torch.sqrt(v.square().mean(1, keepdim=True) + eps)
+        x = v * r * w_pre.double()
+        # the error of h' and that of the root
+        tx = c * (size * r * w_pre.double().abs() + x.abs() * (1 + (size.square().mean(1, keepdim=True)).sqrt() * r))
+        return v, x, c * size, tx
+    return v, x, c * size, None
+
+
+NORM_CASES = [
+    # T, d, h, y, x, post, gate
+    (1, 2048, F32, F32, F16, False, None),
+    (1, 1, F32, F32, F32, True, None),
+    (3, 7, F16, BF16, F32, True, "token"),
+    (5, 8, BF16, F32, BF16, False, "channel"),
+    (333, 1001, F16, F32, F16, False, "token"),
+    (17, 256, BF16, F16, F16, True, "both"),
+    (9, 520, F32, F32, BF16, True, "one"),
+    (65, 1024, F16, F16, F16, True, "channel"),
+    (4, 1032, F32, F32, F16, False, "both"),
+    (7, 4096, BF16, F32, BF16, True, "channel"),
+    (2, 8192, F32, BF16, F32, True, "token"),
+    (2, 16384, F16, F16, F16, False, None),
+    (2, 40000, F32, F32, F16, True, "channel"),   # wider than registers, 16-byte rows
+    (2, 20001, BF16, F32, F16, True, "both"),     # wider than registers, any alignment
+    (2, 5003, F16, F32, F32, True, "token"),
+]
+
+
+def _gate(g, kind, T, d):
+    shape = {None: None, "token": (T, 1), "channel": (1, d), "both": (T, d), "one": (1, 1)}[kind]
+    return None if shape is None else torch.sigmoid(_randn(g, *shape))
+
+
+@pytest.mark.parametrize("case", NORM_CASES, ids=[f"{c[0]}x{c[1]}" for c in NORM_CASES])
+@pytest.mark.parametrize("place", ["dense", "strided", "in_place"])
+def test_norm_residual(case, place):
+    T, d, ht, yt, xt, post, kind = case
+    g = _gen(T * 10007 + d)
+    pad = 0 if place != "strided" else 5
+
+    def make(t, scale):
+        buf = (scale * _randn(g, T, d + pad)).to(t)
+        return buf[:, pad:] if pad else buf
+
+    h, y = make(ht, 2.0), make(yt, 0.5)
+    h_in = h.clone()
+    x = torch.full((T, d + pad), float("nan"), dtype=xt, device="cuda")[:, :d]
+    w_pre = 1 + 0.1 * _randn(g, d)
+    w_post = 1 + 0.1 * _randn(g, d) if post else None
+    gate = _gate(g, kind, T, d)
+    out = None if place == "in_place" else torch.full((T, d + pad), float("nan"), dtype=ht, device="cuda")[:, :d]
+    B.norm_residual(h, y, w_pre, x, w_post=w_post, gate=gate, alpha=0.7, eps=1e-5, h_out=out)
+    rh, rx, th, tx = _norm_ref(h_in, y, w_pre, w_post, gate, 0.7, 1e-5)
+    got = h if out is None else out
+    _within(got, rh, th + _rounding(rh, ht), "h'")
+    _within(x, rx, tx + _rounding(rx, xt), "x")
+    if out is not None:
+        assert torch.equal(h, h_in)
+
+
+def test_norm_residual_parts():
+    """The norm alone, the residual alone, and nothing written beside them."""
+    g = _gen(3)
+    h, y, w = _randn(g, 6, 96), _randn(g, 6, 96), _randn(g, 96)
+    x = torch.empty(6, 96, device="cuda", dtype=F16)
+    h0 = h.clone()
+    B.norm_residual(h, w_pre=w, x=x)
+    rh, rx, th, tx = _norm_ref(h, None, w, None, None, 1.0, 1e-6)
+    _within(x, rx, tx + _rounding(rx, F16), "norm alone")
+    assert torch.equal(h, h0)
+    B.norm_residual(h, y, alpha=-0.5)
+    rh, _, th, _ = _norm_ref(h0, y, None, None, None, -0.5, 1e-6)
+    _within(h, rh, th + _rounding(rh, F32), "residual alone")
+    B.norm_residual(h[:0], y[:0], w, x[:0])  # no rows
+
+
+@pytest.mark.parametrize("d", [64, 2048, 40000])
+def test_norm_residual_special_rows(d):
+    """A row of zeros gives zeros; a NaN stays in its row."""
+    g = _gen(4)
+    h, w = _randn(g, 4, d), torch.ones(d, device="cuda")
+    y = torch.zeros(4, d, device="cuda")
+    h[1] = 0
+    h[2, d // 2] = float("nan")
+    x = torch.empty(4, d, device="cuda")
+    B.norm_residual(h, y, w, x, w_post=w)
+    assert bool((x[1] == 0).all()) and bool(torch.isnan(x[2]).all())
+    assert bool(torch.isfinite(x[0]).all()) and bool(torch.isfinite(x[3]).all())
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+def _route_ref(logits, K, scoring, renorm, scale):
+    """ids, weights (float64), offsets, order on the CPU; rows with a NaN or +inf give -1 and 0."""
+    l = logits.cpu().double()
+    T, E = l.shape
+    v, i = torch.sort(l, dim=1, descending=True, stable=True)
+    ok = v[:, :K] > -np.inf
+    ok &= (l < np.inf).all(1, keepdim=True)  # false for NaN too
+    if scoring == "softmax":
+        w = torch.exp(v[:, :K] - v[:, :1].clamp_min(-1e300))
+        tot = torch.exp(l - v[:, :1].clamp_min(-1e300)).sum(1, keepdim=True)
+    else:
+        w, tot = 1 / (1 + torch.exp(-v[:, :K])), torch.ones(T, 1, dtype=torch.float64)
+    w = torch.where(ok, w, torch.zeros_like(w))
+    if renorm:
+        tot = w.sum(1, keepdim=True)
+    w = torch.where(ok, scale * w / tot, torch.zeros_like(w))
+    ids = torch.where(ok, i[:, :K], -1)
+    key = torch.where(ids < 0, E, ids).reshape(-1)
+    order = torch.sort(key, stable=True).indices
+    n = int((key < E).sum())
+    order[n:] = -1
+    offsets = torch.zeros(E + 1, dtype=torch.long)
+    offsets[1:] = torch.bincount(key, minlength=E + 1)[:E].cumsum(0)
+    return ids, w, offsets, order
+
+
+def _route(logits, K, groups=True, **kw):
+    T, E = logits.shape
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    ids, gw = torch.full((T, K), -7, **i32), torch.full((T, K), float("nan"), device="cuda")
+    off, order = (torch.full((E + 1,), -7, **i32), torch.full((T * K,), -7, **i32)) if groups else (None, None)
+    st = torch.zeros(1, **i32)
+    n = B.topk_route_workspace_bytes(T, E, K)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+    B.topk_route(logits, ids, gw, off, order, workspace=ws, status=st, **kw)
+    return ids, gw, off, order, B.read_status(st)
+
+
+def _check_route(logits, K, scoring, renorm, scale=1.0, status=0):
+    ids, gw, off, order, st = _route(logits, K, scoring=scoring, renormalise=renorm, scale=scale)
+    rids, rw, roff, rorder = _route_ref(logits, K, scoring, renorm, scale)
+    assert st == status
+    assert torch.equal(ids.cpu().long(), rids)
+    assert torch.equal(off.cpu().long(), roff)
+    assert torch.equal(order.cpu().long(), rorder)
+    # the exponent's argument is off by one unit of |l - m| (up to ~30 here), exp by two, the sum by its additions
+    _within(gw.cpu(), rw, 128 * U24 * rw.abs() + TINY[F32], "weights")
+
+
+ROUTE_CASES = [
+    (1, 1, 1), (1, 128, 8), (2, 5, 5), (31, 33, 3), (64, 128, 8), (128, 64, 6), (129, 128, 8), (1000, 200, 7),
+    (5000, 128, 8), (300, 512, 16), (40, 513, 9), (500, 2000, 40), (3, 300, 64), (700, 32, 32), (260, 8192, 2),
+]
+
+
+@pytest.mark.parametrize("case", ROUTE_CASES, ids=["x".join(map(str, c)) for c in ROUTE_CASES])
+@pytest.mark.parametrize("mode", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)],
+                         ids=lambda m: m[0] + ("_renorm" if m[1] else ""))
+def test_topk_route(case, mode):
+    T, E, K = case
+    g = _gen(T + 31 * E + K)
+    dtype = (F32, F16, BF16)[(T + E) % 3]  # 16-bit logits have many equal values
+    logits = (1.5 * _randn(g, T, E)).to(dtype)
+    _check_route(logits, K, *mode, scale=2.5)
+
+
+@pytest.mark.parametrize("T", [40, 400])
+def test_topk_route_closed_and_bad_rows(T):
+    """Closed experts, rows without any open one, ties of integers and of signed zeros, a strided operand,
+    rows with NaN and +inf."""
+    g = _gen(T)
+    buf = torch.round(2 * _randn(g, T, 70))
+    buf[buf == 0] *= -1.0
+    logits = buf[:, 3:63]
+    shut = torch.rand((T, 60), generator=g, device="cuda") < 0.7
+    logits.masked_fill_(shut, float("-inf"))
+    logits[5] = float("-inf")
+    logits[T - 1, 1:] = float("-inf")
+    for mode in (("softmax", True), ("softmax", False), ("sigmoid", True)):
+        _check_route(logits, 9, *mode)
+    logits[2, 7] = float("nan")
+    logits[3, 59] = float("inf")
+    _check_route(logits, 9, "softmax", True, status=B.ST_NONFINITE)
+    _check_route(logits[:, :4], 4, "softmax", True)
+
+
+def test_topk_route_extremes():
+    """Logits whose exponentials leave fp32's range; every token on one expert; nothing but the ids."""
+    l = torch.tensor([[3e38, -3e38, 0.0], [-200.0, -210.0, -3e38], [88.0, 89.0, 200.0]], device="cuda")
+    for mode in (("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)):
+        ids, gw, _, _, st = _route(l, 2, scoring=mode[0], renormalise=mode[1])
+        rids, rw, _, _ = _route_ref(l, 2, mode[0], mode[1], 1.0)
+        assert st == 0 and torch.equal(ids.cpu().long(), rids)
+        # arguments up to 210 here: one unit of them in the exponent
+        _within(gw.cpu(), rw, 512 * U24 * rw.abs() + 2.0 ** -125, mode)
+    one = torch.zeros(300, 16, device="cuda")
+    one[:, 11] = 1.0
+    _check_route(one, 1, "softmax", True)
+    ids, _, _, _, _ = _route(one, 1, groups=False)
+    assert bool((ids == 11).all())
+    off = torch.full((17,), -1, dtype=torch.int32, device="cuda")
+    z = torch.empty(0, 1, dtype=torch.int32, device="cuda")
+    B.topk_route(one[:0], z, z.float(), off)
+    assert bool((off == 0).all())
+
+
+# ---------------------------------------------------------------------------
+# 4-bit matrices
+# ---------------------------------------------------------------------------
+def _q4_ref(W, G):
+    """Codes and fp16 scales of W [E][rows][cols] by the stated quantiser (fp32 operations, as stated)."""
+    W = W.float().cpu().numpy()
+    E, R, C = W.shape
+    Cp = -(-C // G) * G
+    w = np.zeros((E, R, Cp), np.float32)
+    w[:, :, :C] = W
+    w = w.reshape(E, R, Cp // G, G)
+    s = (np.float32(2) * np.abs(w).max(3) / np.float32(15)).astype(np.float16)
+    sf = s.astype(np.float32)[..., None]
+    with np.errstate(divide="ignore", invalid="ignore"):
+        q = np.where(sf > 0, np.clip(np.floor(w / sf + np.float32(8)), 0, 15), 0)
+    return q.reshape(E, R, Cp)[:, :, :C].astype(np.int64), s
+
+
+def _q4_blob(W, G):
+    blob = torch.full((B.q4_bytes(*W.shape, G),), 0xAB, dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.q4_pack(W, G, blob, st)
+    return blob, B.read_status(st)
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 37, 24), (3, 16, 64), (2, 50, 200), (1, 130, 328)])
+def test_q4_pack_format(shape, G):
+    """The packed bytes, decoded by the format's text, hold the quantiser's codes and scales; padding is zero;
+    unpacking gives s (q - 7.5)."""
+    E, R, C = shape
+    g = _gen(R * C + G)
+    W = _randn(g, E, R, C).to((F32, F16, BF16)[(R + G // 32) % 3])
+    W[0, 0, : min(C, G)] = 0  # a group of zeros
+    blob, st = _q4_blob(W, G)
+    assert st == 0
+    q, s = _q4_ref(W, G)
+    Cp, nb = -(-C // max(64, G)) * max(64, G), -(-R // 16)
+    blocks = blob.cpu().numpy().reshape(E, nb, -1)
+    words = blocks[:, :, : 8 * Cp].copy().view(np.uint32).reshape(E, nb, Cp // 64, 32, 4)
+    scales = blocks[:, :, 8 * Cp:].copy().view(np.float16).reshape(E, nb, Cp // G, 16)
+    want_q = np.zeros((E, nb * 16, Cp), np.int64)
+    want_q[:, :R, :C] = q
+    got_q = np.zeros_like(want_q)
+    for lane in range(32):
+        a, b = lane // 4, lane % 4
+        for t in range(4):
+            for p in range(2):
+                for u in range(2):
+                    for v in range(2):
+                        n = 4 * p + 2 * u + v
+                        got_q[:, a + 8 * v::16, 16 * t + 8 * u + 2 * b + p::64] = words[:, :, :, lane, t] >> (4 * n) & 15
+    assert np.array_equal(got_q, want_q)
+    want_s = np.zeros((E, nb * 16, Cp // G), np.float16)
+    want_s[:, :R, : s.shape[2]] = s
+    got_s = scales.transpose(0, 1, 3, 2).reshape(E, nb * 16, Cp // G)
+    assert np.array_equal(got_s.view(np.uint16), want_s.view(np.uint16))
+    out = torch.empty(E, R, C, device="cuda")
+    B.q4_unpack(blob, G, out)
+    ref = (want_q[:, :R, :C] - 7.5) * np.repeat(want_s[:, :R].astype(np.float64), G, 2)[:, :, :C]
+    assert np.array_equal(out.cpu().numpy(), ref.astype(np.float32))
+
+
+def test_q4_pack_bad_groups():
+    """A NaN, an infinity and a scale beyond fp16 store their group as zeros and set the status; others stay."""
+    W = torch.ones(1, 4, 128, device="cuda")
+    W[0, 1, 5] = float("nan")
+    W[0, 2, 70] = float("inf")
+    W[0, 3, 0] = 1e6
+    blob, st = _q4_blob(W, 64)
+    assert st == B.ST_NONFINITE | B.ST_BADSCALE
+    out = torch.empty(1, 4, 128, device="cuda")
+    B.q4_unpack(blob, 64, out)
+    zero = torch.zeros(4, 2, dtype=torch.bool)
+    zero[1, 0] = zero[2, 1] = zero[3, 0] = True
+    got = (out.view(4, 2, 64) == 0).all(2).cpu()
+    assert torch.equal(got, zero)
+
+
+Q4_CASES = [
+    # d_model, d_ff, E, K, T's
+    (64, 32, 4, 2, (1, 4)),
+    (37, 24, 6, 3, (1, 5, 40)),
+    (16, 8, 3, 2, (1, 3)),
+    (300, 136, 5, 5, (1, 2, 21)),
+    (256, 64, 4, 2, (48, 130)),
+    (2048, 768, 128, 8, (1, 2, 16, 64)),
+    (1000, 4104, 8, 2, (1, 7)),
+    (96, 14336, 8, 2, (1, 5)),
+    (33, 520, 1, 1, (1, 100)),
+    (64, 4096, 40, 24, (1, 3)),
+]
+
+
+def _q4_inputs(d_model, d_ff, E, K, T, seed, up=True):
+    g = _gen(seed)
+    W = _randn(g, E, d_model, d_ff) * d_ff ** -0.5
+    yg, yu = 2 * _randn(g, T, K, d_ff), _randn(g, T, K, d_ff) if up else None
+    ids = torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :K].to(torch.int32).contiguous()
+    return W, yg, yu, ids, torch.softmax(_randn(g, T, K), 1)
+
+
+def _q4_run(dims, blob, G, yg, yu, ids, gw, out=None, stream=None):
+    T = ids.shape[0]
+    out = torch.full((T, dims.d_model), float("nan"), device="cuda") if out is None else out
+    n = B.ffn_down_q4_workspace_bytes(dims, G, T)
+    ws = torch.full((max(n, 256),), 0xFF, dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.ffn_down_q4(dims, blob, G, yg, yu, ids, gw, T, out, ws, n, st)
+    return out, B.read_status(st)
+
+
+def _q4_down_ref(blob, shape, G, yg, yu, ids, gw):
+    """(out, bound), float64 on the GPU, expert by expert, from the unpacked values."""
+    E, R, C = shape
+    W = torch.empty(shape, device="cuda")
+    B.q4_unpack(blob, G, W)
+    T, K = ids.shape
+    h = yg.double().view(T * K, C)
+    if yu is not None:
+        h = h * torch.sigmoid(h) * yu.double().view(T * K, C)
+    y, size = torch.zeros(T * K, R, dtype=torch.float64, device="cuda"), torch.zeros(T * K, R, dtype=torch.float64, device="cuda")
+    flat = ids.view(-1)
+    for e in range(E):
+        at = (flat == e).nonzero().view(-1)
+        if at.numel():
+            y[at] = h[at] @ W[e].double().T
+            size[at] = h[at].abs() @ W[e].double().abs().T
+    g = gw.double().view(T, K, 1)
+    # h: a few units of fp32 (exp, division, product) and 2^-22 from its two fp16 parts; the sum: G / 16 steps
+    # inside a group, the groups, at most 8 column ranges, the slots
+    n = G // 16 + C // G + 8 + K + 4
+    return (y.view(T, K, R) * g).sum(1), ((n * U23 + 2.0 ** -22 + 8 * U24) * size.view(T, K, R) * g.abs()).sum(1) + 1e-37
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("case", Q4_CASES, ids=["x".join(map(str, c[:4])) for c in Q4_CASES])
+def test_ffn_down_q4(case, G):
+    d_model, d_ff, E, K, tokens = case
+    dims = B.ffn_dims(d_model, d_ff, E, K)
+    for T in tokens:
+        W, yg, yu, ids, gw = _q4_inputs(d_model, d_ff, E, K, T, 17 * T + d_ff)
+        blob, st = _q4_blob(W, G)
+        assert st == 0
+        for up in (yu, None):
+            out, st = _q4_run(dims, blob, G, yg, up, ids, gw)
+            assert st == 0
+            ref, tol = _q4_down_ref(blob, W.shape, G, yg, up, ids, gw)
+            _within(out, ref, tol, (T, up is None))
+
+
+@pytest.mark.parametrize("T", [1, 6])
+def test_ffn_down_q4_ids(T):
+    """Ids outside [0, E) are left out and reported; the same expert in two slots; every token on one expert; a
+    token without any expert."""
+    W, yg, yu, ids, gw = _q4_inputs(80, 96, 5, 3, T, 5 + T)
+    dims = B.ffn_dims(80, 96, 5, 3)
+    blob, _ = _q4_blob(W, 32)
+    for edit, bad in ((lambda i: i.__setitem__((0, 1), -1), True), (lambda i: i.__setitem__((T - 1, 0), 5), True),
+                      (lambda i: i.fill_(3), False), (lambda i: i[0].fill_(-1), True), (lambda i: i.fill_(99), True)):
+        j = ids.clone()
+        edit(j)
+        out, st = _q4_run(dims, blob, 32, yg, yu, j, gw)
+        assert st == (B.ST_BADEXPERT if bad else 0)
+        ref, tol = _q4_down_ref(blob, W.shape, 32, yg, yu, j, gw)
+        _within(out, ref, tol, "ids")
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_ffn_down_q4_range(T):
+    """|h| far beyond fp16's range and far below it: a power of two brings each row into range."""
+    W, yg, yu, ids, gw = _q4_inputs(64, 128, 4, 2, T, 77)
+    dims = B.ffn_dims(64, 128, 4, 2)
+    blob, _ = _q4_blob(W, 64)
+    for s in (1e8, 1e-12, 0.0):
+        out, st = _q4_run(dims, blob, 64, s * yg, None, ids, gw)
+        ref, tol = _q4_down_ref(blob, W.shape, 64, s * yg, None, ids, gw)
+        assert st == 0
+        _within(out, ref, tol, s)
+
+
+# ---------------------------------------------------------------------------
+# products grouped by expert
+# ---------------------------------------------------------------------------
+def _offsets(sizes):
+    return torch.tensor([0] + list(np.cumsum(sizes)), dtype=torch.int32, device="cuda")
+
+
+def _gmm_ref(a, W, W_up, offsets, rows, div, scatter, out, K):
+    """(out, bound before rounding): float64 on the GPU; rows that no group names keep out's values."""
+    ref = out.double().clone()
+    tol = torch.zeros_like(ref)
+    off = offsets.tolist()
+    n = (K // 16 + 24) * U23
+    for e in range(W.shape[0]):
+        at = torch.arange(off[e], off[e + 1], device="cuda")
+        if not at.numel():
+            continue
+        src = at if rows is None else rows[at].long() // div
+        dst = rows[at].long() if scatter else at
+        x = a[src].double()
+        y, s = x @ W[e].double().T, x.abs() @ W[e].double().abs().T
+        t = n * s
+        if W_up is not None:
+            u, su = x @ W_up[e].double().T, x.abs() @ W_up[e].double().abs().T
+            sig = torch.sigmoid(y)
+            # |SiLU'| <= 1.1; exp and division: the argument's rounding and a few units
+            t = 1.1 * t * u.abs() + (y * sig).abs() * n * su + (y * sig * u).abs() * (8 + y.abs()) * U24
+            t = t + 1.1 * n * s * n * su
+            y = y * sig * u
+        ref[dst], tol[dst] = y, t
+    return ref, tol
+
+
+def _check_gmm(sizes, N, K, dtype, out_dtype, form, seed=0, lda=0, spare=0):
+    g = _gen(seed + N + 7 * K + sum(sizes))
+    E, P = len(sizes), sum(sizes)
+    W = (_randn(g, E, N, K) * K ** -0.5).to(dtype)
+    W_up = (_randn(g, E, N, K) * K ** -0.5).to(dtype) if form.startswith("gated") else None
+    n = P + spare
+    rows, div, scatter = None, 1, False
+    if form in ("gated_gather", "gather"):
+        div = 3
+        rows = torch.randint(0, max(1, n), (n,), generator=g, device="cuda", dtype=torch.int32)
+        n_a = -(-n // div)
+    else:
+        n_a = n
+        if form == "scatter":
+            rows = torch.randperm(n, generator=g, device="cuda").to(torch.int32)
+            scatter = True
+    a = _randn(g, n_a, K + lda).to(dtype)[:, :K]
+    out = torch.full((n, N), 7.0, dtype=out_dtype, device="cuda")
+    ref, tol = _gmm_ref(a, W, W_up, _offsets(sizes), rows, div, scatter, out, K)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.grouped_matmul(a, W, _offsets(sizes), out, W_up=W_up, rows=rows, rows_per_a=div, scatter=scatter, status=st)
+    assert B.read_status(st) == 0
+    _within(out, ref, torch.where(tol > 0, tol + _rounding(ref, out_dtype), tol), (form, N, K))
+
+
+GMM_SIZES = [
+    ([1], 16, 8), ([1, 0, 2], 5, 24), ([0, 7, 1, 0, 9], 130, 64), ([33, 1, 64, 0], 257, 136), ([3] * 40, 96, 256),
+    ([8, 8, 8, 8, 8, 8, 8, 8], 768, 2048), ([300], 64, 72), ([129, 511, 2], 300, 520), ([257, 1, 0, 96, 40], 512, 1024),
+    ([0, 0, 0, 5], 384, 4096), ([1000, 24], 128, 768), ([17] * 130, 264, 320),
+]
+
+
+@pytest.mark.parametrize("form", ["sorted", "gather", "scatter", "gated", "gated_gather"])
+@pytest.mark.parametrize("case", GMM_SIZES, ids=[f"{len(s)}x{sum(s)}x{n}x{k}" for s, n, k in GMM_SIZES])
+def test_grouped_matmul(case, form):
+    sizes, N, K = case
+    for dtype, out_dtype in ((F16, F16), (BF16, BF16), (F16, F32), (BF16, F32)):
+        _check_gmm(sizes, N, K, dtype, out_dtype, form)
+
+
+def test_grouped_matmul_strided_and_spare_rows():
+    """Rows of A further apart than K; places behind the last group and rows without a pair stay as they were."""
+    for form in ("sorted", "gated_gather", "scatter"):
+        _check_gmm([5, 0, 40, 300], 136, 72, F16, F16, form, lda=16, spare=37)
+        _check_gmm([2, 1], 40, 64, BF16, F32, form, lda=8, spare=3)
+        _check_gmm([0, 0], 40, 64, BF16, F32, form, spare=3)
+
+
+@pytest.mark.parametrize("scale", [1, 40])
+def test_grouped_matmul_bad_indexes(scale):
+    """Offsets outside the rows are clamped, row indexes outside A or out are left out; both are reported and
+    every other row is right.  scale 40: the path for many rows."""
+    g = _gen(9)
+    n, N, K = 12 * scale, 48, 64
+    a, W = _randn(g, n, K).half(), _randn(g, 3, N, K).half()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(offsets, rows=None, scatter=False):
+        out = torch.full((n, N), 7.0, device="cuda")
+        st.zero_()
+        B.grouped_matmul(a, W, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out, rows=rows, scatter=scatter,
+                         status=st)
+        return out, B.read_status(st)
+
+    def want(offsets, rows=None, scatter=False):
+        out = torch.full((n, N), 7.0, device="cuda")
+        o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        return _gmm_ref(a, W, None, o, rows, 1, scatter, out, K)
+
+    for off, clamped in (([0, 4 * scale, 4 * scale, 99 * scale], [0, 4 * scale, 4 * scale, n]),
+                         ([-5, 3 * scale, 2 * scale, 2 * scale], [0, 3 * scale, 3 * scale, 3 * scale])):
+        out, bits = run(off)
+        assert bits == B.ST_BADGROUP
+        ref, tol = want(clamped)
+        _within(out, ref, tol + _rounding(ref, F32), off)
+    rows = torch.randperm(n, generator=g, device="cuda").to(torch.int32)
+    bad = rows.clone()
+    bad[3], bad[7 * scale] = -1, n
+    for scatter in (False, True):
+        out, bits = run([0, 4 * scale, 9 * scale, n], bad, scatter)
+        assert bits == B.ST_BADGROUP
+        ref, tol = want([0, 4 * scale, 9 * scale, n], rows, scatter)
+        for i in (3, 7 * scale):
+            at = int(rows[i]) if scatter else i
+            ref[at], tol[at] = 7.0, 0.0
+        _within(out, ref, tol + _rounding(ref, F32) * (tol > 0), scatter)
+
+
+def test_grouped_matmul_non_finite_rows_stay_apart():
+    """NaN and infinities in one row of A, or in another expert's rows and matrix, reach no other row."""
+    g = _gen(11)
+    for sizes in ([3, 4, 2], [150, 90, 200]):
+        P = sum(sizes)
+        a, W = _randn(g, P, 72).half(), _randn(g, 3, 40, 72).half()
+        a[1], a[sizes[0]] = float("nan"), float("inf")
+        W[2] = float("nan")
+        out = torch.zeros(P, 40, device="cuda")
+        B.grouped_matmul(a, W, _offsets(sizes), out)
+        fin = torch.isfinite(out).all(1).cpu()
+        want = torch.ones(P, dtype=torch.bool)
+        want[1] = want[sizes[0]] = False
+        want[sizes[0] + sizes[1]:] = False
+        assert torch.equal(fin, want)

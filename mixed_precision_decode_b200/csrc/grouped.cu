@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "elem.cuh"
+#include "tc_common.cuh"
 
 namespace bitsmoe {
 
@@ -61,6 +62,7 @@ __device__ __forceinline__ float silu_f(float v) { return v / (1.0f + expf(-v));
 // loads 16 contiguous bytes of weight row g (and g + 8), eight k's that the two MMAs
 // of a 32-wide step take as k = 2c, 2c+1, 2c+8, 2c+9; the input rows are loaded with
 // the same order of k, so the sum over k is the same and no operand is rearranged.
+constexpr int kGmmTcRows = 8;  // rows per expert, on average, beyond which the tensor-core path is taken
 constexpr int kMvWarps = 8;
 constexpr int kMvThreads = 32 * kMvWarps;
 constexpr int kMvRows = 16;
@@ -224,6 +226,426 @@ static int launch_gmm_mv(const GmmParams& P, cudaStream_t s) {
     return launch_pdl(k_gmm_mv<BF16, GATED, 4>, grid, block, 0, s, P);
 }
 
+// ---------------------------------------------------------------------------
+// many rows per expert: the tensor cores
+// ---------------------------------------------------------------------------
+// The transposed product, out^T = W a^T: the weights' rows are the MMA's M, the
+// expert's input rows its N, so a ragged group costs its size rounded up to 32 and not
+// to a tile of 128.  Two CTAs (a cluster, one per SM) share each tile: tcgen05.mma
+// cta_group::2 with M = 256 weight rows (128 per CTA; of both matrices when gated) and
+// N = up to 256 (gated: 128) input rows, half of whose rows each CTA stages; an SM then
+// reads 8 KB of shared memory per 128 x 256 x 16 step instead of 12.  Persistent CTA
+// pairs walk the tiles -- expert, then block of 256 weight rows, then piece of the
+// group, so that the pieces that share weights run at the same time and the weights
+// come from HBM once.  Warp roles in each CTA: one issues the TMA loads (weights, and
+// input rows when they are contiguous), one -- in the first CTA of the pair -- the
+// MMAs, four move finished accumulators from tensor memory to out while the next
+// tile's MMAs fill the other half of tensor memory, and with gathered input rows four
+// more fetch those by 16-byte asynchronous copies into the same swizzled layout.
+// The number of tiles is known on the device alone: every CTA derives it from offsets.
+constexpr int kGtM = 128;                        // weight rows per CTA and matrix
+constexpr int kGtK = 64;                         // K per stage: one 128-byte swizzled row
+constexpr int kGtMaxStages = 12;
+constexpr uint32_t kGtAStage = kGtM * kGtK * 2;  // 16 KB
+constexpr int kGtEpiWarps = 4, kGtGatherWarps = 4;
+constexpr int kGtEpiWarp0 = 2, kGtGatherWarp0 = kGtEpiWarp0 + kGtEpiWarps;
+constexpr int kGtLag = 3;                        // stages of gathered rows in flight per thread
+constexpr size_t kGtSmem = 222 * 1024;           // dynamic shared memory a CTA uses at most (5 KB are static)
+
+struct GmmTcParams {
+    GmmParams p;
+    int tok;          // input rows per piece, at most (a multiple of 32)
+    int ntiles;       // blocks of 256 weight rows
+    int nst;          // K stages
+    int stages;       // ring
+    uint32_t stage_bytes;
+};
+
+// A bounded wait that first tries without reading the clock; acquires at cluster scope.
+__device__ __forceinline__ bool gt_wait(uint32_t bar, uint32_t parity) {
+    long long t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        long long t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t0 == 0)
+            t0 = t;
+        else if (t - t0 > kTcWaitNs)
+            return false;
+    }
+}
+__device__ __forceinline__ uint32_t gt_mapa(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void gt_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void gt_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A TMA tile into this CTA's shared memory that completes on a barrier of either CTA of the pair.
+__device__ __forceinline__ void gt_tma2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void gt_commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void gt_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void gt_ld32(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+
+// One tile of the walk.
+struct GtTile {
+    int e, n0;   // expert, first weight row of the pair's block
+    int i0, cnt; // first sorted row and rows of the piece
+    int n_mma;   // cnt rounded up to 32
+};
+__device__ __forceinline__ int gt_pieces(int cnt, int tok) { return (cnt + tok - 1) / tok; }
+
+// Tile `item`; s_tab[e]: tiles of the experts before e.
+__device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab, int item) {
+    int lo = 0, hi = Q.p.E;  // s_tab[lo] <= item < s_tab[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tab[mid] <= item)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    GtTile t;
+    t.e = lo;
+    int i0, i1;
+    group_range(Q.p, lo, i0, i1);
+    const int np = gt_pieces(i1 - i0, Q.tok), within = item - s_tab[lo];
+    // pieces of equal size, whole steps of 32
+    const int size = (int)roundup((uint64_t)((i1 - i0 + np - 1) / np), 32);
+    t.n0 = within / np * (2 * kGtM);
+    t.i0 = i0 + within % np * size;
+    t.cnt = max(0, min(size, i1 - t.i0));
+    t.n_mma = max(32, (int)roundup((uint64_t)t.cnt, 32));
+    return t;
+}
+
+template <bool GATED, bool GATHER>
+__global__ void __launch_bounds__(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarps : 0)), 1)
+    k_gmm_tc(const GmmTcParams Q, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmU,
+             const __grid_constant__ CUtensorMap tmA64, const __grid_constant__ CUtensorMap tmA16) {
+    constexpr int NW = GATED ? 2 : 1;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint64_t s_full[kGtMaxStages], s_empty[kGtMaxStages], s_afull[2], s_aempty[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_fail;
+    __shared__ int s_dst[kGtEpiWarps][256];  // per epilogue warp: output row of each input row of a piece, -1 for none
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const GmmParams& P = Q.p;
+    const uint32_t sbase = (tc_smem(smem_raw) + 1023u) & ~1023u;
+    int* s_tab = reinterpret_cast<int*>(smem_raw + (sbase - tc_smem(smem_raw)) + (size_t)Q.stages * Q.stage_bytes);  // [E+1]
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&s_tmem)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (tid == 32) {
+        for (int i = 0; i < kGtMaxStages; i++) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc_smem(&s_full[i])),
+                         "r"(1u + (GATHER ? 2u * kGtGatherWarps : 0u)));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(tc_smem(&s_empty[i])));
+        }
+        for (int i = 0; i < 2; i++) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(tc_smem(&s_afull[i])));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc_smem(&s_aempty[i])), "r"(2u * kGtEpiWarps));
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_fail = 0;
+    }
+    pdl_wait();
+    pdl_trigger();
+    // tiles of every expert, then their running sum
+    for (int e = tid; e < P.E; e += blockDim.x) {
+        int i0, i1;
+        group_range(P, e, i0, i1);
+        s_tab[e + 1] = gt_pieces(i1 - i0, Q.tok) * Q.ntiles;
+    }
+    if (tid == 0) s_tab[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+        int base = 0;
+        for (int e0 = 0; e0 < P.E; e0 += 32) {
+            int v = e0 + lane < P.E ? s_tab[e0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (e0 + lane < P.E) s_tab[e0 + lane + 1] = base + v;
+            base += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    gt_cluster_sync();  // both CTAs' barriers and tensor memory are ready
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = s_tmem;
+    const int total = s_tab[P.E], first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+    const uint32_t b_off = NW * kGtAStage;
+    volatile int* fail = &s_fail;
+
+    if (warp == 0) {
+        // the weights' tiles, and contiguous input rows; the pair's bytes complete on the first CTA's barrier
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int item = first; item < total && ok; item += step) {
+                const GtTile t = gt_tile(Q, s_tab, item);
+                const int half = t.n_mma / 2, row_w = t.e * P.N + t.n0 + (int)rank * kGtM;
+                const int row_a = t.i0 + (int)rank * half;
+                const uint32_t bytes = 2u * (NW * kGtAStage + (GATHER ? 0u : (uint32_t)half * 128u));
+                for (int k = 0; k < Q.nst; k++, it++) {
+                    const int s = it % Q.stages;
+                    const uint32_t use = (uint32_t)(it / Q.stages);
+                    if (!gt_wait(tc_smem(&s_empty[s]), (use & 1u) ^ 1u) || *fail) {
+                        *fail = 1;
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes, bar = gt_mapa(tc_smem(&s_full[s]), 0);
+                    if (rank == 0)
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&s_full[s])),
+                                     "r"(bytes)
+                                     : "memory");
+                    gt_tma2d(st, &tmW, k * kGtK, row_w, bar);
+                    if (GATED) gt_tma2d(st + kGtAStage, &tmU, k * kGtK, row_w, bar);
+                    if (!GATHER) {
+                        int r = 0;
+                        for (; r + 64 <= half; r += 64) gt_tma2d(st + b_off + 128u * r, &tmA64, k * kGtK, row_a + r, bar);
+                        for (; r < half; r += 16) gt_tma2d(st + b_off + 128u * r, &tmA16, k * kGtK, row_a + r, bar);
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int it = 0, n = 0;
+            bool ok = true;
+            for (int item = first; item < total && ok; item += step, n++) {
+                const GtTile t = gt_tile(Q, s_tab, item);
+                const uint32_t idesc = tc_idesc(2 * kGtM, t.n_mma) | (P.type == BITSMOE_BF16 ? (1u << 7) | (1u << 10) : 0u);
+                const int buf = n & 1;
+                const uint32_t d = tmem + 256u * buf;
+                if (!gt_wait(tc_smem(&s_aempty[buf]), ((uint32_t)(n >> 1) & 1u) ^ 1u) || *fail) {
+                    *fail = 1;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int k = 0; k < Q.nst; k++, it++) {
+                    const int s = it % Q.stages;
+                    if (!gt_wait(tc_smem(&s_full[s]), (uint32_t)(it / Q.stages) & 1u) || *fail) {
+                        *fail = 1;
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes;
+#pragma unroll
+                    for (int kk = 0; kk < kGtK / 16; kk++) {
+                        const uint64_t bd = tc_desc_sw128(st + b_off + 32u * kk);
+#pragma unroll
+                        for (int m = 0; m < NW; m++)
+                            gt_mma(d + 128u * m, tc_desc_sw128(st + m * kGtAStage + 32u * kk), bd, idesc,
+                                   (k > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    gt_commit_both(tc_smem(&s_empty[s]));
+                }
+                if (ok) gt_commit_both(tc_smem(&s_afull[buf]));
+            }
+        }
+    } else if (warp < kGtGatherWarp0) {
+        // accumulators to out: a thread owns a weight row, a column of tensor memory is an input row
+        const int sub = warp & 3;  // the 32 lanes of tensor memory a warp can read
+        int* dst_of = s_dst[warp - kGtEpiWarp0];
+        int n = 0;
+        for (int item = first; item < total; item += step, n++) {
+            const GtTile t = gt_tile(Q, s_tab, item);
+            const int buf = n & 1;
+            for (int j = lane; j < t.cnt; j += 32) {
+                int64_t src, dst;
+                dst_of[j] = row_pair(P, t.i0 + j, src, dst) ? (int)dst : -1;
+            }
+            __syncwarp();
+            const bool ready = gt_wait(tc_smem(&s_afull[buf]), (uint32_t)(n >> 1) & 1u) && !*fail;
+            if (!__all_sync(0xffffffffu, ready)) {
+                *fail = 1;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const int row = t.n0 + (int)rank * kGtM + 32 * sub + lane;
+            const bool live = row < P.N;
+            const uint32_t tl = tmem + 256u * buf + ((uint32_t)(32 * sub) << 16);
+            for (int c0 = 0; c0 < t.cnt; c0 += 32) {
+                uint32_t v[NW][32];
+#pragma unroll
+                for (int m = 0; m < NW; m++) gt_ld32(tl + 128u * m + (uint32_t)c0, v[m]);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 32; j++) {
+                    const int dst = c0 + j < t.cnt ? dst_of[c0 + j] : -1;
+                    float y = __uint_as_float(v[0][j]);
+                    if (GATED) y = silu_f(y) * __uint_as_float(v[NW - 1][j]);
+                    if (dst >= 0 && live) {
+                        const int64_t at = (int64_t)dst * P.N + row;
+                        if (P.out_type == BITSMOE_F32)
+                            static_cast<float*>(P.out)[at] = y;
+                        else
+                            static_cast<uint16_t*>(P.out)[at] = (uint16_t)to_half_bits(y, P.type);
+                    }
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) gt_arrive_cluster(gt_mapa(tc_smem(&s_aempty[buf]), 0));
+        }
+    } else if (GATHER) {
+        // this CTA's half of the piece's input rows: 8 threads a row, 16 bytes each, chunk ch of row r at ch ^ (r mod 8)
+        const int gt = tid - 32 * kGtGatherWarp0, ch = gt & 7, r0 = gt >> 3;
+        constexpr int RPT = 8;  // rows a thread fetches: r0 + 16 i of up to 128
+        int it = 0, done = 0;   // stages issued and handed over
+        bool ok = true;
+        auto hand_over = [&](int upto) {
+            for (; done < upto; done++) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) gt_arrive_cluster(gt_mapa(tc_smem(&s_full[done % Q.stages]), 0));
+            }
+        };
+        for (int item = first; item < total && ok; item += step) {
+            const GtTile t = gt_tile(Q, s_tab, item);
+            const int half = t.n_mma / 2;
+            const uint16_t* src_row[RPT];
+#pragma unroll
+            for (int i = 0; i < RPT; i++) {
+                const int r = r0 + 16 * i, j = (int)rank * half + r;
+                int64_t src = 0, dst;
+                src_row[i] = r < half && j < t.cnt && row_pair(P, t.i0 + j, src, dst) ? P.a + src * P.lda : nullptr;
+            }
+            for (int k = 0; k < Q.nst; k++, it++) {
+                const int s = it % Q.stages;
+                const bool ready = gt_wait(tc_smem(&s_empty[s]), ((uint32_t)(it / Q.stages) & 1u) ^ 1u) && !*fail;
+                if (!__all_sync(0xffffffffu, ready)) {
+                    *fail = 1;
+                    ok = false;
+                    break;
+                }
+                const uint32_t b = sbase + (uint32_t)s * Q.stage_bytes + b_off;
+                const int kc = k * kGtK + 8 * ch;
+#pragma unroll
+                for (int i = 0; i < RPT; i++) {
+                    const int r = r0 + 16 * i;
+                    if (r < half) {
+                        const bool in = src_row[i] != nullptr && kc < P.D;  // else zeros
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         b + 128u * r + ((uint32_t)(ch ^ (r & 7)) << 4)),
+                                     "l"(in ? src_row[i] + kc : P.a), "r"(in ? 16 : 0)
+                                     : "memory");
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.wait_group %0;" ::"n"(kGtLag) : "memory");
+                if (it >= kGtLag) hand_over(it - kGtLag + 1);
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (ok) hand_over(it);
+    }
+    __syncwarp();
+    if (*fail && lane == 0 && P.status) atomicOr(P.status, BITSMOE_ST_TIMEOUT);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    gt_cluster_sync();  // neither CTA leaves while the other may signal its barriers or use its shared memory
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+template <bool GATED, bool GATHER>
+static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
+    GmmTcParams Q{};
+    Q.p = P;
+    const int avg = (P.P + P.E - 1) / P.E, most = GATED ? 128 : 256;
+    Q.tok = avg <= 32 ? 64 : avg <= 64 ? 128 : most;
+    Q.tok = std::min(Q.tok, most);
+    Q.ntiles = (P.N + 2 * kGtM - 1) / (2 * kGtM);
+    Q.nst = (P.D + kGtK - 1) / kGtK;
+    Q.stage_bytes = (GATED ? 2 : 1) * kGtAStage + (uint32_t)Q.tok / 2 * 128u;
+    const size_t tab = roundup(4ull * (P.E + 1), 16);
+    Q.stages = (int)std::min<size_t>(kGtMaxStages, (kGtSmem - 1024 - tab) / Q.stage_bytes);
+    const size_t smem = 1024 + (size_t)Q.stages * Q.stage_bytes + tab;
+    CUtensorMap tmW, tmU, tmA64, tmA16;
+    int rc = tc_tensor_map(&tmW, P.w, P.D, P.E * P.N, kGtM);
+    if (!rc) rc = tc_tensor_map(&tmU, GATED ? P.w_up : P.w, P.D, P.E * P.N, kGtM);
+    if (GATHER) {
+        tmA64 = tmA16 = tmW;  // not used
+    } else {
+        if (!rc) rc = tc_tensor_map_ld(&tmA64, P.a, P.D, P.n_a, P.lda, 64);
+        if (!rc) rc = tc_tensor_map_ld(&tmA16, P.a, P.D, P.n_a, P.lda, 16);
+    }
+    if (rc) return rc;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_gmm_tc<GATED, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGtSmem);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    const int64_t tiles = (int64_t)Q.ntiles * (std::min(P.P, P.E) + P.P / Q.tok);  // at least as many as there are
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(sms / 2, tiles)));
+    cfg.blockDim = dim3(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarps : 0)));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, k_gmm_tc<GATED, GATHER>, Q, tmW, tmU, tmA64, tmA16);
+    return e == cudaSuccess ? BITSMOE_OK : set_cuda_error(e);
+}
+
 }  // namespace bitsmoe
 
 using namespace bitsmoe;
@@ -263,6 +685,10 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_dims* dims, const void*
     P.out_type = d.out_type;
     P.scatter = scatter != 0;
     cudaStream_t s = (cudaStream_t)stream;
+    if (d.n_rows > kGmmTcRows * (int64_t)d.n_experts) {
+        if (rows) return W_up ? launch_gmm_tc<true, true>(P, s) : launch_gmm_tc<false, true>(P, s);
+        return W_up ? launch_gmm_tc<true, false>(P, s) : launch_gmm_tc<false, false>(P, s);
+    }
     if (d.in_type == BITSMOE_BF16) return W_up ? launch_gmm_mv<true, true>(P, s) : launch_gmm_mv<true, false>(P, s);
     return W_up ? launch_gmm_mv<false, true>(P, s) : launch_gmm_mv<false, false>(P, s);
 }

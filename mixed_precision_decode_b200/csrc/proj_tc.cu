@@ -242,11 +242,11 @@ bool proj_tc_supported(int T, int d_in, int r) {
     return T >= 8 && r % kTcM == 0 && d_in % (kTcK * kTcCluster) == 0;
 }
 
-// A 2-D fp16 tensor map over rows x d_in (row-major), boxes of 64 K-elements x
-// box_rows rows in the 128-byte swizzle; rows past the end read as zeros.
-int tc_tensor_map(CUtensorMap* map, const uint16_t* base, int d_in, int rows, int box_rows) {
+// A 2-D map of 16-bit elements over rows x d_in, rows ld elements apart, boxes of 64
+// K-elements x box_rows rows in the 128-byte swizzle; rows past the end read as zeros.
+int tc_tensor_map_ld(CUtensorMap* map, const uint16_t* base, int d_in, int rows, int64_t ld, int box_rows) {
     const cuuint64_t dims[2] = {(cuuint64_t)d_in, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)d_in * 2};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
     const cuuint32_t box[2] = {(cuuint32_t)kTcK, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     // The driver function comes through the runtime's entry-point query, so the
@@ -269,6 +269,10 @@ int tc_tensor_map(CUtensorMap* map, const uint16_t* base, int d_in, int rows, in
                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return rc == CUDA_SUCCESS ? BITSMOE_OK : set_cuda_error(cudaErrorInvalidValue);
+}
+
+int tc_tensor_map(CUtensorMap* map, const uint16_t* base, int d_in, int rows, int box_rows) {
+    return tc_tensor_map_ld(map, base, d_in, rows, d_in, box_rows);
 }
 
 int launch_proj_tc(const uint16_t* phi_t, const uint16_t* X, float* Z, int T, int d_in, int r, int32_t* status,

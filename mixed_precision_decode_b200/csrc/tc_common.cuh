@@ -58,5 +58,7 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity) {
 // A 2-D fp16 tensor map over rows x inner (row-major), boxes of 64 inner elements x
 // box_rows rows in the 128-byte swizzle; rows past the end read as zeros.
 int tc_tensor_map(CUtensorMap* map, const uint16_t* base, int inner, int rows, int box_rows);
+// The same with rows ld elements apart (ld a multiple of 8).
+int tc_tensor_map_ld(CUtensorMap* map, const uint16_t* base, int inner, int rows, int64_t ld, int box_rows);
 
 }  // namespace bitsmoe

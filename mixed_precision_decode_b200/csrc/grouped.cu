@@ -240,17 +240,25 @@ static int launch_gmm_mv(const GmmParams& P, cudaStream_t s) {
 // come from HBM once.  Warp roles in each CTA: one issues the TMA loads (weights, and
 // input rows when they are contiguous), one -- in the first CTA of the pair -- the
 // MMAs, four move finished accumulators from tensor memory to out while the next
-// tile's MMAs fill the other half of tensor memory, and with gathered input rows four
-// more fetch those by 16-byte asynchronous copies into the same swizzled layout.
+// tile's MMAs fill the other half of tensor memory, and with gathered input rows eight
+// more fetch those by 16-byte asynchronous copies into the same swizzled layout and one
+// passes their arrival on.
 // The number of tiles is known on the device alone: every CTA derives it from offsets.
 constexpr int kGtM = 128;                        // weight rows per CTA and matrix
 constexpr int kGtK = 64;                         // K per stage: one 128-byte swizzled row
 constexpr int kGtMaxStages = 12;
 constexpr uint32_t kGtAStage = kGtM * kGtK * 2;  // 16 KB
-constexpr int kGtEpiWarps = 4, kGtGatherWarps = 4;
-constexpr int kGtEpiWarp0 = 2, kGtGatherWarp0 = kGtEpiWarp0 + kGtEpiWarps;
-constexpr int kGtLag = 3;                        // stages of gathered rows in flight per thread
+constexpr int kGtEpiWarps = 4, kGtGatherWarps = 8;
+constexpr int kGtEpiWarp0 = 2, kGtRelayWarp = kGtEpiWarp0 + kGtEpiWarps, kGtGatherWarp0 = kGtRelayWarp + 1;
+constexpr int gt_threads(bool gather) { return 32 * (gather ? kGtGatherWarp0 + kGtGatherWarps : kGtRelayWarp); }
 constexpr size_t kGtSmem = 222 * 1024;           // dynamic shared memory a CTA uses at most (5 KB are static)
+
+constexpr int kGtBoxes = 5;
+__host__ __device__ constexpr int gt_box(int i) { return i < 3 ? 16 << i : 32 * i; }  // 16, 32, 64, 96, 128 rows
+struct GtMaps {
+    CUtensorMap w, u;          // weights: boxes of 128 rows
+    CUtensorMap a[kGtBoxes];   // input rows
+};
 
 struct GmmTcParams {
     GmmParams p;
@@ -261,25 +269,37 @@ struct GmmTcParams {
     uint32_t stage_bytes;
 };
 
-// A bounded wait that first tries without reading the clock; acquires at cluster scope.
+// A bounded wait of a whole warp; every lane gets the same answer.  The clock is read
+// once in 64 tries.
 __device__ __forceinline__ bool gt_wait(uint32_t bar, uint32_t parity) {
     long long t0 = 0;
-    for (;;) {
+    for (int i = 1;; i++) {
         uint32_t ok;
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(ok)
             : "r"(bar), "r"(parity)
             : "memory");
-        if (ok) return true;
-        long long t;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-        if (t0 == 0)
-            t0 = t;
-        else if (t - t0 > kTcWaitNs)
-            return false;
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (i % 64 == 0) {
+            long long t;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+            t = __shfl_sync(0xffffffffu, t, 0);
+            if (t0 == 0)
+                t0 = t;
+            else if (t - t0 > kTcWaitNs)
+                return false;
+        }
     }
+}
+// True in one lane of a converged warp.  The warp-wide roles below run their loops in
+// every lane and issue under this: ptxas then knows that one thread executes the TMA and
+// MMA instructions, whose operands are warp-uniform registers, and need not serialise
+// over the lanes (under `if (lane == 0)` an MMA took about 100 cycles to issue).
+__device__ __forceinline__ bool gt_elect() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ uint32_t gt_mapa(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -287,7 +307,7 @@ __device__ __forceinline__ uint32_t gt_mapa(uint32_t addr, uint32_t rank) {
     return r;
 }
 __device__ __forceinline__ void gt_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void gt_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -356,12 +376,11 @@ __device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab
 }
 
 template <bool GATED, bool GATHER>
-__global__ void __launch_bounds__(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarps : 0)), 1)
-    k_gmm_tc(const GmmTcParams Q, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmU,
-             const __grid_constant__ CUtensorMap tmA64, const __grid_constant__ CUtensorMap tmA16) {
+__global__ void __launch_bounds__(gt_threads(GATHER), 1)
+    k_gmm_tc(const GmmTcParams Q, const __grid_constant__ GtMaps M) {
     constexpr int NW = GATED ? 2 : 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t s_full[kGtMaxStages], s_empty[kGtMaxStages], s_afull[2], s_aempty[2];
+    __shared__ uint64_t s_full[kGtMaxStages], s_empty[kGtMaxStages], s_rows[kGtMaxStages], s_afull[2], s_aempty[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     __shared__ int s_dst[kGtEpiWarps][256];  // per epilogue warp: output row of each input row of a piece, -1 for none
@@ -380,7 +399,8 @@ __global__ void __launch_bounds__(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarp
     if (tid == 32) {
         for (int i = 0; i < kGtMaxStages; i++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc_smem(&s_full[i])),
-                         "r"(1u + (GATHER ? 2u * kGtGatherWarps : 0u)));
+                         "r"(GATHER ? 3u : 1u));  // the TMA bytes; each CTA's gathered rows
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc_smem(&s_rows[i])), "r"(32u * kGtGatherWarps));
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(tc_smem(&s_empty[i])));
         }
         for (int i = 0; i < 2; i++) {
@@ -424,74 +444,80 @@ __global__ void __launch_bounds__(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarp
 
     if (warp == 0) {
         // the weights' tiles, and contiguous input rows; the pair's bytes complete on the first CTA's barrier
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int item = first; item < total && ok; item += step) {
-                const GtTile t = gt_tile(Q, s_tab, item);
-                const int half = t.n_mma / 2, row_w = t.e * P.N + t.n0 + (int)rank * kGtM;
-                const int row_a = t.i0 + (int)rank * half;
-                const uint32_t bytes = 2u * (NW * kGtAStage + (GATHER ? 0u : (uint32_t)half * 128u));
-                for (int k = 0; k < Q.nst; k++, it++) {
-                    const int s = it % Q.stages;
-                    const uint32_t use = (uint32_t)(it / Q.stages);
-                    if (!gt_wait(tc_smem(&s_empty[s]), (use & 1u) ^ 1u) || *fail) {
-                        *fail = 1;
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes, bar = gt_mapa(tc_smem(&s_full[s]), 0);
+        const uint32_t full0 = gt_mapa(tc_smem(&s_full[0]), 0);
+        int s = 0;
+        uint32_t phase = 1;  // parity of the stage's last release: nothing to wait for in the first round
+        bool ok = true;
+        for (int item = first; item < total && ok; item += step) {
+            const GtTile t = gt_tile(Q, s_tab, item);
+            const int half = t.n_mma / 2, row_w = t.e * P.N + t.n0 + (int)rank * kGtM;
+            const int row_a = t.i0 + (int)rank * half;
+            // one box of at least the half's rows: an issued TMA costs more than the rows behind them
+            const int bi = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : half <= 96 ? 3 : 4;
+            const CUtensorMap* tmA = &M.a[bi];
+            const uint32_t bytes = 2u * (NW * kGtAStage + (GATHER ? 0u : 128u * (uint32_t)gt_box(bi)));
+            for (int k = 0; k < Q.nst; k++) {
+                ok = gt_wait(tc_smem(&s_empty[s]), phase);
+                if (!ok) break;
+                if (gt_elect()) {
+                    const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes, bar = full0 + 8u * (uint32_t)s;
                     if (rank == 0)
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&s_full[s])),
                                      "r"(bytes)
                                      : "memory");
-                    gt_tma2d(st, &tmW, k * kGtK, row_w, bar);
-                    if (GATED) gt_tma2d(st + kGtAStage, &tmU, k * kGtK, row_w, bar);
-                    if (!GATHER) {
-                        int r = 0;
-                        for (; r + 64 <= half; r += 64) gt_tma2d(st + b_off + 128u * r, &tmA64, k * kGtK, row_a + r, bar);
-                        for (; r < half; r += 16) gt_tma2d(st + b_off + 128u * r, &tmA16, k * kGtK, row_a + r, bar);
-                    }
+                    gt_tma2d(st, &M.w, k * kGtK, row_w, bar);
+                    if (GATED) gt_tma2d(st + kGtAStage, &M.u, k * kGtK, row_w, bar);
+                    if (!GATHER) gt_tma2d(st + b_off, tmA, k * kGtK, row_a, bar);
+                }
+                __syncwarp();
+                if (++s == Q.stages) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
         }
+        if (!ok) *fail = 1;
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            int it = 0, n = 0;
+        if (rank == 0) {
+            int s = 0, buf = 0;
+            uint32_t phase = 0, aphase = 1;
             bool ok = true;
-            for (int item = first; item < total && ok; item += step, n++) {
+            for (int item = first; item < total && ok; item += step) {
                 const GtTile t = gt_tile(Q, s_tab, item);
                 const uint32_t idesc = tc_idesc(2 * kGtM, t.n_mma) | (P.type == BITSMOE_BF16 ? (1u << 7) | (1u << 10) : 0u);
-                const int buf = n & 1;
                 const uint32_t d = tmem + 256u * buf;
-                if (!gt_wait(tc_smem(&s_aempty[buf]), ((uint32_t)(n >> 1) & 1u) ^ 1u) || *fail) {
-                    *fail = 1;
-                    break;
-                }
+                ok = gt_wait(tc_smem(&s_aempty[buf]), aphase);
+                if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int k = 0; k < Q.nst; k++, it++) {
-                    const int s = it % Q.stages;
-                    if (!gt_wait(tc_smem(&s_full[s]), (uint32_t)(it / Q.stages) & 1u) || *fail) {
-                        *fail = 1;
-                        ok = false;
-                        break;
-                    }
+                for (int k = 0; k < Q.nst; k++) {
+                    ok = gt_wait(tc_smem(&s_full[s]), phase);
+                    if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes;
+                    if (gt_elect()) {
+                        const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes;
+                        // a K step of 16 elements is 32 bytes further in the swizzled row: 2 in the descriptor's address
+                        const uint64_t ad = tc_desc_sw128(st), bd = tc_desc_sw128(st + b_off);
 #pragma unroll
-                    for (int kk = 0; kk < kGtK / 16; kk++) {
-                        const uint64_t bd = tc_desc_sw128(st + b_off + 32u * kk);
+                        for (int kk = 0; kk < kGtK / 16; kk++)
 #pragma unroll
-                        for (int m = 0; m < NW; m++)
-                            gt_mma(d + 128u * m, tc_desc_sw128(st + m * kGtAStage + 32u * kk), bd, idesc,
-                                   (k > 0 || kk > 0) ? 1u : 0u);
+                            for (int m = 0; m < NW; m++)
+                                gt_mma(d + 128u * m, ad + (uint64_t)(m * (kGtAStage >> 4) + 2 * kk), bd + 2u * kk, idesc,
+                                       (k > 0 || kk > 0) ? 1u : 0u);
+                        gt_commit_both(tc_smem(&s_empty[s]));
+                        if (k == Q.nst - 1) gt_commit_both(tc_smem(&s_afull[buf]));
                     }
-                    gt_commit_both(tc_smem(&s_empty[s]));
+                    __syncwarp();
+                    if (++s == Q.stages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (ok) gt_commit_both(tc_smem(&s_afull[buf]));
+                buf ^= 1;
+                if (buf == 0) aphase ^= 1u;
             }
+            if (!ok) *fail = 1;
         }
-    } else if (warp < kGtGatherWarp0) {
+    } else if (warp < kGtRelayWarp) {
         // accumulators to out: a thread owns a weight row, a column of tensor memory is an input row
         const int sub = warp & 3;  // the 32 lanes of tensor memory a warp can read
         int* dst_of = s_dst[warp - kGtEpiWarp0];
@@ -504,8 +530,7 @@ __global__ void __launch_bounds__(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarp
                 dst_of[j] = row_pair(P, t.i0 + j, src, dst) ? (int)dst : -1;
             }
             __syncwarp();
-            const bool ready = gt_wait(tc_smem(&s_afull[buf]), (uint32_t)(n >> 1) & 1u) && !*fail;
-            if (!__all_sync(0xffffffffu, ready)) {
+            if (!gt_wait(tc_smem(&s_afull[buf]), (uint32_t)(n >> 1) & 1u)) {
                 *fail = 1;
                 break;
             }
@@ -518,9 +543,10 @@ __global__ void __launch_bounds__(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarp
 #pragma unroll
                 for (int m = 0; m < NW; m++) gt_ld32(tl + 128u * m + (uint32_t)c0, v[m]);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                const int my_dst = c0 + lane < t.cnt ? dst_of[c0 + lane] : -1;
 #pragma unroll
                 for (int j = 0; j < 32; j++) {
-                    const int dst = c0 + j < t.cnt ? dst_of[c0 + j] : -1;
+                    const int dst = __shfl_sync(0xffffffffu, my_dst, j);
                     float y = __uint_as_float(v[0][j]);
                     if (GATED) y = silu_f(y) * __uint_as_float(v[NW - 1][j]);
                     if (dst >= 0 && live) {
@@ -536,57 +562,67 @@ __global__ void __launch_bounds__(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarp
             __syncwarp();
             if (lane == 0) gt_arrive_cluster(gt_mapa(tc_smem(&s_aempty[buf]), 0));
         }
+    } else if (GATHER && warp == kGtRelayWarp) {
+        // A stage's gathered rows have arrived: the copies wrote shared memory as ordinary
+        // stores do, the MMAs read it as the asynchronous proxy; then tell the first CTA.
+        // (A gathering thread that fenced would wait for its later copies as well.)
+        const uint32_t full0 = gt_mapa(tc_smem(&s_full[0]), 0);
+        int s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int item = first; item < total && ok; item += step)
+            for (int k = 0; k < Q.nst; k++) {
+                ok = gt_wait(tc_smem(&s_rows[s]), phase);
+                if (!ok) break;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (gt_elect()) gt_arrive_cluster(full0 + 8u * (uint32_t)s);
+                __syncwarp();
+                if (++s == Q.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        if (!ok) *fail = 1;
     } else if (GATHER) {
         // this CTA's half of the piece's input rows: 8 threads a row, 16 bytes each, chunk ch of row r at ch ^ (r mod 8)
         const int gt = tid - 32 * kGtGatherWarp0, ch = gt & 7, r0 = gt >> 3;
-        constexpr int RPT = 8;  // rows a thread fetches: r0 + 16 i of up to 128
-        int it = 0, done = 0;   // stages issued and handed over
+        constexpr int RS = 4 * kGtGatherWarps, RPT = kGtM / RS;  // rows a thread fetches: r0 + RS i of up to 128
+        const uint32_t b0 = sbase + b_off + 128u * r0 + ((uint32_t)(ch ^ (r0 & 7)) << 4);  // RS is a multiple of 8
+        int s = 0;
+        uint32_t phase = 1;
         bool ok = true;
-        auto hand_over = [&](int upto) {
-            for (; done < upto; done++) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) gt_arrive_cluster(gt_mapa(tc_smem(&s_full[done % Q.stages]), 0));
-            }
-        };
         for (int item = first; item < total && ok; item += step) {
             const GtTile t = gt_tile(Q, s_tab, item);
             const int half = t.n_mma / 2;
-            const uint16_t* src_row[RPT];
+            const uint16_t* src_row[RPT];  // NULL: zeros
 #pragma unroll
             for (int i = 0; i < RPT; i++) {
-                const int r = r0 + 16 * i, j = (int)rank * half + r;
+                const int r = r0 + RS * i, j = (int)rank * half + r;
                 int64_t src = 0, dst;
-                src_row[i] = r < half && j < t.cnt && row_pair(P, t.i0 + j, src, dst) ? P.a + src * P.lda : nullptr;
+                src_row[i] = r < half && j < t.cnt && row_pair(P, t.i0 + j, src, dst) ? P.a + src * P.lda + 8 * ch : nullptr;
             }
-            for (int k = 0; k < Q.nst; k++, it++) {
-                const int s = it % Q.stages;
-                const bool ready = gt_wait(tc_smem(&s_empty[s]), ((uint32_t)(it / Q.stages) & 1u) ^ 1u) && !*fail;
-                if (!__all_sync(0xffffffffu, ready)) {
-                    *fail = 1;
-                    ok = false;
-                    break;
-                }
-                const uint32_t b = sbase + (uint32_t)s * Q.stage_bytes + b_off;
-                const int kc = k * kGtK + 8 * ch;
+            for (int k = 0; k < Q.nst; k++) {
+                ok = gt_wait(tc_smem(&s_empty[s]), phase);
+                if (!ok) break;
+                const uint32_t b = b0 + (uint32_t)s * Q.stage_bytes;
+                const bool in_k = k * kGtK + 8 * ch < P.D;
 #pragma unroll
-                for (int i = 0; i < RPT; i++) {
-                    const int r = r0 + 16 * i;
-                    if (r < half) {
-                        const bool in = src_row[i] != nullptr && kc < P.D;  // else zeros
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                         b + 128u * r + ((uint32_t)(ch ^ (r & 7)) << 4)),
-                                     "l"(in ? src_row[i] + kc : P.a), "r"(in ? 16 : 0)
+                for (int i = 0; i < RPT; i++)
+                    if (r0 + RS * i < half) {
+                        const bool in = src_row[i] != nullptr && in_k;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(b + 128u * RS * i),
+                                     "l"(in ? src_row[i] + k * kGtK : P.a), "r"(in ? 16 : 0)
                                      : "memory");
                     }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc_smem(&s_rows[s])) : "memory");
+                if (++s == Q.stages) {
+                    s = 0;
+                    phase ^= 1u;
                 }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                asm volatile("cp.async.wait_group %0;" ::"n"(kGtLag) : "memory");
-                if (it >= kGtLag) hand_over(it - kGtLag + 1);
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (ok) hand_over(it);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok) *fail = 1;
     }
     __syncwarp();
     if (*fail && lane == 0 && P.status) atomicOr(P.status, BITSMOE_ST_TIMEOUT);
@@ -611,15 +647,11 @@ static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
     const size_t tab = roundup(4ull * (P.E + 1), 16);
     Q.stages = (int)std::min<size_t>(kGtMaxStages, (kGtSmem - 1024 - tab) / Q.stage_bytes);
     const size_t smem = 1024 + (size_t)Q.stages * Q.stage_bytes + tab;
-    CUtensorMap tmW, tmU, tmA64, tmA16;
-    int rc = tc_tensor_map(&tmW, P.w, P.D, P.E * P.N, kGtM);
-    if (!rc) rc = tc_tensor_map(&tmU, GATED ? P.w_up : P.w, P.D, P.E * P.N, kGtM);
-    if (GATHER) {
-        tmA64 = tmA16 = tmW;  // not used
-    } else {
-        if (!rc) rc = tc_tensor_map_ld(&tmA64, P.a, P.D, P.n_a, P.lda, 64);
-        if (!rc) rc = tc_tensor_map_ld(&tmA16, P.a, P.D, P.n_a, P.lda, 16);
-    }
+    GtMaps M;
+    int rc = tc_tensor_map(&M.w, P.w, P.D, P.E * P.N, kGtM);
+    if (!rc && GATED) rc = tc_tensor_map(&M.u, P.w_up, P.D, P.E * P.N, kGtM);
+    for (int i = 0; i < kGtBoxes && !rc && !GATHER; i++)
+        rc = tc_tensor_map_ld(&M.a[i], P.a, P.D, P.n_a, P.lda, gt_box(i));
     if (rc) return rc;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -630,7 +662,7 @@ static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
     const int64_t tiles = (int64_t)Q.ntiles * (std::min(P.P, P.E) + P.P / Q.tok);  // at least as many as there are
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(sms / 2, tiles)));
-    cfg.blockDim = dim3(32 * (kGtGatherWarp0 + (GATHER ? kGtGatherWarps : 0)));
+    cfg.blockDim = dim3(gt_threads(GATHER));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -642,7 +674,7 @@ static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, k_gmm_tc<GATED, GATHER>, Q, tmW, tmU, tmA64, tmA16);
+    e = cudaLaunchKernelEx(&cfg, k_gmm_tc<GATED, GATHER>, Q, M);
     return e == cudaSuccess ? BITSMOE_OK : set_cuda_error(e);
 }
 

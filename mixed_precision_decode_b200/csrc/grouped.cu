@@ -49,7 +49,9 @@ __device__ __forceinline__ bool row_pair(const GmmParams& P, int i, int64_t& src
     return true;
 }
 
-__device__ __forceinline__ float silu_f(float v) { return v / (1.0f + expf(-v)); }
+// The approximate division (2 units of the last place) has no branch; its denominator is
+// at least 1, and it gives 0 where that leaves the range (v below about -88).
+__device__ __forceinline__ float silu_f(float v) { return __fdividef(v, 1.0f + expf(-v)); }
 
 // ---------------------------------------------------------------------------
 // few rows per expert
@@ -251,7 +253,7 @@ constexpr uint32_t kGtAStage = kGtM * kGtK * 2;  // 16 KB
 constexpr int kGtEpiWarps = 4, kGtGatherWarps = 8;
 constexpr int kGtEpiWarp0 = 2, kGtRelayWarp = kGtEpiWarp0 + kGtEpiWarps, kGtGatherWarp0 = kGtRelayWarp + 1;
 constexpr int gt_threads(bool gather) { return 32 * (gather ? kGtGatherWarp0 + kGtGatherWarps : kGtRelayWarp); }
-constexpr size_t kGtSmem = 222 * 1024;           // dynamic shared memory a CTA uses at most (5 KB are static)
+constexpr size_t kGtSmem = 206 * 1024;           // dynamic shared memory a CTA uses at most (21 KB are static)
 
 constexpr int kGtBoxes = 5;
 __host__ __device__ constexpr int gt_box(int i) { return i < 3 ? 16 << i : 32 * i; }  // 16, 32, 64, 96, 128 rows
@@ -267,6 +269,7 @@ struct GmmTcParams {
     int nst;          // K stages
     int stages;       // ring
     uint32_t stage_bytes;
+    int vec;          // rows of out are whole 16-byte pieces
 };
 
 // A bounded wait of a whole warp; every lane gets the same answer.  The clock is read
@@ -384,6 +387,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     __shared__ int s_dst[kGtEpiWarps][256];  // per epilogue warp: output row of each input row of a piece, -1 for none
+    __shared__ __align__(16) uint4 s_out[kGtEpiWarps][256];  // per epilogue warp: 32 x 32 results
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -521,6 +525,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
         // accumulators to out: a thread owns a weight row, a column of tensor memory is an input row
         const int sub = warp & 3;  // the 32 lanes of tensor memory a warp can read
         int* dst_of = s_dst[warp - kGtEpiWarp0];
+        uint4* stage_out = s_out[warp - kGtEpiWarp0];
         int n = 0;
         for (int item = first; item < total; item += step, n++) {
             const GtTile t = gt_tile(Q, s_tab, item);
@@ -543,18 +548,49 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
 #pragma unroll
                 for (int m = 0; m < NW; m++) gt_ld32(tl + 128u * m + (uint32_t)c0, v[m]);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                const int my_dst = c0 + lane < t.cnt ? dst_of[c0 + lane] : -1;
+                if (GATED) {
 #pragma unroll
-                for (int j = 0; j < 32; j++) {
-                    const int dst = __shfl_sync(0xffffffffu, my_dst, j);
-                    float y = __uint_as_float(v[0][j]);
-                    if (GATED) y = silu_f(y) * __uint_as_float(v[NW - 1][j]);
-                    if (dst >= 0 && live) {
-                        const int64_t at = (int64_t)dst * P.N + row;
-                        if (P.out_type == BITSMOE_F32)
-                            static_cast<float*>(P.out)[at] = y;
-                        else
-                            static_cast<uint16_t*>(P.out)[at] = (uint16_t)to_half_bits(y, P.type);
+                    for (int j = 0; j < 32; j++)
+                        v[0][j] = __float_as_uint(silu_f(__uint_as_float(v[0][j])) * __uint_as_float(v[NW - 1][j]));
+                }
+                if (Q.vec) {
+                    // through shared memory, [input row][32 weight rows]: then 16 bytes per thread and store
+                    const int cols = min(32, t.cnt - c0), cw = P.out_type == BITSMOE_F32 ? 8 : 4;  // 16-byte pieces a row
+                    __syncwarp();
+                    if (P.out_type == BITSMOE_F32) {
+                        float* f = reinterpret_cast<float*>(stage_out);
+#pragma unroll
+                        for (int j = 0; j < 32; j++) f[32 * j + lane] = __uint_as_float(v[0][j]);
+                    } else {
+                        uint16_t* h = reinterpret_cast<uint16_t*>(stage_out);
+                        if (P.type == BITSMOE_F16) {
+#pragma unroll
+                            for (int j = 0; j < 32; j++)
+                                h[32 * j + lane] = (uint16_t)to_half_bits(__uint_as_float(v[0][j]), BITSMOE_F16);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j++)
+                                h[32 * j + lane] = (uint16_t)to_half_bits(__uint_as_float(v[0][j]), BITSMOE_BF16);
+                        }
+                    }
+                    __syncwarp();
+                    const int piece = lane % cw;
+                    const int row0 = t.n0 + (int)rank * kGtM + 32 * sub + piece * (32 / cw);  // whole pieces inside N
+#pragma unroll 4
+                    for (int j = lane / cw; j < cols; j += 32 / cw) {
+                        const int dst = dst_of[c0 + j];
+                        const uint4 w = stage_out[j * cw + piece];
+                        if (dst >= 0 && row0 < P.N)
+                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(P.out) +
+                                                      ((int64_t)dst * P.N + row0) * (16 / (32 / cw))) = w;
+                    }
+                } else {
+                    const int my_dst = c0 + lane < t.cnt ? dst_of[c0 + lane] : -1;
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        const int dst = __shfl_sync(0xffffffffu, my_dst, j);
+                        const float y[1] = {__uint_as_float(v[0][j])};
+                        if (dst >= 0 && live) store_elems<1>(P.out, P.out_type, (int64_t)dst * P.N + row, y);
                     }
                 }
             }
@@ -647,6 +683,7 @@ static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
     const size_t tab = roundup(4ull * (P.E + 1), 16);
     Q.stages = (int)std::min<size_t>(kGtMaxStages, (kGtSmem - 1024 - tab) / Q.stage_bytes);
     const size_t smem = 1024 + (size_t)Q.stages * Q.stage_bytes + tab;
+    Q.vec = (uintptr_t)P.out % 16 == 0 && P.N % (16 / elem_bytes(P.out_type)) == 0;
     GtMaps M;
     int rc = tc_tensor_map(&M.w, P.w, P.D, P.E * P.N, kGtM);
     if (!rc && GATED) rc = tc_tensor_map(&M.u, P.w_up, P.D, P.E * P.N, kGtM);

@@ -73,6 +73,32 @@ __device__ __forceinline__ void store_elems(void* p, int type, int64_t i, const 
     }
 }
 
+// Inclusive scan over a CTA of THREADS threads, one value each; s_warp [32].
+template <int THREADS>
+__device__ __forceinline__ int cta_scan(int v, int* s_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        int w = lane < THREADS / 32 ? s_warp[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += u;
+        }
+        s_warp[lane] = w;
+    }
+    __syncthreads();
+    if (warp > 0) v += s_warp[warp - 1];
+    __syncthreads();
+    return v;
+}
+
 // Programmatic dependent launch: the wait returns when every kernel before this one
 // in the stream has finished and its writes are visible; the trigger lets the next
 // kernel (if it was launched the same way) start its own pre-wait part.

@@ -25,10 +25,6 @@
 
 namespace bitsmoe {
 
-int launch_route_ids(const int32_t* ids, int npairs, int E, const RouteWS& rw, int32_t* status, cudaStream_t s);
-int launch_combine(const int32_t* ids, const float* gw, float* Ye, float* Ysum, int T, int K, int E, int d_out,
-                   cudaStream_t s);
-
 constexpr int kQ4Cols = 64;        // columns of a tile
 constexpr int kQ4Rows = 16;        // rows of a tile
 constexpr int kQ4TileBytes = 512;  // 16 x 64 codes
@@ -222,200 +218,444 @@ struct Q4Params {
     const float* yg;     // [pairs][cols]
     const float* yu;     // or NULL
     const int32_t* ids;  // [pairs]
-    RouteWS rw;          // routing groups
+    const float* gw;     // [pairs]
+    float* out;          // [T][rows]
+    int32_t* status;
+    int32_t* order;      // [pairs] grouped by expert
+    int4* pieces;        // [slots] expert (-1: none), first place in order, pairs
     uint32_t* hb;        // [pairs][cols_p / 64][2][32] B operands (high part, low part)
     float* hscale;       // [pairs]
     float* y;            // [pairs][rows]
-    int E, pairs;
-    int ksplit;          // warps that share a block of 16 rows along the columns
-    int chunk;           // blocks of 16 rows per CTA
+    int E, K, T, pairs, slots;
+    int tok;             // pairs per piece
+    int ksplit;          // warps that share row blocks along the columns
 };
 
-// A warp per pair: h, its scale and its B operands.
-constexpr int kQ4hWarps = 8;
-__global__ void __launch_bounds__(32 * kQ4hWarps) k_q4_h(const Q4Params P) {
-    const int lane = threadIdx.x & 31;
-    const int pair = (int)blockIdx.x * kQ4hWarps + ((int)threadIdx.x >> 5);
-    pdl_wait();
-    pdl_trigger();
-    if (pair >= P.pairs) return;
-    const int e = P.ids[pair];
-    if (e < 0 || e >= P.E) return;  // in no group
-    const int64_t base = (int64_t)pair * P.M.cols;
-    const int nch = P.M.cols / 8;
-    float m = 0.0f;
-    for (int c = lane; c < nch; c += 32) {
-        float h[8];
-        q4_h8(P.yg, P.yu, base + 8 * c, h);
+// 16 weight bytes of a lane, read once.
+__device__ __forceinline__ uint4 q4_ld(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// U consecutive tiles of RB row blocks in one lane's registers: codes, and the scales of
+// rows g and g + 8 (of both groups of a tile when G = 32).
+template <int G, int RB, int U>
+struct Q4Tiles {
+    static constexpr int NS = G < kQ4Cols ? kQ4Cols / G : 1;
+    uint4 w[U][RB];
+    uint16_t s[U][RB][NS][2];
+
+    // Tiles t .. t + U - 1 below t1 of the row blocks at base, base + bb, ...; nrb of them exist.
+    __device__ __forceinline__ void load(const uint8_t* base, int64_t bb, int64_t scale_off, int nrb, int t, int t1,
+                                         int lane) {
+        const int g = lane >> 2;
 #pragma unroll
-        for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(h[j]));
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int r = 0; r < RB; r++) {
+                const bool in = t + u < t1 && r < nrb;
+                const uint8_t* b = base + r * bb;
+                w[u][r] = in ? q4_ld(b + (int64_t)(t + u) * kQ4TileBytes + 16 * lane) : make_uint4(0, 0, 0, 0);
+                const uint16_t* sc = reinterpret_cast<const uint16_t*>(b + scale_off);
+#pragma unroll
+                for (int n = 0; n < NS; n++) {
+                    const int gr = G > kQ4Cols ? (t + u) / (G / kQ4Cols) : (t + u) * NS + n;
+                    s[u][r][n][0] = in ? __ldg(sc + gr * kQ4Rows + g) : (uint16_t)0;
+                    s[u][r][n][1] = in ? __ldg(sc + gr * kQ4Rows + g + 8) : (uint16_t)0;
+                }
+            }
     }
-    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // non-negative: ordered like their bits
-    const float scale = q4_h_scale(m), inv = 1.0f / scale;
-    if (lane == 0) P.hscale[pair] = scale;
-    uint32_t* hb = P.hb + (int64_t)pair * P.M.cols_p;
-    for (int c = lane; c < P.M.cols_p / 8; c += 32) {
-        float h[8] = {};
-        if (c < nch) q4_h8(P.yg, P.yu, base + 8 * c, h);
-        uint32_t* tile = hb + (int64_t)(c / 8) * 64;
+};
+
+// One tile times its B operands, added to the row block's sums; part: the sums of a
+// group that spans two tiles (G = 128) wait there for its scale.
+template <int G, int NB>
+__device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], const uint32_t (&bw)[NB][8], bool group_ends,
+                                        float (&part)[NB][4], float (&acc)[NB][4]) {
+    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            uint32_t hi, lo;
-            q4_split(h[j] * inv, h[j + 1] * inv, hi, lo);
-            const int w = q4_b_word(c % 8 * 8 + j);
-            tile[w] = hi;
-            tile[32 + w] = lo;
+    for (int t = 0; t < 4; t++) {
+        const uint32_t a[4] = {q4_pair(word[t] << 4), q4_pair(word[t]), q4_pair(word[t] >> 4), q4_pair(word[t] >> 8)};
+#pragma unroll
+        for (int j = 0; j < NB; j++) q4_mma(part[j], a, bw[j][2 * t], bw[j][2 * t + 1]);
+        const bool ends = G <= 32 ? (t & 1) : t == 3 && (G <= kQ4Cols || group_ends);
+        if (ends) {
+            const int n = G <= 32 ? t >> 1 : 0;
+            const float s0 = __half2float(__ushort_as_half(s[n][0])), s1 = __half2float(__ushort_as_half(s[n][1]));
+#pragma unroll
+            for (int j = 0; j < NB; j++) {
+                acc[j][0] = fmaf(s0, part[j][0], acc[j][0]);
+                acc[j][1] = fmaf(s0, part[j][1], acc[j][1]);
+                acc[j][2] = fmaf(s1, part[j][2], acc[j][2]);
+                acc[j][3] = fmaf(s1, part[j][3], acc[j][3]);
+                part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.0f;
+            }
         }
     }
 }
 
+// ---------------------------------------------------------------------------
+// one token
+// ---------------------------------------------------------------------------
+// One launch.  A CTA owns blocks of 16 output rows for every slot, so the sum over the
+// slots, in order, stays inside it; its 16 warps are the slots x ranges of columns.
+// Each warp forms the B operands of its own range of its slot's h in shared memory --
+// scaled by the range's own power of two -- while its first weights are on their way.
+// Before the programmatic-launch wait the CTA asks L2 for its rows of the experts that
+// the ids name at that moment (a prefetch alone: nothing read there is used, and the
+// loads after the wait go by the ids as they are then).
+constexpr int kQ4T1Warps = 16;
+constexpr size_t kQ4T1Smem = 200 * 1024;
+
+template <int G>
+__global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
+    constexpr int U = 6;
+    extern __shared__ __align__(16) uint32_t s_h[];  // [K][tiles][2][32], then [row blocks][warp][16] and [K] ids, weights
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int ntiles = P.M.cols_p / kQ4Cols, nblk = P.M.nblk;
+    const int nrb = (nblk - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // row blocks blockIdx + i gridDim
+    float* s_part = reinterpret_cast<float*>(s_h + (size_t)P.K * P.M.cols_p);
+    int* s_e = reinterpret_cast<int*>(s_part + (size_t)nrb * P.K * P.ksplit * kQ4Rows);
+    float* s_g = reinterpret_cast<float*>(s_e + P.K);
+    const int64_t bb = q4_block_bytes(P.M.cols_p, G), scale_off = (int64_t)P.M.cols_p * 8;
+    for (int v = threadIdx.x; v < P.K * nrb; v += 32 * kQ4T1Warps) {
+        const int e = P.ids[v % P.K];
+        if (e >= 0 && e < P.E)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             P.M.blob + ((int64_t)e * nblk + blockIdx.x + (int64_t)(v / P.K) * gridDim.x) * bb),
+                         "r"((uint32_t)bb)
+                         : "memory");
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x < P.K) {
+        const int e = P.ids[threadIdx.x];
+        const bool ok = e >= 0 && e < P.E;
+        s_e[threadIdx.x] = ok ? e : -1;
+        s_g[threadIdx.x] = P.gw[threadIdx.x];
+        if (!ok && blockIdx.x == 0 && P.status) atomicOr(P.status, BITSMOE_ST_BADEXPERT);
+    }
+    __syncthreads();
+    // units: (slot, range of whole groups)
+    constexpr int TG = G > kQ4Cols ? G / kQ4Cols : 1;
+    const int per = ((ntiles / TG + P.ksplit - 1) / P.ksplit) * TG;
+    for (int unit = warp; unit < P.K * P.ksplit; unit += kQ4T1Warps) {
+        const int j = unit / P.ksplit, t0 = min(ntiles, unit % P.ksplit * per), t1 = min(ntiles, t0 + per);
+        const int e = s_e[j];
+        uint32_t* hb = s_h + ((size_t)j * ntiles) * 64;
+        float scale = 1.0f;
+        Q4Tiles<G, 1, U> first;
+        if (e >= 0) {
+            const uint8_t* base = P.M.blob + ((int64_t)e * nblk + blockIdx.x) * bb;
+            first.load(base, bb, scale_off, 1, t0, t1, lane);
+            const int64_t hrow = (int64_t)j * P.M.cols;
+            const int c1 = min(8 * t1, P.M.cols / 8);
+            float m = 0.0f;
+            for (int ch = 8 * t0 + lane; ch < c1; ch += 32) {
+                float h[8];
+                q4_h8(P.yg, P.yu, hrow + 8 * ch, h);
+#pragma unroll
+                for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(h[i]));
+            }
+            scale = q4_h_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
+            const float inv = 1.0f / scale;
+            for (int ch = 8 * t0 + lane; ch < 8 * t1; ch += 32) {
+                float h[8] = {};
+                if (ch < c1) q4_h8(P.yg, P.yu, hrow + 8 * ch, h);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    uint32_t hi, lo;
+                    q4_split(h[i] * inv, h[i + 1] * inv, hi, lo);
+                    const int w = q4_b_word(ch % 8 * 8 + i);
+                    hb[(ch / 8) * 64 + w] = hi;
+                    hb[(ch / 8) * 64 + 32 + w] = lo;
+                }
+            }
+            __syncwarp();
+        }
+        for (int i = 0; i < nrb; i++) {
+            float acc[1][4] = {}, part[1][4] = {};
+            if (e >= 0) {
+                const uint8_t* base = P.M.blob + ((int64_t)e * nblk + blockIdx.x + (int64_t)i * gridDim.x) * bb;
+                for (int tb = t0; tb < t1; tb += U) {
+                    if (i > 0 || tb > t0) first.load(base, bb, scale_off, 1, tb, t1, lane);
+#pragma unroll
+                    for (int u = 0; u < U; u++) {
+                        if (tb + u >= t1) break;
+                        uint32_t bw[1][8] = {};
+                        if (g < 2) {  // column 0: the high part, column 1: the rest; the others are zero
+                            const uint4* src = reinterpret_cast<const uint4*>(hb + (tb + u) * 64 + 32 * g + 8 * c);
+                            const uint4 lo = src[0], hi = src[1];
+                            bw[0][0] = lo.x; bw[0][1] = lo.y; bw[0][2] = lo.z; bw[0][3] = lo.w;
+                            bw[0][4] = hi.x; bw[0][5] = hi.y; bw[0][6] = hi.z; bw[0][7] = hi.w;
+                        }
+                        q4_tile<G, 1>(first.w[u][0], first.s[u][0], bw, (tb + u) % TG == TG - 1, part, acc);
+                    }
+                }
+            }
+            if (c == 0) {
+                float* o = s_part + ((size_t)i * P.K * P.ksplit + unit) * kQ4Rows;
+                o[g] = (acc[0][0] + acc[0][1]) * scale;
+                o[g + 8] = (acc[0][2] + acc[0][3]) * scale;
+            }
+        }
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < nrb * kQ4Rows; v += 32 * kQ4T1Warps) {
+        const int i = v / kQ4Rows, r = v % kQ4Rows;
+        const int row = ((int)blockIdx.x + i * (int)gridDim.x) * kQ4Rows + r;
+        if (row >= P.M.rows) continue;
+        float y = 0.0f;
+        for (int j = 0; j < P.K; j++) {
+            if (s_e[j] < 0) continue;
+            float d = 0.0f;
+            for (int k = 0; k < P.ksplit; k++) d += s_part[((size_t)i * P.K * P.ksplit + j * P.ksplit + k) * kQ4Rows + r];
+            y = fmaf(s_g[j], d, y);
+        }
+        P.out[row] = y;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// several tokens
+// ---------------------------------------------------------------------------
+// First launch: the first CTA groups the pairs by expert and cuts the groups into
+// pieces of `tok` pairs; every other CTA forms h, its scale and its B operands for one
+// pair (independent of the grouping).
+constexpr int kQ4PrepThreads = 512;
+
+__device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
+    __shared__ int s_warp[32];
+    __shared__ int s_carry[2];
+    const int tid = threadIdx.x;
+    for (int e = tid; e < P.E; e += kQ4PrepThreads) s_cnt[e] = 0;
+    if (tid < 2) s_carry[tid] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int p = tid; p < P.pairs; p += kQ4PrepThreads) {
+        const int e = P.ids[p];
+        if (e >= 0 && e < P.E)
+            atomicAdd(&s_cnt[e], 1);
+        else
+            bad = true;
+    }
+    if (bad && P.status) atomicOr(P.status, BITSMOE_ST_BADEXPERT);
+    __syncthreads();
+    for (int e0 = 0; e0 < P.E; e0 += kQ4PrepThreads) {
+        const int e = e0 + tid, n = e < P.E ? s_cnt[e] : 0, np = (n + P.tok - 1) / P.tok;
+        const int end = cta_scan<kQ4PrepThreads>(n, s_warp) + s_carry[0];
+        const int pend = cta_scan<kQ4PrepThreads>(np, s_warp) + s_carry[1];
+        if (e < P.E) s_cnt[e] = end - n;  // becomes the place of the expert's next pair
+        for (int i = 0; i < np; i++)
+            P.pieces[pend - np + i] = make_int4(e, end - n + i * P.tok, min(P.tok, n - i * P.tok), 0);
+        __syncthreads();
+        if (tid == kQ4PrepThreads - 1) {
+            s_carry[0] = end;
+            s_carry[1] = pend;
+        }
+        __syncthreads();
+    }
+    for (int i = s_carry[1] + tid; i < P.slots; i += kQ4PrepThreads) P.pieces[i] = make_int4(-1, 0, 0, 0);
+    // a pair's place inside its group may vary; its result does not depend on it
+    for (int p = tid; p < P.pairs; p += kQ4PrepThreads) {
+        const int e = P.ids[p];
+        if (e >= 0 && e < P.E) P.order[atomicAdd(&s_cnt[e], 1)] = p;
+    }
+}
+
+__global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
+    extern __shared__ int32_t s_cnt[];
+    __shared__ unsigned s_max;
+    const int tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    if (blockIdx.x == 0) {
+        q4_group(P, s_cnt);
+        return;
+    }
+    const int pair = (int)blockIdx.x - 1, e = P.ids[pair];
+    if (e < 0 || e >= P.E) return;  // in no group
+    if (tid == 0) s_max = 0u;
+    __syncthreads();
+    const int64_t base = (int64_t)pair * P.M.cols;
+    const int nch = P.M.cols / 8;
+    constexpr int KEEP = 2;  // chunks of 8 a thread keeps between the two passes
+    float h[KEEP][8];
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KEEP; i++) {
+        const int c = tid + i * kQ4PrepThreads;
+#pragma unroll
+        for (int j = 0; j < 8; j++) h[i][j] = 0.0f;
+        if (c < nch) q4_h8(P.yg, P.yu, base + 8 * c, h[i]);
+#pragma unroll
+        for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(h[i][j]));
+    }
+    for (int c = tid + KEEP * kQ4PrepThreads; c < nch; c += kQ4PrepThreads) {
+        float v[8];
+        q4_h8(P.yg, P.yu, base + 8 * c, v);
+#pragma unroll
+        for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
+    }
+    const unsigned wm = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // non-negative: ordered like their bits
+    if ((tid & 31) == 0) atomicMax(&s_max, wm);
+    __syncthreads();
+    const float scale = q4_h_scale(__uint_as_float(s_max)), inv = 1.0f / scale;
+    if (tid == 0) P.hscale[pair] = scale;
+    uint32_t* hb = P.hb + (int64_t)pair * P.M.cols_p;
+    auto put = [&](int c, const float(&v)[8]) {
+        uint32_t* tile = hb + (int64_t)(c / 8) * 64;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            uint32_t hi, lo;
+            q4_split(v[j] * inv, v[j + 1] * inv, hi, lo);
+            const int w = q4_b_word(c % 8 * 8 + j);
+            tile[w] = hi;
+            tile[32 + w] = lo;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; i++)
+        if (tid + i * kQ4PrepThreads < P.M.cols_p / 8) put(tid + i * kQ4PrepThreads, h[i]);
+    for (int c = tid + KEEP * kQ4PrepThreads; c < P.M.cols_p / 8; c += kQ4PrepThreads) {
+        float v[8] = {};
+        if (c < nch) q4_h8(P.yg, P.yu, base + 8 * c, v);
+        put(c, v);
+    }
+}
+
+// Second launch: CTA = (a piece of up to 4 NTL pairs of one expert, (8 / ksplit) RB
+// blocks of 16 rows); its 8 warps are row groups x ranges of columns.  A warp's next U
+// tiles are loaded while it multiplies the last ones; the B operands come through L1.
 constexpr int kQ4Warps = 8;
 constexpr int kQ4Threads = 32 * kQ4Warps;
 
-// Grouped pairs: CTA = (a piece of 4 NTL pairs of one expert, `chunk` blocks of 16
-// rows).  Its 8 warps are 8 / ksplit row blocks at a time x ksplit ranges of columns.
-template <int G, int NTL>
+template <int G, int NTL, int RB, int U>
 __global__ void __launch_bounds__(kQ4Threads) k_q4_mt(const Q4Params P) {
-    constexpr int U = 4;  // tiles in flight per warp
-    __shared__ float s_part[kQ4Warps][kQ4Rows][4 * NTL + 1];
+    __shared__ float s_part[kQ4Warps][RB * kQ4Rows][4 * NTL + 1];
+    __shared__ int s_pair[4 * NTL];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();
     pdl_trigger();
-    // the piece: experts' groups cut into 4 NTL pairs, in expert order
-    int e = -1, p0 = 0, np = 0;
-    {
-        int base = 0;
-        const int nact = *P.rw.nactive;
-        for (int q0 = 0; q0 < nact && e < 0; q0 += 32) {
-            const int q = q0 + lane;
-            int s0 = 0, s1 = 0, ex = 0;
-            if (q < nact) {
-                ex = P.rw.active[q];
-                s0 = P.rw.start[ex];
-                s1 = P.rw.start[ex + 1];
-            }
-            const int n = (s1 - s0 + 4 * NTL - 1) / (4 * NTL);
-            int inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += u;
-            }
-            const int k = (int)blockIdx.y - (base + inc - n);
-            const unsigned who = __ballot_sync(0xffffffffu, k >= 0 && k < n);
-            if (who) {
-                const int l = __ffs(who) - 1;
-                e = __shfl_sync(0xffffffffu, ex, l);
-                p0 = __shfl_sync(0xffffffffu, s0 + k * 4 * NTL, l);
-                np = min(4 * NTL, __shfl_sync(0xffffffffu, s1, l) - p0);
-            }
-            base += __shfl_sync(0xffffffffu, inc, 31);
-        }
-    }
+    const int4 piece = P.pieces[blockIdx.y];
+    const int e = piece.x, np = piece.z;
     if (e < 0) return;
+    const int ntiles = P.M.cols_p / kQ4Cols;
+    const int wk = warp % P.ksplit, wr = warp / P.ksplit, nwr = kQ4Warps / P.ksplit;
+    constexpr int TG = G > kQ4Cols ? G / kQ4Cols : 1;  // ranges of whole groups
+    const int per = ((ntiles / TG + P.ksplit - 1) / P.ksplit) * TG;
+    const int t0 = min(ntiles, wk * per), t1 = min(ntiles, t0 + per);
+    const int64_t bb = q4_block_bytes(P.M.cols_p, G), scale_off = (int64_t)P.M.cols_p * 8;
+    const int blk0 = (int)blockIdx.x * nwr * RB, blk = blk0 + wr * RB, nrb = min(RB, P.M.nblk - blk);
+    const uint8_t* base = P.M.blob + ((int64_t)e * P.M.nblk + (nrb > 0 ? blk : 0)) * bb;
+    Q4Tiles<G, RB, U> cur, nxt;
+    cur.load(base, bb, scale_off, nrb, t0, t1, lane);
     // this lane's column g of each 8-column B operand: pair g / 2, high part for even g
     const uint32_t* hb[NTL];
 #pragma unroll
     for (int j = 0; j < NTL; j++) {
         const int i = 4 * j + g / 2;
-        hb[j] = i < np ? P.hb + (int64_t)P.rw.pairs[p0 + i] * P.M.cols_p + 32 * (g & 1) + 8 * c : nullptr;
+        hb[j] = i < np ? P.hb + (int64_t)P.order[piece.y + i] * P.M.cols_p + 32 * (g & 1) + 8 * c : nullptr;
     }
-    const int ntiles = P.M.cols_p / kQ4Cols;
-    const int wk = warp % P.ksplit, wr = warp / P.ksplit, nwr = kQ4Warps / P.ksplit;
-    // ranges of whole groups: a multiple of 2 tiles when a group spans 2
-    constexpr int TG = G > kQ4Cols ? G / kQ4Cols : 1;
-    const int per = ((ntiles / TG + P.ksplit - 1) / P.ksplit) * TG;
-    const int t0 = min(ntiles, wk * per), t1 = min(ntiles, t0 + per);
-    const int64_t bb = q4_block_bytes(P.M.cols_p, G);
-    const int rb0 = (int)blockIdx.x * P.chunk, rb1 = min(P.M.nblk, rb0 + P.chunk);
-    for (int rb = rb0; rb < rb1; rb += nwr) {
-        const int blk = rb + wr;
-        float acc[NTL][4];
+    if (threadIdx.x < np) s_pair[threadIdx.x] = P.order[piece.y + threadIdx.x];
+    float acc[RB][NTL][4], part[RB][NTL][4];
+#pragma unroll
+    for (int r = 0; r < RB; r++)
 #pragma unroll
         for (int j = 0; j < NTL; j++)
 #pragma unroll
-            for (int q = 0; q < 4; q++) acc[j][q] = 0.0f;
-        if (blk < rb1) {
-            const uint8_t* base = P.M.blob + ((int64_t)e * P.M.nblk + blk) * bb;
-            const uint16_t* scales = reinterpret_cast<const uint16_t*>(base + (int64_t)P.M.cols_p * 8);
-            float part[NTL][4];
+            for (int q = 0; q < 4; q++) acc[r][j][q] = part[r][j][q] = 0.0f;
+    for (int tb = t0; tb < t1; tb += U) {
+        if (tb + U < t1) nxt.load(base, bb, scale_off, nrb, tb + U, t1, lane);
 #pragma unroll
-            for (int j = 0; j < NTL; j++)
+        for (int u = 0; u < U; u++) {
+            if (tb + u >= t1) break;
+            uint32_t bw[NTL][8];
 #pragma unroll
-                for (int q = 0; q < 4; q++) part[j][q] = 0.0f;
-            for (int tb = t0; tb < t1; tb += U) {
-                uint4 wv[U];
-#pragma unroll
-                for (int u = 0; u < U; u++)
-                    wv[u] = tb + u < t1 ? *reinterpret_cast<const uint4*>(base + (int64_t)(tb + u) * kQ4TileBytes + 16 * lane)
-                                        : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const int tile = tb + u;
-                    if (tile >= t1) break;
-                    uint32_t bw[NTL][8];
-#pragma unroll
-                    for (int j = 0; j < NTL; j++) {
-                        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                        if (hb[j]) {
-                            const uint4* src = reinterpret_cast<const uint4*>(hb[j] + (int64_t)tile * 64);
-                            lo = src[0];
-                            hi = src[1];
-                        }
-                        bw[j][0] = lo.x; bw[j][1] = lo.y; bw[j][2] = lo.z; bw[j][3] = lo.w;
-                        bw[j][4] = hi.x; bw[j][5] = hi.y; bw[j][6] = hi.z; bw[j][7] = hi.w;
-                    }
-                    const uint32_t word[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
-#pragma unroll
-                    for (int t = 0; t < 4; t++) {
-                        const uint32_t a[4] = {q4_pair(word[t] << 4), q4_pair(word[t]), q4_pair(word[t] >> 4),
-                                               q4_pair(word[t] >> 8)};
-#pragma unroll
-                        for (int j = 0; j < NTL; j++) q4_mma(part[j], a, bw[j][2 * t], bw[j][2 * t + 1]);
-                        const int col = tile * kQ4Cols + 16 * (t + 1);
-                        if (col % G == 0) {  // the group ends here
-                            const int gr = col / G - 1;
-                            const float s0 = __half2float(__ushort_as_half(scales[gr * kQ4Rows + g]));
-                            const float s1 = __half2float(__ushort_as_half(scales[gr * kQ4Rows + g + 8]));
-#pragma unroll
-                            for (int j = 0; j < NTL; j++) {
-                                acc[j][0] = fmaf(s0, part[j][0], acc[j][0]);
-                                acc[j][1] = fmaf(s0, part[j][1], acc[j][1]);
-                                acc[j][2] = fmaf(s1, part[j][2], acc[j][2]);
-                                acc[j][3] = fmaf(s1, part[j][3], acc[j][3]);
-                                part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.0f;
-                            }
-                        }
-                    }
+            for (int j = 0; j < NTL; j++) {
+                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                if (hb[j]) {
+                    const uint4* src = reinterpret_cast<const uint4*>(hb[j] + (int64_t)(tb + u) * 64);
+                    lo = src[0];
+                    hi = src[1];
                 }
+                bw[j][0] = lo.x; bw[j][1] = lo.y; bw[j][2] = lo.z; bw[j][3] = lo.w;
+                bw[j][4] = hi.x; bw[j][5] = hi.y; bw[j][6] = hi.z; bw[j][7] = hi.w;
             }
+#pragma unroll
+            for (int r = 0; r < RB; r++)
+                q4_tile<G, NTL>(cur.w[u][r], cur.s[u][r], bw, (tb + u) % TG == TG - 1, part[r], acc[r]);
         }
-        // columns 2c and 2c + 1 of a fragment are the high and the low part of pair c
+        cur = nxt;
+    }
+    // columns 2c and 2c + 1 of a fragment are the high and the low part of pair c
+#pragma unroll
+    for (int r = 0; r < RB; r++)
 #pragma unroll
         for (int j = 0; j < NTL; j++) {
-            s_part[warp][g][4 * j + c] = acc[j][0] + acc[j][1];
-            s_part[warp][g + 8][4 * j + c] = acc[j][2] + acc[j][3];
+            s_part[warp][r * kQ4Rows + g][4 * j + c] = acc[r][j][0] + acc[r][j][1];
+            s_part[warp][r * kQ4Rows + g + 8][4 * j + c] = acc[r][j][2] + acc[r][j][3];
         }
-        __syncthreads();
-        for (int v = threadIdx.x; v < nwr * kQ4Rows * np; v += kQ4Threads) {
-            const int r = v % kQ4Rows, i = v / kQ4Rows % np, w = v / (kQ4Rows * np);
-            const int row = (rb + w) * kQ4Rows + r;
-            if (rb + w < rb1 && row < P.M.rows) {
-                float sum = 0.0f;
-                for (int k = 0; k < P.ksplit; k++) sum += s_part[w * P.ksplit + k][r][i];
-                const int pair = P.rw.pairs[p0 + i];
-                P.y[(int64_t)pair * P.M.rows + row] = sum * P.hscale[pair];
-            }
+    __syncthreads();
+    const int rows_cta = nwr * RB * kQ4Rows;
+    for (int v = threadIdx.x; v < rows_cta * np; v += kQ4Threads) {
+        const int r = v % rows_cta, i = v / rows_cta;
+        const int row = blk0 * kQ4Rows + r;
+        if (row >= P.M.rows) continue;
+        float sum = 0.0f;
+        for (int k = 0; k < P.ksplit; k++) sum += s_part[r / (RB * kQ4Rows) * P.ksplit + k][r % (RB * kQ4Rows)][i];
+        const int pair = s_pair[i];
+        P.y[(int64_t)pair * P.M.rows + row] = sum * P.hscale[pair];
+    }
+}
+
+// Third launch: each token's sum over its slots, in order.
+__global__ void __launch_bounds__(256) k_q4_sum(const Q4Params P) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t n = (int64_t)P.T * P.M.rows;
+    for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < n; x += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = x / P.M.rows;
+        const int row = (int)(x % P.M.rows);
+        float acc = 0.0f;
+        for (int j = 0; j < P.K; j++) {
+            const int64_t pair = t * P.K + j;
+            const int e = P.ids[pair];
+            if (e >= 0 && e < P.E) acc = fmaf(P.gw[pair], P.y[pair * P.M.rows + row], acc);
         }
-        __syncthreads();
+        P.out[x] = acc;
     }
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+constexpr int kQ4MaxE = 8192;  // the grouping counts them in shared memory (32 KB)
+
+// Pairs per piece: 4, 8 or 16, by the expected group size.
+static int q4_tok(int pairs, int E) {
+    const int avg = pairs / E;
+    return avg <= 3 ? 4 : avg <= 6 ? 8 : 16;
+}
+static int q4_slots(int pairs, int E) { return std::min(pairs, E) + pairs / q4_tok(pairs, E); }
+
+// The single-token kernel: h and the partial sums of a CTA's row blocks fit its shared memory.
+static size_t q4_t1_smem(const bitsmoe_ffn_dims* d, int group, int sms) {
+    const int nblk = (d->d_model + kQ4Rows - 1) / kQ4Rows, grid = std::min(nblk, sms), nrb = (nblk + grid - 1) / grid;
+    const size_t units = (size_t)d->top_k * std::max(1, kQ4T1Warps / d->top_k);
+    return 4ull * d->top_k * q4_cols_padded(d->d_ff, group) + 4ull * nrb * units * kQ4Rows + 8ull * d->top_k;
+}
+constexpr int kQ4Sms = 148;  // CTAs of the single-token kernel: one per SM
+static bool q4_single(const bitsmoe_ffn_dims* d, int group, int T) {
+    return T == 1 && d->top_k <= 64 && q4_t1_smem(d, group, kQ4Sms) <= kQ4T1Smem;
+}
+
 struct Q4WS {
-    RouteWS route;
+    int32_t* order;
+    int4* pieces;
     uint32_t* hb;
     float* hscale;
     float* y;
@@ -430,12 +670,9 @@ static Q4WS q4_ws(const bitsmoe_ffn_dims* d, int group, int T, uint8_t* base) {
         used = off + bytes;
         return base ? base + off : nullptr;
     };
-    const uint64_t E = d->n_experts, pairs = (uint64_t)T * d->top_k, dp = q4_cols_padded(d->d_ff, group);
-    w.route.count = (int32_t*)take(4 * E);
-    w.route.start = (int32_t*)take(4 * (E + 1));
-    w.route.active = (int32_t*)take(4 * E);
-    w.route.nactive = (int32_t*)take(4);
-    w.route.pairs = (int32_t*)take(4 * pairs + 4);
+    const uint64_t pairs = (uint64_t)T * d->top_k, dp = q4_cols_padded(d->d_ff, group);
+    w.order = (int32_t*)take(4 * pairs);
+    w.pieces = (int4*)take(16ull * q4_slots((int)pairs, d->n_experts));
     w.hb = (uint32_t*)take(4 * pairs * dp);
     w.hscale = (float*)take(4 * pairs);
     w.y = (float*)take(4 * pairs * d->d_model);
@@ -444,16 +681,32 @@ static Q4WS q4_ws(const bitsmoe_ffn_dims* d, int group, int T, uint8_t* base) {
 }
 
 static bool q4_dims_ok(const bitsmoe_ffn_dims* d, int group, int T) {
-    return d && d->d_model >= 1 && d->d_ff >= 8 && d->d_ff % 8 == 0 && d->n_experts >= 1 && d->top_k >= 1 &&
-           q4_group_ok(group) && T >= 0 && (int64_t)T * d->top_k <= 0x7fffffff && d->d_ff <= (1 << 30) &&
-           d->d_model <= (1 << 30);
+    return d && d->d_model >= 1 && d->d_ff >= 8 && d->d_ff % 8 == 0 && d->n_experts >= 1 && d->n_experts <= kQ4MaxE &&
+           d->top_k >= 1 && q4_group_ok(group) && T >= 0 && (int64_t)T * d->top_k <= 0x3fffffff &&
+           d->d_ff <= (1 << 30) && d->d_model <= (1 << 30);
 }
 
 template <int G>
-static int launch_q4_mt(const Q4Params& P, int ntl, const dim3& grid, cudaStream_t s) {
-    if (ntl == 1) return launch_pdl(k_q4_mt<G, 1>, grid, dim3(kQ4Threads), 0, s, P);
-    if (ntl == 2) return launch_pdl(k_q4_mt<G, 2>, grid, dim3(kQ4Threads), 0, s, P);
-    return launch_pdl(k_q4_mt<G, 4>, grid, dim3(kQ4Threads), 0, s, P);
+static int launch_q4_mt(Q4Params& P, cudaStream_t s) {
+    // warps along the columns: enough of them to fill the SMs when few row blocks are touched
+    const int rb = P.tok == 16 ? 1 : 2;
+    const int64_t tasks = (int64_t)std::min(P.pairs, P.E) * ((P.M.nblk + rb - 1) / rb);
+    const int64_t want = 148 * 24;
+    P.ksplit = tasks >= want ? 1 : 2 * tasks >= want ? 2 : 4 * tasks >= want ? 4 : 8;
+    const int per_cta = kQ4Warps / P.ksplit * rb;
+    if (P.slots > 65535) return BITSMOE_EINVAL;
+    const dim3 grid((unsigned)((P.M.nblk + per_cta - 1) / per_cta), (unsigned)P.slots), block(kQ4Threads);
+    if (P.tok == 4) return launch_pdl(k_q4_mt<G, 1, 2, 2>, grid, block, 0, s, P);
+    if (P.tok == 8) return launch_pdl(k_q4_mt<G, 2, 2, 2>, grid, block, 0, s, P);
+    return launch_pdl(k_q4_mt<G, 4, 1, 4>, grid, block, 0, s, P);
+}
+
+template <int G>
+static int launch_q4_t1(Q4Params& P, size_t smem, cudaStream_t s) {
+    P.ksplit = std::max(1, kQ4T1Warps / P.K);
+    const cudaError_t e = cudaFuncSetAttribute(k_q4_t1<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQ4T1Smem);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    return launch_pdl(k_q4_t1<G>, dim3((unsigned)std::min(P.M.nblk, kQ4Sms)), dim3(32 * kQ4T1Warps), smem, s, P);
 }
 
 }  // namespace bitsmoe
@@ -517,13 +770,13 @@ BITSMOE_API int bitsmoe_q4_unpack(const void* blob, int32_t n_experts, int32_t r
 }
 
 BITSMOE_API uint64_t bitsmoe_ffn_down_q4_workspace_bytes(const bitsmoe_ffn_dims* dims, int32_t group, int32_t T) {
-    if (!q4_dims_ok(dims, group, T) || T == 0) return 0;
+    if (!q4_dims_ok(dims, group, T) || T == 0 || q4_single(dims, group, T)) return 0;
     return q4_ws(dims, group, T, nullptr).used;
 }
 
 BITSMOE_API int bitsmoe_ffn_down_q4_launches(const bitsmoe_ffn_dims* dims, int32_t group, int32_t T) {
     if (!q4_dims_ok(dims, group, T)) return BITSMOE_EINVAL;
-    return T == 0 ? 0 : 4;
+    return T == 0 ? 0 : q4_single(dims, group, T) ? 1 : 3;
 }
 
 BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_ffn_dims* dims, const void* blob, int32_t group, const float* Y_gate,
@@ -540,34 +793,34 @@ BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_ffn_dims* dims, const void* bl
     if (need > 0 && (!workspace || (uintptr_t)workspace % 256)) return BITSMOE_EINVAL;
     if (workspace_bytes < need) return BITSMOE_ESIZE;
     cudaStream_t s = (cudaStream_t)stream;
-    const int E = dims->n_experts, K = dims->top_k, pairs = T * K;
-    const Q4WS w = q4_ws(dims, group, T, (uint8_t*)workspace);
     Q4Params P{};
     P.M = q4_matrix(blob, dims->d_model, dims->d_ff, group);
     P.yg = Y_gate;
     P.yu = Y_up;
     P.ids = topk_ids;
-    P.rw = w.route;
+    P.gw = gate_w;
+    P.out = out;
+    P.status = status;
+    P.E = dims->n_experts;
+    P.K = dims->top_k;
+    P.T = T;
+    P.pairs = T * dims->top_k;
+    if (q4_single(dims, group, T)) {
+        const size_t smem = q4_t1_smem(dims, group, kQ4Sms);
+        return group == 32 ? launch_q4_t1<32>(P, smem, s) : group == 64 ? launch_q4_t1<64>(P, smem, s) : launch_q4_t1<128>(P, smem, s);
+    }
+    const Q4WS w = q4_ws(dims, group, T, (uint8_t*)workspace);
+    P.order = w.order;
+    P.pieces = w.pieces;
     P.hb = w.hb;
     P.hscale = w.hscale;
     P.y = w.y;
-    P.E = E;
-    P.pairs = pairs;
-    int rc = launch_route_ids(topk_ids, pairs, E, w.route, status, s);
+    P.tok = q4_tok(P.pairs, P.E);
+    P.slots = q4_slots(P.pairs, P.E);
+    int rc = launch_pdl(k_q4_prep, dim3((unsigned)P.pairs + 1), dim3(kQ4PrepThreads), 4ull * P.E, s, P);
     if (rc) return rc;
-    rc = launch_pdl(k_q4_h, dim3((unsigned)((pairs + kQ4hWarps - 1) / kQ4hWarps)), dim3(32 * kQ4hWarps), 0, s, P);
+    rc = group == 32 ? launch_q4_mt<32>(P, s) : group == 64 ? launch_q4_mt<64>(P, s) : launch_q4_mt<128>(P, s);
     if (rc) return rc;
-    const int avg = pairs / E;
-    const int ntl = avg <= 3 ? 1 : avg <= 6 ? 2 : 4;
-    const int64_t slots = std::min(pairs, E) + pairs / (4 * ntl);
-    // warps along the columns: enough of them to fill the SMs when few row blocks are touched
-    const int64_t tasks = (int64_t)std::min<int64_t>(slots, std::min(pairs, E)) * P.M.nblk;
-    P.ksplit = tasks >= 148 * 32 ? 1 : tasks >= 148 * 16 ? 2 : tasks >= 148 * 8 ? 4 : 8;
-    P.chunk = kQ4Warps;
-    if (slots > 65535) return BITSMOE_EINVAL;
-    const dim3 grid((unsigned)((P.M.nblk + P.chunk - 1) / P.chunk), (unsigned)slots);
-    rc = group == 32 ? launch_q4_mt<32>(P, ntl, grid, s) : group == 64 ? launch_q4_mt<64>(P, ntl, grid, s)
-                                                                        : launch_q4_mt<128>(P, ntl, grid, s);
-    if (rc) return rc;
-    return launch_combine(topk_ids, gate_w, w.y, out, T, K, E, dims->d_model, s);
+    const int64_t n = (int64_t)T * dims->d_model;
+    return launch_pdl(k_q4_sum, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 148 * 16)), dim3(256), 0, s, P);
 }

@@ -215,31 +215,6 @@ __device__ void walk_pairs(const RouteParams& P, int p0, int p1, int32_t* cnt, i
     }
 }
 
-// Inclusive scan over the CTA of one value per thread.
-__device__ int cta_scan(int v, int* s_warp) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        int w = s_warp[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += u;
-        }
-        s_warp[lane] = w;
-    }
-    __syncthreads();
-    if (warp > 0) v += s_warp[warp - 1];
-    __syncthreads();
-    return v;
-}
-
 // Groups the pairs of the CTA's tokens [t0, t1).  nb > 1: the counts of the other
 // CTAs' tokens are in P.hist.  s_cnt [nw][E].
 __device__ void group_pairs(const RouteParams& P, int t0, int t1, int b, int nb, int32_t* s_cnt, int* s_warp) {
@@ -269,7 +244,7 @@ __device__ void group_pairs(const RouteParams& P, int t0, int t1, int b, int nb,
                 }
             }
         }
-        const int end = carry + cta_scan(total, s_warp);
+        const int end = carry + cta_scan<kRtThreads>(total, s_warp);
         if (e < P.E) {
             int run = end - total + before;
             for (int w = 0; w < P.nw; w++) {

@@ -184,6 +184,13 @@ __device__ __forceinline__ void q4_mma(float (&c)[4], const uint32_t (&a)[4], ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void q4_mma_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // SiLU(yg) * yu of 8 values (yu NULL: yg itself).
 __device__ __forceinline__ void q4_h8(const float* yg, const float* yu, int64_t i, float (&h)[8]) {
     load_elems<8>(yg, BITSMOE_F32, i, h);
@@ -241,48 +248,59 @@ __device__ __forceinline__ uint4 q4_ld(const uint8_t* p) {
 }
 
 // U consecutive tiles of RB row blocks in one lane's registers: codes, and the scales of
-// rows g and g + 8 (of both groups of a tile when G = 32).
+// rows g and g + 8 (of both groups of a tile when G = 32).  codes[r]: this lane's 16
+// bytes of the first tile of row block r; scales[r]: its rows' scales of that tile's group.
 template <int G, int RB, int U>
 struct Q4Tiles {
     static constexpr int NS = G < kQ4Cols ? kQ4Cols / G : 1;
     uint4 w[U][RB];
     uint16_t s[U][RB][NS][2];
 
-    // Tiles t .. t + U - 1 below t1 of the row blocks at base, base + bb, ...; nrb of them exist.
-    __device__ __forceinline__ void load(const uint8_t* base, int64_t bb, int64_t scale_off, int nrb, int t, int t1,
-                                         int lane) {
-        const int g = lane >> 2;
+    __device__ __forceinline__ void load(const uint8_t* const (&codes)[RB], const uint16_t* const (&scales)[RB]) {
 #pragma unroll
         for (int u = 0; u < U; u++)
 #pragma unroll
             for (int r = 0; r < RB; r++) {
-                const bool in = t + u < t1 && r < nrb;
-                const uint8_t* b = base + r * bb;
-                w[u][r] = in ? q4_ld(b + (int64_t)(t + u) * kQ4TileBytes + 16 * lane) : make_uint4(0, 0, 0, 0);
-                const uint16_t* sc = reinterpret_cast<const uint16_t*>(b + scale_off);
+                w[u][r] = q4_ld(codes[r] + u * kQ4TileBytes);
 #pragma unroll
                 for (int n = 0; n < NS; n++) {
-                    const int gr = G > kQ4Cols ? (t + u) / (G / kQ4Cols) : (t + u) * NS + n;
-                    s[u][r][n][0] = in ? __ldg(sc + gr * kQ4Rows + g) : (uint16_t)0;
-                    s[u][r][n][1] = in ? __ldg(sc + gr * kQ4Rows + g + 8) : (uint16_t)0;
+                    const uint16_t* sc = scales[r] + (G > kQ4Cols ? u / (G / kQ4Cols) : u * NS + n) * kQ4Rows;
+                    s[u][r][n][0] = __ldg(sc);
+                    s[u][r][n][1] = __ldg(sc + 8);
                 }
             }
     }
 };
+// Moves tile pointers on by n tiles (a multiple of 2 when a group is two tiles).
+template <int G, int RB>
+__device__ __forceinline__ void q4_advance(const uint8_t* (&codes)[RB], const uint16_t* (&scales)[RB], int n) {
+#pragma unroll
+    for (int r = 0; r < RB; r++) {
+        codes[r] += n * kQ4TileBytes;
+        scales[r] += n * kQ4Cols / G * kQ4Rows;
+    }
+}
 
-// One tile times its B operands, added to the row block's sums; part: the sums of a
-// group that spans two tiles (G = 128) wait there for its scale.
-template <int G, int NB>
-__device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], const uint32_t (&bw)[NB][8], bool group_ends,
-                                        float (&part)[NB][4], float (&acc)[NB][4]) {
+// One tile times its B operands (NB of the NL columns groups that acc has), added to the
+// row block's sums.  With G = 128 a group is two tiles: `part` carries its sum from the
+// first (half = 0) to the second, where its scale is applied.
+template <int G, int NB, int NL>
+__device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], const uint32_t (&bw)[NL][8], int half,
+                                        float (&part)[NL][4], float (&acc)[NL][4]) {
     const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int t = 0; t < 4; t++) {
         const uint32_t a[4] = {q4_pair(word[t] << 4), q4_pair(word[t]), q4_pair(word[t] >> 4), q4_pair(word[t] >> 8)};
+        const bool begins = G <= 32 ? (t & 1) == 0 : t == 0;
 #pragma unroll
-        for (int j = 0; j < NB; j++) q4_mma(part[j], a, bw[j][2 * t], bw[j][2 * t + 1]);
-        const bool ends = G <= 32 ? (t & 1) : t == 3 && (G <= kQ4Cols || group_ends);
-        if (ends) {
+        for (int j = 0; j < NB; j++) {
+            if (begins && (G <= kQ4Cols || half == 0))
+                q4_mma_zero(part[j], a, bw[j][2 * t], bw[j][2 * t + 1]);
+            else
+                q4_mma(part[j], a, bw[j][2 * t], bw[j][2 * t + 1]);
+        }
+        const bool ends = G <= 32 ? (t & 1) : t == 3;
+        if (ends && (G <= kQ4Cols || half == 1)) {
             const int n = G <= 32 ? t >> 1 : 0;
             const float s0 = __half2float(__ushort_as_half(s[n][0])), s1 = __half2float(__ushort_as_half(s[n][1]));
 #pragma unroll
@@ -291,7 +309,6 @@ __device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], c
                 acc[j][1] = fmaf(s0, part[j][1], acc[j][1]);
                 acc[j][2] = fmaf(s1, part[j][2], acc[j][2]);
                 acc[j][3] = fmaf(s1, part[j][3], acc[j][3]);
-                part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.0f;
             }
         }
     }
@@ -310,9 +327,26 @@ __device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], c
 constexpr int kQ4T1Warps = 16;
 constexpr size_t kQ4T1Smem = 200 * 1024;
 
+// U tiles of one row block times h.
+template <int G, int U>
+__device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, 1, U>& tiles, const uint32_t* hb, int g, int c,
+                                            float (&part)[1][4], float (&acc)[1][4]) {
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        uint32_t bw[1][8] = {};
+        if (g < 2) {  // column 0: the high part, column 1: the rest; the others are zero
+            const uint4* src = reinterpret_cast<const uint4*>(hb + u * 64 + 32 * g + 8 * c);
+            const uint4 lo = src[0], hi = src[1];
+            bw[0][0] = lo.x; bw[0][1] = lo.y; bw[0][2] = lo.z; bw[0][3] = lo.w;
+            bw[0][4] = hi.x; bw[0][5] = hi.y; bw[0][6] = hi.z; bw[0][7] = hi.w;
+        }
+        q4_tile<G, 1, 1>(tiles.w[u][0], tiles.s[u][0], bw, u & 1, part, acc);
+    }
+}
+
 template <int G>
 __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
-    constexpr int U = 6;
+    constexpr int U = 6, V = G > kQ4Cols ? 2 : 1;  // tiles per batch, and per step of what is left
     extern __shared__ __align__(16) uint32_t s_h[];  // [K][tiles][2][32], then [row blocks][warp][16] and [K] ids, weights
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int ntiles = P.M.cols_p / kQ4Cols, nblk = P.M.nblk;
@@ -347,10 +381,14 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
         const int e = s_e[j];
         uint32_t* hb = s_h + ((size_t)j * ntiles) * 64;
         float scale = 1.0f;
-        Q4Tiles<G, 1, U> first;
-        if (e >= 0) {
+        Q4Tiles<G, 1, U> tiles;
+        const bool batches = t1 - t0 >= U;
+        if (e >= 0 && t0 < t1) {
             const uint8_t* base = P.M.blob + ((int64_t)e * nblk + blockIdx.x) * bb;
-            first.load(base, bb, scale_off, 1, t0, t1, lane);
+            const uint8_t* codes[1] = {base + 16 * lane};
+            const uint16_t* scales[1] = {reinterpret_cast<const uint16_t*>(base + scale_off) + g};
+            q4_advance<G>(codes, scales, t0);
+            if (batches) tiles.load(codes, scales);
             const int64_t hrow = (int64_t)j * P.M.cols;
             const int c1 = min(8 * t1, P.M.cols / 8);
             float m = 0.0f;
@@ -378,22 +416,22 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
         }
         for (int i = 0; i < nrb; i++) {
             float acc[1][4] = {}, part[1][4] = {};
-            if (e >= 0) {
+            if (e >= 0 && t0 < t1) {
                 const uint8_t* base = P.M.blob + ((int64_t)e * nblk + blockIdx.x + (int64_t)i * gridDim.x) * bb;
-                for (int tb = t0; tb < t1; tb += U) {
-                    if (i > 0 || tb > t0) first.load(base, bb, scale_off, 1, tb, t1, lane);
-#pragma unroll
-                    for (int u = 0; u < U; u++) {
-                        if (tb + u >= t1) break;
-                        uint32_t bw[1][8] = {};
-                        if (g < 2) {  // column 0: the high part, column 1: the rest; the others are zero
-                            const uint4* src = reinterpret_cast<const uint4*>(hb + (tb + u) * 64 + 32 * g + 8 * c);
-                            const uint4 lo = src[0], hi = src[1];
-                            bw[0][0] = lo.x; bw[0][1] = lo.y; bw[0][2] = lo.z; bw[0][3] = lo.w;
-                            bw[0][4] = hi.x; bw[0][5] = hi.y; bw[0][6] = hi.z; bw[0][7] = hi.w;
-                        }
-                        q4_tile<G, 1>(first.w[u][0], first.s[u][0], bw, (tb + u) % TG == TG - 1, part, acc);
-                    }
+                const uint8_t* codes[1] = {base + 16 * lane};
+                const uint16_t* scales[1] = {reinterpret_cast<const uint16_t*>(base + scale_off) + g};
+                q4_advance<G>(codes, scales, t0);
+                int tb = t0;
+                for (; tb + U <= t1; tb += U) {
+                    if (i > 0 || tb > t0) tiles.load(codes, scales);
+                    q4_t1_batch<G, U>(tiles, hb + tb * 64, g, c, part, acc);
+                    q4_advance<G>(codes, scales, U);
+                }
+                for (; tb < t1; tb += V) {
+                    Q4Tiles<G, 1, V> one;
+                    one.load(codes, scales);
+                    q4_t1_batch<G, V>(one, hb + tb * 64, g, c, part, acc);
+                    q4_advance<G>(codes, scales, V);
                 }
             }
             if (c == 0) {
@@ -530,11 +568,68 @@ __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
 // Second launch: CTA = (a piece of up to 4 NTL pairs of one expert, (8 / ksplit) RB
 // blocks of 16 rows); its 8 warps are row groups x ranges of columns.  A warp's next U
 // tiles are loaded while it multiplies the last ones; the B operands come through L1.
+// Bound by instructions as much as by HBM: a tile of 512 bytes takes 44 to turn its
+// codes into fp16, 4 MMAs per column group and about 12 for loads and scales.
 constexpr int kQ4Warps = 8;
 constexpr int kQ4Threads = 32 * kQ4Warps;
 
+// U tiles of a warp's row blocks times the first NB of NTL column groups; hb: B operands of the first tile.
+template <int G, int NB, int NTL, int RB, int U>
+__device__ __forceinline__ void q4_batch(const Q4Tiles<G, RB, U>& tiles, const uint32_t* const (&hb)[NTL],
+                                         float (&part)[RB][NTL][4], float (&acc)[RB][NTL][4]) {
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        uint32_t bw[NTL][8];
+#pragma unroll
+        for (int j = 0; j < NB; j++) {
+            const uint4* src = reinterpret_cast<const uint4*>(hb[j] + u * 64);
+            const uint4 lo = src[0], hi = src[1];
+            bw[j][0] = lo.x; bw[j][1] = lo.y; bw[j][2] = lo.z; bw[j][3] = lo.w;
+            bw[j][4] = hi.x; bw[j][5] = hi.y; bw[j][6] = hi.z; bw[j][7] = hi.w;
+        }
+#pragma unroll
+        for (int r = 0; r < RB; r++) q4_tile<G, NB, NTL>(tiles.w[u][r], tiles.s[u][r], bw, u & 1, part[r], acc[r]);
+    }
+}
+
+// n tiles of a warp's row blocks; while one batch of U is multiplied the next is loaded.
+template <int G, int NB, int NTL, int RB, int U>
+__device__ __forceinline__ void q4_range(const uint8_t* (&codes)[RB], const uint16_t* (&scales)[RB],
+                                         const uint32_t* (&hb)[NTL], int n, float (&acc)[RB][NTL][4]) {
+    constexpr int V = G > kQ4Cols ? 2 : 1;
+    float part[RB][NTL][4];
+    Q4Tiles<G, RB, U> one, two;
+    int left = n / U;
+    auto next = [&](Q4Tiles<G, RB, U>& t) {
+        t.load(codes, scales);
+        q4_advance<G>(codes, scales, U);
+    };
+    auto use = [&](const Q4Tiles<G, RB, U>& t) {
+        q4_batch<G, NB, NTL, RB, U>(t, hb, part, acc);
+#pragma unroll
+        for (int j = 0; j < NB; j++) hb[j] += U * 64;
+        left--;
+    };
+    if (left > 0) next(one);
+    while (left > 0) {
+        if (left > 1) next(two);
+        use(one);
+        if (left == 0) break;
+        if (left > 1) next(one);
+        use(two);
+    }
+    for (int k = n % U; k > 0; k -= V) {
+        Q4Tiles<G, RB, V> t;
+        t.load(codes, scales);
+        q4_advance<G>(codes, scales, V);
+        q4_batch<G, NB, NTL, RB, V>(t, hb, part, acc);
+#pragma unroll
+        for (int j = 0; j < NB; j++) hb[j] += V * 64;
+    }
+}
+
 template <int G, int NTL, int RB, int U>
-__global__ void __launch_bounds__(kQ4Threads) k_q4_mt(const Q4Params P) {
+__global__ void __launch_bounds__(kQ4Threads, 2) k_q4_mt(const Q4Params P) {
     __shared__ float s_part[kQ4Warps][RB * kQ4Rows][4 * NTL + 1];
     __shared__ int s_pair[4 * NTL];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -548,49 +643,41 @@ __global__ void __launch_bounds__(kQ4Threads) k_q4_mt(const Q4Params P) {
     constexpr int TG = G > kQ4Cols ? G / kQ4Cols : 1;  // ranges of whole groups
     const int per = ((ntiles / TG + P.ksplit - 1) / P.ksplit) * TG;
     const int t0 = min(ntiles, wk * per), t1 = min(ntiles, t0 + per);
-    const int64_t bb = q4_block_bytes(P.M.cols_p, G), scale_off = (int64_t)P.M.cols_p * 8;
-    const int blk0 = (int)blockIdx.x * nwr * RB, blk = blk0 + wr * RB, nrb = min(RB, P.M.nblk - blk);
-    const uint8_t* base = P.M.blob + ((int64_t)e * P.M.nblk + (nrb > 0 ? blk : 0)) * bb;
-    Q4Tiles<G, RB, U> cur, nxt;
-    cur.load(base, bb, scale_off, nrb, t0, t1, lane);
-    // this lane's column g of each 8-column B operand: pair g / 2, high part for even g
+    const int64_t bb = q4_block_bytes(P.M.cols_p, G);
+    const int blk0 = (int)blockIdx.x * nwr * RB;
+    const uint8_t* codes[RB];
+    const uint16_t* scales[RB];
+#pragma unroll
+    for (int r = 0; r < RB; r++) {
+        const uint8_t* base = P.M.blob + ((int64_t)e * P.M.nblk + min(blk0 + wr * RB + r, P.M.nblk - 1)) * bb;
+        codes[r] = base + 16 * lane;
+        scales[r] = reinterpret_cast<const uint16_t*>(base + (int64_t)P.M.cols_p * 8) + g;
+    }
+    // this lane's column g of each 8-column B operand: pair g / 2, high part for even g; columns past the last pair
+    // repeat it and are not stored
     const uint32_t* hb[NTL];
 #pragma unroll
     for (int j = 0; j < NTL; j++) {
-        const int i = 4 * j + g / 2;
-        hb[j] = i < np ? P.hb + (int64_t)P.order[piece.y + i] * P.M.cols_p + 32 * (g & 1) + 8 * c : nullptr;
+        const int i = min(4 * j + g / 2, np - 1);
+        hb[j] = P.hb + (int64_t)P.order[piece.y + i] * P.M.cols_p + 32 * (g & 1) + 8 * c;
     }
     if (threadIdx.x < np) s_pair[threadIdx.x] = P.order[piece.y + threadIdx.x];
-    float acc[RB][NTL][4], part[RB][NTL][4];
+    float acc[RB][NTL][4];
 #pragma unroll
     for (int r = 0; r < RB; r++)
 #pragma unroll
         for (int j = 0; j < NTL; j++)
 #pragma unroll
-            for (int q = 0; q < 4; q++) acc[r][j][q] = part[r][j][q] = 0.0f;
-    for (int tb = t0; tb < t1; tb += U) {
-        if (tb + U < t1) nxt.load(base, bb, scale_off, nrb, tb + U, t1, lane);
+            for (int q = 0; q < 4; q++) acc[r][j][q] = 0.0f;
+    q4_advance<G>(codes, scales, t0);
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (tb + u >= t1) break;
-            uint32_t bw[NTL][8];
-#pragma unroll
-            for (int j = 0; j < NTL; j++) {
-                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                if (hb[j]) {
-                    const uint4* src = reinterpret_cast<const uint4*>(hb[j] + (int64_t)(tb + u) * 64);
-                    lo = src[0];
-                    hi = src[1];
-                }
-                bw[j][0] = lo.x; bw[j][1] = lo.y; bw[j][2] = lo.z; bw[j][3] = lo.w;
-                bw[j][4] = hi.x; bw[j][5] = hi.y; bw[j][6] = hi.z; bw[j][7] = hi.w;
-            }
-#pragma unroll
-            for (int r = 0; r < RB; r++)
-                q4_tile<G, NTL>(cur.w[u][r], cur.s[u][r], bw, (tb + u) % TG == TG - 1, part[r], acc[r]);
-        }
-        cur = nxt;
-    }
+    for (int j = 0; j < NTL; j++) hb[j] += t0 * 64;
+    if (NTL > 2 && np > 8)
+        q4_range<G, NTL, NTL, RB, U>(codes, scales, hb, t1 - t0, acc);
+    else if (NTL > 1 && np > 4)
+        q4_range<G, NTL < 2 ? 1 : 2, NTL, RB, U>(codes, scales, hb, t1 - t0, acc);
+    else
+        q4_range<G, 1, NTL, RB, U>(codes, scales, hb, t1 - t0, acc);
     // columns 2c and 2c + 1 of a fragment are the high and the low part of pair c
 #pragma unroll
     for (int r = 0; r < RB; r++)

@@ -14,11 +14,12 @@
 // its A operand, so a lane's 32 codes of a tile are one 16-byte load and no code
 // moves between lanes; then the group scales.
 //
-// Arithmetic: q - 7.5 is exact in fp16 (one mask and one fused multiply-add per two
-// codes, from the bit pattern 0x6400 | q << 4 = 1024 + 16 q).  h is split into an
-// fp16 high part and the fp16 rest after a power-of-two scaling into fp16's range;
-// the two are two columns of the B operand, so a product keeps fp32's precision.
-// A group's fp32 sum is multiplied by its scale in fp32.
+// Arithmetic: q - 8 is exact in fp16, two codes by one mask and one addition (from the
+// bit pattern 0x6400 | q = 1024 + q) or fused multiply-add (0x6400 | 16 q = 1024 + 16 q).
+// h is split into an fp16 high part and the fp16 rest after a power-of-two scaling into
+// fp16's range; the two are two columns of the B operand, so a product keeps fp32's
+// precision.  A group's fp32 sum starts from half the sum of its h, which makes its
+// codes q - 7.5, and is multiplied by its scale in fp32.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -168,13 +169,16 @@ __global__ void k_q4_unpack(const Q4Matrix M, int64_t n, float* __restrict__ out
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
-// The four registers of the A operand of one k step: q - 7.5 of the word's nibbles in
-// fp16, exact: (0x6400 | 16 q) = 1024 + 16 q, times 1/16, minus 71.5.
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
-    const uint32_t v = (w & 0x00f000f0u) | 0x64006400u;
-    const __half2 sixteenth = __half2half2(__ushort_as_half(0x2c00)), bias = __half2half2(__ushort_as_half(0xd478));
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), sixteenth, bias);
-    return *reinterpret_cast<const uint32_t*>(&r);
+// Two registers of the A operand of a k step: q - 8 in fp16, exact, of the nibbles at
+// bits 0 and 16 and at bits 4 and 20.
+__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t& a0, uint32_t& a1) {
+    const uint32_t l = (w & 0x000f000fu) | 0x64006400u, h = (w & 0x00f000f0u) | 0x64006400u;
+    const __half2 m1032 = __half2half2(__ushort_as_half(0xe408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
+                  m72 = __half2half2(__ushort_as_half(0xd480));
+    const __half2 lo = __hadd2(*reinterpret_cast<const __half2*>(&l), m1032);
+    const __half2 hi = __hfma2(*reinterpret_cast<const __half2*>(&h), sixteenth, m72);
+    a0 = *reinterpret_cast<const uint32_t*>(&lo);
+    a1 = *reinterpret_cast<const uint32_t*>(&hi);
 }
 
 __device__ __forceinline__ void q4_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -184,11 +188,12 @@ __device__ __forceinline__ void q4_mma(float (&c)[4], const uint32_t (&a)[4], ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void q4_mma_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// The same from c = (start, 0, start, 0).
+__device__ __forceinline__ void q4_mma_start(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float start) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(start), "f"(0.0f));
 }
 
 // SiLU(yg) * yu of 8 values (yu NULL: yg itself).
@@ -231,6 +236,7 @@ struct Q4Params {
     int32_t* order;      // [pairs] grouped by expert
     int4* pieces;        // [slots] expert (-1: none), first place in order, pairs
     uint32_t* hb;        // [pairs][cols_p / 64][2][32] B operands (high part, low part)
+    float* hsum;         // [pairs][cols_p / G] half the sums of h / hscale over the groups
     float* hscale;       // [pairs]
     float* y;            // [pairs][rows]
     int E, K, T, pairs, slots;
@@ -281,21 +287,24 @@ __device__ __forceinline__ void q4_advance(const uint8_t* (&codes)[RB], const ui
     }
 }
 
-// One tile times its B operands (NB of the NL columns groups that acc has), added to the
-// row block's sums.  With G = 128 a group is two tiles: `part` carries its sum from the
-// first (half = 0) to the second, where its scale is applied.
+// One tile times its B operands (NB of the NL column groups that acc has), added to the
+// row block's sums.  start: half the sum of h over each group that begins here, for the
+// pair of this lane's accumulator columns.  With G = 128 a group is two tiles: `part`
+// carries its sum from the first (half = 0) to the second, where its scale is applied.
 template <int G, int NB, int NL>
-__device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], const uint32_t (&bw)[NL][8], int half,
-                                        float (&part)[NL][4], float (&acc)[NL][4]) {
+__device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], const uint32_t (&bw)[NL][8],
+                                        const float (*start)[NL], int half, float (&part)[NL][4], float (&acc)[NL][4]) {
     const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int t = 0; t < 4; t++) {
-        const uint32_t a[4] = {q4_pair(word[t] << 4), q4_pair(word[t]), q4_pair(word[t] >> 4), q4_pair(word[t] >> 8)};
+        uint32_t a[4];
+        q4_pairs(word[t], a[0], a[1]);
+        q4_pairs(word[t] >> 8, a[2], a[3]);
         const bool begins = G <= 32 ? (t & 1) == 0 : t == 0;
 #pragma unroll
         for (int j = 0; j < NB; j++) {
             if (begins && (G <= kQ4Cols || half == 0))
-                q4_mma_zero(part[j], a, bw[j][2 * t], bw[j][2 * t + 1]);
+                q4_mma_start(part[j], a, bw[j][2 * t], bw[j][2 * t + 1], start[G <= 32 ? t >> 1 : 0][j]);
             else
                 q4_mma(part[j], a, bw[j][2 * t], bw[j][2 * t + 1]);
         }
@@ -314,6 +323,22 @@ __device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], c
     }
 }
 
+// Half the sum of a group's h from the group's chunks of 8 columns, one per lane, in
+// neighbouring lanes: returned in every one of them.
+template <int G>
+__device__ __forceinline__ float q4_group_half(const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&lo[j]));
+        v += (a.x + b.x) + (a.y + b.y);
+    }
+#pragma unroll
+    for (int o = 1; o < G / 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return 0.5f * v;
+}
+
 // ---------------------------------------------------------------------------
 // one token
 // ---------------------------------------------------------------------------
@@ -327,10 +352,10 @@ __device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], c
 constexpr int kQ4T1Warps = 16;
 constexpr size_t kQ4T1Smem = 200 * 1024;
 
-// U tiles of one row block times h.
+// U tiles of one row block times h; sums: of the first tile's group.
 template <int G, int U>
-__device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, 1, U>& tiles, const uint32_t* hb, int g, int c,
-                                            float (&part)[1][4], float (&acc)[1][4]) {
+__device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, 1, U>& tiles, const uint32_t* hb, const float* sums, int g,
+                                            int c, float (&part)[1][4], float (&acc)[1][4]) {
 #pragma unroll
     for (int u = 0; u < U; u++) {
         uint32_t bw[1][8] = {};
@@ -340,18 +365,24 @@ __device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, 1, U>& tiles, const
             bw[0][0] = lo.x; bw[0][1] = lo.y; bw[0][2] = lo.z; bw[0][3] = lo.w;
             bw[0][4] = hi.x; bw[0][5] = hi.y; bw[0][6] = hi.z; bw[0][7] = hi.w;
         }
-        q4_tile<G, 1, 1>(tiles.w[u][0], tiles.s[u][0], bw, u & 1, part, acc);
+        constexpr int NS = Q4Tiles<G, 1, U>::NS;
+        float start[NS][1];
+#pragma unroll
+        for (int n = 0; n < NS; n++) start[n][0] = c == 0 ? sums[u * kQ4Cols / G + n] : 0.0f;
+        q4_tile<G, 1, 1>(tiles.w[u][0], tiles.s[u][0], bw, start, u & 1, part, acc);
     }
 }
 
 template <int G>
 __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
     constexpr int U = 6, V = G > kQ4Cols ? 2 : 1;  // tiles per batch, and per step of what is left
-    extern __shared__ __align__(16) uint32_t s_h[];  // [K][tiles][2][32], then [row blocks][warp][16] and [K] ids, weights
+    extern __shared__ __align__(16) uint32_t s_h[];  // [K][tiles][2][32], then [K][groups], [row blocks][unit][16], ids, weights
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int ntiles = P.M.cols_p / kQ4Cols, nblk = P.M.nblk;
     const int nrb = (nblk - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // row blocks blockIdx + i gridDim
-    float* s_part = reinterpret_cast<float*>(s_h + (size_t)P.K * P.M.cols_p);
+    const int ngroups = P.M.cols_p / G;
+    float* s_sum = reinterpret_cast<float*>(s_h + (size_t)P.K * P.M.cols_p);
+    float* s_part = s_sum + P.K * ngroups;
     int* s_e = reinterpret_cast<int*>(s_part + (size_t)nrb * P.K * P.ksplit * kQ4Rows);
     float* s_g = reinterpret_cast<float*>(s_e + P.K);
     const int64_t bb = q4_block_bytes(P.M.cols_p, G), scale_off = (int64_t)P.M.cols_p * 8;
@@ -380,6 +411,7 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
         const int j = unit / P.ksplit, t0 = min(ntiles, unit % P.ksplit * per), t1 = min(ntiles, t0 + per);
         const int e = s_e[j];
         uint32_t* hb = s_h + ((size_t)j * ntiles) * 64;
+        const float* sums = s_sum + j * ngroups;
         float scale = 1.0f;
         Q4Tiles<G, 1, U> tiles;
         const bool batches = t1 - t0 >= U;
@@ -400,16 +432,22 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
             }
             scale = q4_h_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
             const float inv = 1.0f / scale;
-            for (int ch = 8 * t0 + lane; ch < 8 * t1; ch += 32) {
+            // whole warps: a group's chunks sit in neighbouring lanes
+            for (int ch = 8 * t0 + lane; ch - lane < 8 * t1; ch += 32) {
                 float h[8] = {};
+                uint32_t hi[4], lo[4];
                 if (ch < c1) q4_h8(P.yg, P.yu, hrow + 8 * ch, h);
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    uint32_t hi, lo;
-                    q4_split(h[i] * inv, h[i + 1] * inv, hi, lo);
-                    const int w = q4_b_word(ch % 8 * 8 + i);
-                    hb[(ch / 8) * 64 + w] = hi;
-                    hb[(ch / 8) * 64 + 32 + w] = lo;
+                for (int i = 0; i < 4; i++) q4_split(h[2 * i] * inv, h[2 * i + 1] * inv, hi[i], lo[i]);
+                const float sum = q4_group_half<G>(hi, lo);
+                if (ch < 8 * t1) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int w = q4_b_word(ch % 8 * 8 + 2 * i);
+                        hb[(ch / 8) * 64 + w] = hi[i];
+                        hb[(ch / 8) * 64 + 32 + w] = lo[i];
+                    }
+                    if (ch % (G / 8) == 0) s_sum[j * ngroups + ch / (G / 8)] = sum;
                 }
             }
             __syncwarp();
@@ -424,13 +462,13 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
                 int tb = t0;
                 for (; tb + U <= t1; tb += U) {
                     if (i > 0 || tb > t0) tiles.load(codes, scales);
-                    q4_t1_batch<G, U>(tiles, hb + tb * 64, g, c, part, acc);
+                    q4_t1_batch<G, U>(tiles, hb + tb * 64, sums + tb * kQ4Cols / G, g, c, part, acc);
                     q4_advance<G>(codes, scales, U);
                 }
                 for (; tb < t1; tb += V) {
                     Q4Tiles<G, 1, V> one;
                     one.load(codes, scales);
-                    q4_t1_batch<G, V>(one, hb + tb * 64, g, c, part, acc);
+                    q4_t1_batch<G, V>(one, hb + tb * 64, sums + tb * kQ4Cols / G, g, c, part, acc);
                     q4_advance<G>(codes, scales, V);
                 }
             }
@@ -504,6 +542,7 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
     }
 }
 
+template <int G>
 __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
     extern __shared__ int32_t s_cnt[];
     __shared__ unsigned s_max;
@@ -544,21 +583,27 @@ __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
     const float scale = q4_h_scale(__uint_as_float(s_max)), inv = 1.0f / scale;
     if (tid == 0) P.hscale[pair] = scale;
     uint32_t* hb = P.hb + (int64_t)pair * P.M.cols_p;
+    // whole warps: a group's chunks sit in neighbouring lanes
     auto put = [&](int c, const float(&v)[8]) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) q4_split(v[2 * j] * inv, v[2 * j + 1] * inv, hi[j], lo[j]);
+        const float sum = q4_group_half<G>(hi, lo);
+        if (c >= P.M.cols_p / 8) return;
         uint32_t* tile = hb + (int64_t)(c / 8) * 64;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            uint32_t hi, lo;
-            q4_split(v[j] * inv, v[j + 1] * inv, hi, lo);
-            const int w = q4_b_word(c % 8 * 8 + j);
-            tile[w] = hi;
-            tile[32 + w] = lo;
+        for (int j = 0; j < 4; j++) {
+            const int w = q4_b_word(c % 8 * 8 + 2 * j);
+            tile[w] = hi[j];
+            tile[32 + w] = lo[j];
         }
+        if (c % (G / 8) == 0) P.hsum[(int64_t)pair * (P.M.cols_p / G) + c / (G / 8)] = sum;
     };
 #pragma unroll
     for (int i = 0; i < KEEP; i++)
-        if (tid + i * kQ4PrepThreads < P.M.cols_p / 8) put(tid + i * kQ4PrepThreads, h[i]);
-    for (int c = tid + KEEP * kQ4PrepThreads; c < P.M.cols_p / 8; c += kQ4PrepThreads) {
+        if (i * kQ4PrepThreads < P.M.cols_p / 8) put(tid + i * kQ4PrepThreads, h[i]);
+    for (int c0 = KEEP * kQ4PrepThreads; c0 < P.M.cols_p / 8; c0 += kQ4PrepThreads) {
+        const int c = c0 + tid;
         float v[8] = {};
         if (c < nch) q4_h8(P.yg, P.yu, base + 8 * c, v);
         put(c, v);
@@ -573,29 +618,37 @@ __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
 constexpr int kQ4Warps = 8;
 constexpr int kQ4Threads = 32 * kQ4Warps;
 
-// U tiles of a warp's row blocks times the first NB of NTL column groups; hb: B operands of the first tile.
+// U tiles of a warp's row blocks times the first NB of NTL column groups; hb: B operands
+// of the first tile, sums: half sums of its group.
 template <int G, int NB, int NTL, int RB, int U>
 __device__ __forceinline__ void q4_batch(const Q4Tiles<G, RB, U>& tiles, const uint32_t* const (&hb)[NTL],
-                                         float (&part)[RB][NTL][4], float (&acc)[RB][NTL][4]) {
+                                         const float* const (&sums)[NTL], float (&part)[RB][NTL][4],
+                                         float (&acc)[RB][NTL][4]) {
+    constexpr int NS = Q4Tiles<G, RB, U>::NS;
 #pragma unroll
     for (int u = 0; u < U; u++) {
         uint32_t bw[NTL][8];
+        float start[NS][NTL];
 #pragma unroll
         for (int j = 0; j < NB; j++) {
             const uint4* src = reinterpret_cast<const uint4*>(hb[j] + u * 64);
             const uint4 lo = src[0], hi = src[1];
             bw[j][0] = lo.x; bw[j][1] = lo.y; bw[j][2] = lo.z; bw[j][3] = lo.w;
             bw[j][4] = hi.x; bw[j][5] = hi.y; bw[j][6] = hi.z; bw[j][7] = hi.w;
+#pragma unroll
+            for (int n = 0; n < NS; n++) start[n][j] = sums[j][u * kQ4Cols / G + n];
         }
 #pragma unroll
-        for (int r = 0; r < RB; r++) q4_tile<G, NB, NTL>(tiles.w[u][r], tiles.s[u][r], bw, u & 1, part[r], acc[r]);
+        for (int r = 0; r < RB; r++)
+            q4_tile<G, NB, NTL>(tiles.w[u][r], tiles.s[u][r], bw, start, u & 1, part[r], acc[r]);
     }
 }
 
 // n tiles of a warp's row blocks; while one batch of U is multiplied the next is loaded.
 template <int G, int NB, int NTL, int RB, int U>
 __device__ __forceinline__ void q4_range(const uint8_t* (&codes)[RB], const uint16_t* (&scales)[RB],
-                                         const uint32_t* (&hb)[NTL], int n, float (&acc)[RB][NTL][4]) {
+                                         const uint32_t* (&hb)[NTL], const float* (&sums)[NTL], int n,
+                                         float (&acc)[RB][NTL][4]) {
     constexpr int V = G > kQ4Cols ? 2 : 1;
     float part[RB][NTL][4];
     Q4Tiles<G, RB, U> one, two;
@@ -605,9 +658,12 @@ __device__ __forceinline__ void q4_range(const uint8_t* (&codes)[RB], const uint
         q4_advance<G>(codes, scales, U);
     };
     auto use = [&](const Q4Tiles<G, RB, U>& t) {
-        q4_batch<G, NB, NTL, RB, U>(t, hb, part, acc);
+        q4_batch<G, NB, NTL, RB, U>(t, hb, sums, part, acc);
 #pragma unroll
-        for (int j = 0; j < NB; j++) hb[j] += U * 64;
+        for (int j = 0; j < NB; j++) {
+            hb[j] += U * 64;
+            sums[j] += U * kQ4Cols / G;
+        }
         left--;
     };
     if (left > 0) next(one);
@@ -622,9 +678,12 @@ __device__ __forceinline__ void q4_range(const uint8_t* (&codes)[RB], const uint
         Q4Tiles<G, RB, V> t;
         t.load(codes, scales);
         q4_advance<G>(codes, scales, V);
-        q4_batch<G, NB, NTL, RB, V>(t, hb, part, acc);
+        q4_batch<G, NB, NTL, RB, V>(t, hb, sums, part, acc);
 #pragma unroll
-        for (int j = 0; j < NB; j++) hb[j] += V * 64;
+        for (int j = 0; j < NB; j++) {
+            hb[j] += V * 64;
+            sums[j] += V * kQ4Cols / G;
+        }
     }
 }
 
@@ -656,10 +715,12 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_mt(const Q4Params P) {
     // this lane's column g of each 8-column B operand: pair g / 2, high part for even g; columns past the last pair
     // repeat it and are not stored
     const uint32_t* hb[NTL];
+    const float* sums[NTL];  // of the pair of its accumulator columns 2c (high part) and 2c + 1
 #pragma unroll
     for (int j = 0; j < NTL; j++) {
-        const int i = min(4 * j + g / 2, np - 1);
-        hb[j] = P.hb + (int64_t)P.order[piece.y + i] * P.M.cols_p + 32 * (g & 1) + 8 * c;
+        const int i = min(4 * j + g / 2, np - 1), k = min(4 * j + c, np - 1);
+        hb[j] = P.hb + (int64_t)P.order[piece.y + i] * P.M.cols_p + 32 * (g & 1) + 8 * c + t0 * 64;
+        sums[j] = P.hsum + (int64_t)P.order[piece.y + k] * (P.M.cols_p / G) + t0 * kQ4Cols / G;
     }
     if (threadIdx.x < np) s_pair[threadIdx.x] = P.order[piece.y + threadIdx.x];
     float acc[RB][NTL][4];
@@ -670,14 +731,12 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_mt(const Q4Params P) {
 #pragma unroll
             for (int q = 0; q < 4; q++) acc[r][j][q] = 0.0f;
     q4_advance<G>(codes, scales, t0);
-#pragma unroll
-    for (int j = 0; j < NTL; j++) hb[j] += t0 * 64;
     if (NTL > 2 && np > 8)
-        q4_range<G, NTL, NTL, RB, U>(codes, scales, hb, t1 - t0, acc);
+        q4_range<G, NTL, NTL, RB, U>(codes, scales, hb, sums, t1 - t0, acc);
     else if (NTL > 1 && np > 4)
-        q4_range<G, NTL < 2 ? 1 : 2, NTL, RB, U>(codes, scales, hb, t1 - t0, acc);
+        q4_range<G, NTL < 2 ? 1 : 2, NTL, RB, U>(codes, scales, hb, sums, t1 - t0, acc);
     else
-        q4_range<G, 1, NTL, RB, U>(codes, scales, hb, t1 - t0, acc);
+        q4_range<G, 1, NTL, RB, U>(codes, scales, hb, sums, t1 - t0, acc);
     // columns 2c and 2c + 1 of a fragment are the high and the low part of pair c
 #pragma unroll
     for (int r = 0; r < RB; r++)
@@ -733,7 +792,8 @@ static int q4_slots(int pairs, int E) { return std::min(pairs, E) + pairs / q4_t
 static size_t q4_t1_smem(const bitsmoe_ffn_dims* d, int group, int sms) {
     const int nblk = (d->d_model + kQ4Rows - 1) / kQ4Rows, grid = std::min(nblk, sms), nrb = (nblk + grid - 1) / grid;
     const size_t units = (size_t)d->top_k * std::max(1, kQ4T1Warps / d->top_k);
-    return 4ull * d->top_k * q4_cols_padded(d->d_ff, group) + 4ull * nrb * units * kQ4Rows + 8ull * d->top_k;
+    const size_t cols_p = q4_cols_padded(d->d_ff, group);
+    return 4ull * d->top_k * (cols_p + cols_p / group) + 4ull * nrb * units * kQ4Rows + 8ull * d->top_k;
 }
 constexpr int kQ4Sms = 148;  // CTAs of the single-token kernel: one per SM
 static bool q4_single(const bitsmoe_ffn_dims* d, int group, int T) {
@@ -744,6 +804,7 @@ struct Q4WS {
     int32_t* order;
     int4* pieces;
     uint32_t* hb;
+    float* hsum;
     float* hscale;
     float* y;
     uint64_t used;
@@ -761,6 +822,7 @@ static Q4WS q4_ws(const bitsmoe_ffn_dims* d, int group, int T, uint8_t* base) {
     w.order = (int32_t*)take(4 * pairs);
     w.pieces = (int4*)take(16ull * q4_slots((int)pairs, d->n_experts));
     w.hb = (uint32_t*)take(4 * pairs * dp);
+    w.hsum = (float*)take(4 * pairs * (dp / group));
     w.hscale = (float*)take(4 * pairs);
     w.y = (float*)take(4 * pairs * d->d_model);
     w.used = used;
@@ -900,11 +962,15 @@ BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_ffn_dims* dims, const void* bl
     P.order = w.order;
     P.pieces = w.pieces;
     P.hb = w.hb;
+    P.hsum = w.hsum;
     P.hscale = w.hscale;
     P.y = w.y;
     P.tok = q4_tok(P.pairs, P.E);
     P.slots = q4_slots(P.pairs, P.E);
-    int rc = launch_pdl(k_q4_prep, dim3((unsigned)P.pairs + 1), dim3(kQ4PrepThreads), 4ull * P.E, s, P);
+    const dim3 pgrid((unsigned)P.pairs + 1), pblock(kQ4PrepThreads);
+    int rc = group == 32   ? launch_pdl(k_q4_prep<32>, pgrid, pblock, 4ull * P.E, s, P)
+             : group == 64 ? launch_pdl(k_q4_prep<64>, pgrid, pblock, 4ull * P.E, s, P)
+                           : launch_pdl(k_q4_prep<128>, pgrid, pblock, 4ull * P.E, s, P);
     if (rc) return rc;
     rc = group == 32 ? launch_q4_mt<32>(P, s) : group == 64 ? launch_q4_mt<64>(P, s) : launch_q4_mt<128>(P, s);
     if (rc) return rc;

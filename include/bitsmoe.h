@@ -405,21 +405,26 @@ int bitsmoe_allocate_widths(const float *amps_host, const double *beta_host, con
  *   u  = y[t],  or  y[t] rsqrt(mean(y[t]^2) + eps) w_post          (w_post given)
  *   h' = h[t] + alpha gate u
  *   x  = h' rsqrt(mean(h'^2) + eps) w_pre
- * in fp32, each output rounded once to its type (x is formed from the fp32 h').
- *   h dev [T] rows of d elements of h_type, h_stride elements apart; y likewise or NULL
- *   (then h' = h, and w_post and gate are NULL); w_post, w_pre dev [d] f32 or NULL;
- *   gate dev f32 or NULL: gate[t gate_stride + i] when gate_per_channel, else
- *   gate[t gate_stride] (gate_stride 0: the same for every row); h_out dev, h's type,
- *   or NULL (not written; may be h itself, with the same stride); x dev of x_type or
- *   NULL (not written; else w_pre is needed).  At least one of h_out and x.  Rows of
- *   an output must not overlap each other or another operand (h_out = h apart).
+ * in fp32, each output rounded once to its type (x is formed from the fp32 h').  Rows of
+ * an output must not overlap each other or another operand (h_out = h apart).
  * Any width and stride; rows on 16-byte boundaries with d a multiple of 8 are read and
- * written 16 bytes at a time.  T = 0 is a no-op.  Errors: EINVAL, ECUDA. */
-int bitsmoe_norm_residual(int32_t T, int32_t d, const void* h, int32_t h_type, int64_t h_stride, const void* y,
-                          int32_t y_type, int64_t y_stride, const float* w_post, const float* gate,
-                          int64_t gate_stride, int32_t gate_per_channel, float alpha, void* h_out,
-                          int64_t h_out_stride, const float* w_pre, void* x, int32_t x_type, int64_t x_stride,
-                          float eps, void* stream);
+ * written 16 bytes at a time.  rows = 0 is a no-op. */
+typedef struct {
+    const void *h;         /* dev, rows of d elements of h_type, h_stride elements apart */
+    const void *y;         /* dev, likewise, or NULL: h' = h, and w_post and gate are NULL */
+    const float *w_post;   /* dev [d] or NULL */
+    const float *gate;     /* dev or NULL: gate[t gate_stride + i] when gate_per_channel, else gate[t gate_stride]
+                              (gate_stride 0: the same for every row) */
+    void *h_out;           /* dev (out) of h's type, or NULL: not written; may be h itself, with the same stride */
+    const float *w_pre;    /* dev [d]; NULL only when x is */
+    void *x;               /* dev (out) of x_type, or NULL: not written; at least one of h_out and x */
+    int64_t h_stride, y_stride, gate_stride, h_out_stride, x_stride;
+    int32_t rows, d, h_type, y_type, x_type, gate_per_channel;
+    float alpha, eps;
+} bitsmoe_norm_args;
+
+/* Errors: EINVAL, ECUDA. */
+int bitsmoe_norm_residual(const bitsmoe_norm_args *args, void *stream);
 
 /* ---- routing ---- */
 #define BITSMOE_SCORE_SOFTMAX 0 /* s = softmax of the row's logits */
@@ -430,23 +435,31 @@ uint64_t bitsmoe_topk_route_workspace_bytes(int32_t T, int32_t n_experts, int32_
 
 /* The top_k experts of every token from its router logits, their gate weights, and the
  * (token, slot) pairs grouped by expert.
- *   logits dev [T] rows of n_experts elements of logits_type, logits_stride apart;
- *   topk_ids dev [T][top_k] int32 (out): the largest logits in descending order, equal
- *   ones in ascending expert order; gate_w dev [T][top_k] f32 (out): scale s, or scale
- *   s / (sum of the token's chosen s) when renormalise.
- *   offsets dev [n_experts + 1] int32 (out) or NULL, order dev [T top_k] int32 (out) or
- *   NULL: pairs t top_k + slot sorted by expert, ascending inside an expert; expert e's
- *   are order[offsets[e] .. offsets[e+1]); -1 behind the last.
  * A logit of -inf closes an expert to the token; a slot without an open expert gets id
  * -1, weight 0 and no group.  A row with a NaN or +inf logit gets -1 and 0 in every
- * slot and sets BITSMOE_ST_NONFINITE.  n_experts <= 8192, top_k <= min(n_experts,
- * 1024).  workspace dev (256-byte aligned, no initialisation) only when offsets or
- * order are given and bitsmoe_topk_route_workspace_bytes is not 0; calls that share it
- * must not overlap.  T = 0 writes zero offsets.  Errors: EINVAL, ESIZE, ECUDA. */
-int bitsmoe_topk_route(const void* logits, int32_t logits_type, int64_t logits_stride, int32_t T, int32_t n_experts,
-                       int32_t top_k, int32_t scoring, int32_t renormalise, float scale, int32_t* topk_ids,
-                       float* gate_w, int32_t* offsets, int32_t* order, void* workspace, uint64_t workspace_bytes,
-                       int32_t* status, void* stream);
+ * slot and sets BITSMOE_ST_NONFINITE.  n_experts <= 8192, top_k <= min(n_experts, 1024).
+ * tokens = 0 writes zero offsets. */
+typedef struct {
+    const void *logits;  /* dev, rows of n_experts elements of logits_type, logits_stride elements apart */
+    int32_t *topk_ids;   /* dev [tokens][top_k] (out): the largest logits in descending order, equal ones in
+                            ascending expert order */
+    float *gate_w;       /* dev [tokens][top_k] (out): scale s, or scale s / (sum of the token's chosen s) when
+                            renormalise */
+    int32_t *offsets;    /* dev [n_experts + 1] (out) or NULL */
+    int32_t *order;      /* dev [tokens top_k] (out) or NULL: pairs t top_k + slot sorted by expert, ascending inside
+                            an expert; expert e's are order[offsets[e] .. offsets[e+1]); -1 behind the last */
+    void *workspace;     /* dev, 256-byte aligned, no initialisation; only when offsets or order are given and
+                            bitsmoe_topk_route_workspace_bytes is not 0.  Calls that share it must not overlap. */
+    int32_t *status;     /* dev or NULL */
+    uint64_t workspace_bytes;
+    int64_t logits_stride;
+    int32_t tokens, n_experts, top_k, logits_type, scoring, renormalise;
+    float scale;
+    int32_t reserved;    /* 0 */
+} bitsmoe_route_args;
+
+/* Errors: EINVAL, ESIZE, ECUDA. */
+int bitsmoe_topk_route(const bitsmoe_route_args *args, void *stream);
 
 /* ---- matrices in 4 bits with group scales ----
  * E matrices [rows][cols]; each group of `group` (32, 64 or 128) columns of a row has
@@ -480,46 +493,61 @@ int bitsmoe_q4_unpack(const void* blob, int32_t n_experts, int32_t rows, int32_t
 uint64_t bitsmoe_ffn_down_q4_workspace_bytes(const bitsmoe_ffn_dims* dims, int32_t group, int32_t T);
 int bitsmoe_ffn_down_q4_launches(const bitsmoe_ffn_dims* dims, int32_t group, int32_t T);
 
-/* bitsmoe_ffn_down with the down matrices [d_model][d_ff] in 4 bits (blob, from
- * bitsmoe_q4_pack with the same group).  Y_up NULL: h = Y_gate, a plain routed product
- * without the activation.  Other arguments, routing errors and the slot-order sum as
- * in bitsmoe_ffn_down; products keep fp32 precision (a group's sum is scaled in fp32).
- * Errors: EINVAL, ESIZE, ECUDA. */
-int bitsmoe_ffn_down_q4(const bitsmoe_ffn_dims* dims, const void* blob, int32_t group, const float* Y_gate,
-                        const float* Y_up, const int32_t* topk_ids, const float* gate_w, int32_t T, float* out,
-                        void* workspace, uint64_t workspace_bytes, int32_t* status, void* stream);
+/* bitsmoe_ffn_down with the down matrices [d_model][d_ff] in 4 bits.  Routing errors and
+ * the slot-order sum as there; products keep fp32 precision (a group's sum is scaled in
+ * fp32).  At most 4096 experts. */
+typedef struct {
+    bitsmoe_ffn_dims dims;
+    int32_t group, tokens;
+    const void *blob;          /* dev, from bitsmoe_q4_pack with the same group; 16-byte aligned */
+    const float *Y_gate;       /* dev [tokens][top_k][d_ff], 16-byte aligned */
+    const float *Y_up;         /* dev, likewise, or NULL: h = Y_gate, a plain routed product without the activation */
+    const int32_t *topk_ids;   /* dev [tokens][top_k] */
+    const float *gate_w;       /* dev [tokens][top_k], applied as given */
+    float *out;                /* dev [tokens][d_model] */
+    void *workspace;           /* dev, 256-byte aligned, no initialisation; NULL when its size is 0 */
+    int32_t *status;           /* dev or NULL */
+    uint64_t workspace_bytes;
+} bitsmoe_q4_args;
+
+/* Errors: EINVAL, ESIZE, ECUDA. */
+int bitsmoe_ffn_down_q4(const bitsmoe_q4_args *args, void *stream);
 
 /* ---- products grouped by expert ---- */
 #define BITSMOE_GMM_MAX_EXPERTS 4096
-
-typedef struct {
-    int32_t n_rows;    /* rows the groups may cover: rows of out, entries of `rows` */
-    int32_t n_a_rows;  /* rows of A */
-    int32_t n_out;     /* N: rows of each expert's matrix */
-    int32_t n_in;      /* K: its columns, a multiple of 8 */
-    int32_t n_experts; /* E <= BITSMOE_GMM_MAX_EXPERTS */
-    int32_t in_type;   /* BITSMOE_F16 or BITSMOE_BF16: A, W and W_up */
-    int32_t out_type;  /* in_type or BITSMOE_F32 */
-} bitsmoe_gmm_dims;
 
 /* Rows sorted by expert times their expert's matrix: for every i with offsets[e] <= i <
  * offsets[e+1], with a = row i of A (rows NULL) or row rows[i] / rows_per_a,
  *   out[o][n] = sum_k W[e][n][k] a[k],                                  or, W_up given,
  *   out[o][n] = SiLU(sum_k W[e][n][k] a[k]) (sum_k W_up[e][n][k] a[k]),
  * o = i, or rows[i] with scatter.  fp32 sums, one rounding to out's type.
- *   A dev rows of n_in elements, a_stride elements apart (a multiple of 8, >= n_in),
- *   W, W_up dev [E][n_out][n_in], all 16-byte aligned; offsets dev [E + 1] int32,
- *   ascending, offsets[E] <= n_rows; rows dev [n_rows] int32 or NULL (then rows_per_a
- *   is 1, scatter 0 and n_a_rows >= n_rows); out dev [n_rows][n_out].
  * offsets and rows as bitsmoe_topk_route writes them: with rows = order and rows_per_a
  * = top_k every routed pair reads its token's row.  Rows of out that no group names are
  * left as they are.  The sizes of the groups stay on the device: nothing waits for
  * them.  An offset outside [0, n_rows] or below the one before it is clamped, and a
  * row index outside A (or out, with scatter) is left out; both set BITSMOE_ST_BADGROUP.
- * Two sorted rows with the same output row race.  Errors: EINVAL, ECUDA. */
-int bitsmoe_grouped_matmul(const bitsmoe_gmm_dims* dims, const void* A, int64_t a_stride, const void* W,
-                           const void* W_up, const int32_t* offsets, const int32_t* rows, int32_t rows_per_a,
-                           int32_t scatter, void* out, int32_t* status, void* stream);
+ * Two sorted rows with the same output row race. */
+typedef struct {
+    const void *A;          /* dev, n_a_rows rows of n_in elements, a_stride elements apart (a multiple of 8, >= n_in) */
+    const void *W;          /* dev [n_experts][n_out][n_in]; A, W and W_up are 16-byte aligned */
+    const void *W_up;       /* dev, likewise, or NULL */
+    const int32_t *offsets; /* dev [n_experts + 1], ascending, the last <= n_rows */
+    const int32_t *rows;    /* dev [n_rows] or NULL: then rows_per_a is 1, scatter 0 and n_a_rows >= n_rows */
+    void *out;              /* dev [n_rows][n_out] */
+    int32_t *status;        /* dev or NULL */
+    int64_t a_stride;
+    int32_t n_rows;         /* rows the groups may cover: rows of out, entries of `rows` */
+    int32_t n_a_rows, n_out;
+    int32_t n_in;           /* a multiple of 8 */
+    int32_t n_experts;      /* <= BITSMOE_GMM_MAX_EXPERTS */
+    int32_t in_type;        /* BITSMOE_F16 or BITSMOE_BF16: A, W and W_up */
+    int32_t out_type;       /* in_type or BITSMOE_F32 */
+    int32_t rows_per_a, scatter;
+    int32_t reserved;       /* 0 */
+} bitsmoe_gmm_args;
+
+/* Errors: EINVAL, ECUDA. */
+int bitsmoe_grouped_matmul(const bitsmoe_gmm_args *args, void *stream);
 
 /* Waits for `stream`, then copies the device status word to *out_host.
  * Errors: EINVAL, ECUDA. */

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -58,12 +59,6 @@ class FfnDims(ctypes.Structure):
                 ("top_k", ctypes.c_int32)]
 
 
-class GmmDims(ctypes.Structure):
-    _fields_ = [("n_rows", ctypes.c_int32), ("n_a_rows", ctypes.c_int32), ("n_out", ctypes.c_int32),
-                ("n_in", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("in_type", ctypes.c_int32),
-                ("out_type", ctypes.c_int32)]
-
-
 class ProjIO(ctypes.Structure):
     _fields_ = [("plan", ctypes.c_void_p), ("blob", ctypes.c_void_p), ("phi_t", ctypes.c_void_p),
                 ("Z", ctypes.c_void_p), ("Y_experts", ctypes.c_void_p), ("Y_sum", ctypes.c_void_p)]
@@ -81,7 +76,6 @@ def lib() -> ctypes.CDLL:
                                f" (checked=True for the bounds-checked build)")
         L = ctypes.CDLL(_LIB_PATH)
         vp, u64, i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int32
-        i64, f32 = ctypes.c_int64, ctypes.c_float
         sig = {
             "bitsmoe_pack_plan": ([ctypes.POINTER(Dims), vp, ctypes.POINTER(vp)], ctypes.c_int),
             "bitsmoe_plan_from_header": ([vp, u64, i32, i32, ctypes.POINTER(vp)], ctypes.c_int),
@@ -118,20 +112,16 @@ def lib() -> ctypes.CDLL:
             "bitsmoe_fqcm_eps": ([vp, i32, i32, i32, vp], ctypes.c_int),
             "bitsmoe_fqcm_beta": ([vp, vp, vp, i32, i32, i32, i32, vp], ctypes.c_int),
             "bitsmoe_allocate_widths": ([vp, vp, vp, i32, i32, i32, u64, vp, vp], ctypes.c_int),
-            "bitsmoe_norm_residual": ([i32, i32, vp, i32, i64, vp, i32, i64, vp, vp, i64, i32, f32, vp, i64, vp, vp, i32,
-                                       i64, f32, vp], ctypes.c_int),
+            "bitsmoe_norm_residual": ([vp, vp], ctypes.c_int),
             "bitsmoe_topk_route_workspace_bytes": ([i32, i32, i32], u64),
-            "bitsmoe_topk_route": ([vp, i32, i64, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp, u64, vp, vp],
-                                   ctypes.c_int),
+            "bitsmoe_topk_route": ([vp, vp], ctypes.c_int),
             "bitsmoe_q4_bytes": ([i32, i32, i32, i32], u64),
             "bitsmoe_q4_pack": ([vp, i32, i32, i32, i32, i32, vp, vp, vp], ctypes.c_int),
             "bitsmoe_q4_unpack": ([vp, i32, i32, i32, i32, vp, vp], ctypes.c_int),
             "bitsmoe_ffn_down_q4_workspace_bytes": ([ctypes.POINTER(FfnDims), i32, i32], u64),
             "bitsmoe_ffn_down_q4_launches": ([ctypes.POINTER(FfnDims), i32, i32], ctypes.c_int),
-            "bitsmoe_ffn_down_q4": ([ctypes.POINTER(FfnDims), vp, i32, vp, vp, vp, vp, i32, vp, vp, u64, vp, vp],
-                                    ctypes.c_int),
-            "bitsmoe_grouped_matmul": ([ctypes.POINTER(GmmDims), vp, i64, vp, vp, vp, vp, i32, i32, vp, vp, vp],
-                                       ctypes.c_int),
+            "bitsmoe_ffn_down_q4": ([vp, vp], ctypes.c_int),
+            "bitsmoe_grouped_matmul": ([vp, vp], ctypes.c_int),
             "bitsmoe_read_status": ([vp, vp, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
             "bitsmoe_strerror": ([ctypes.c_int], ctypes.c_char_p),
             "bitsmoe_version": ([], ctypes.c_int),
@@ -397,42 +387,61 @@ def allocate_widths(amps_host, beta_host, eps_host, d_out: int, budget_bits: int
 
 
 # ---- the block around the routed experts ----
+# These calls take one structure.  It is packed into a bytes object (one C call) instead
+# of a ctypes structure or a long argument list, which cost more than the launch itself.
 _TYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+_NORM = struct.Struct("@7P5q6i2f")         # bitsmoe_norm_args
+_ROUTE = struct.Struct("@7PQq6ifi")        # bitsmoe_route_args
+_Q4 = struct.Struct("@6i8PQ")              # bitsmoe_q4_args
+_GMM = struct.Struct("@7Pq10i")            # bitsmoe_gmm_args
 
 
 def _refuse(what: str, why: str):
     raise BitsMoEError(EINVAL, f"{what}: {why}")
 
 
-def _type(what: str, name: str, t: torch.Tensor) -> int:
-    code = _TYPE.get(t.dtype)
-    if code is None:
-        _refuse(what, f"{name} is {t.dtype}, not float32, float16 or bfloat16")
-    return code
-
-
-def _rows(what: str, name: str, t: torch.Tensor, shape: tuple) -> int:
-    """Row stride of a 2-D operand with unit column stride."""
-    if t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+def _matrix(what: str, name: str, t: torch.Tensor, shape: tuple, dev: int) -> tuple:
+    """(pointer, type, row stride) of a 2-D operand with contiguous rows on GPU dev."""
+    s = t.stride()
+    kind = _TYPE.get(t.dtype)
+    if t.shape != shape or (s[1] != 1 and shape[1] > 1):
         _refuse(what, f"{name} is not {list(shape)} with contiguous rows")
-    return t.stride(0)
+    if kind is None:
+        _refuse(what, f"{name} is {t.dtype}, not float32, float16 or bfloat16")
+    if t.get_device() != dev:
+        _refuse(what, "the tensors are not on one GPU")
+    return t.data_ptr(), kind, s[0]
 
 
-def _dense(what: str, name: str, t: torch.Tensor, dtype, shape: tuple) -> int:
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+def _dense(what: str, name: str, t: torch.Tensor, dtype, shape: tuple, dev: int) -> int:
+    """Pointer of a contiguous operand on GPU dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         _refuse(what, f"{name} is not a contiguous {dtype} tensor of shape {list(shape)}")
+    if t.get_device() != dev:
+        _refuse(what, "the tensors are not on one GPU")
     return t.data_ptr()
 
 
-def _launch(what: str, call, tensors, args: tuple, stream):
-    """Calls the library on the device of the tensors, which they share; the stream
-    defaults to torch's current stream there."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and (t.device != dev or not t.is_cuda):
-            _refuse(what, "the tensors are not on one GPU")
-    if dev.index == torch.cuda.current_device():
-        rc = call(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
+def _where(what: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        _refuse(what, "the tensors are not on one GPU")
+    return dev
+
+
+def _extra(what: str, t, dev: int) -> int:
+    """Pointer of an optional workspace or status tensor on GPU dev; 0 for None."""
+    if t is None:
+        return 0
+    if t.get_device() != dev:
+        _refuse(what, "the tensors are not on one GPU")
+    return t.data_ptr()
+
+
+def _launch(what: str, call, dev: int, stream, *args):
+    """Calls the library with GPU dev current; the stream defaults to torch's current one there."""
+    if dev == torch._C._cuda_getDevice():
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
             rc = call(*args, _stream(stream))
@@ -448,34 +457,42 @@ def norm_residual(h, y=None, w_pre=None, x=None, *, w_post=None, gate=None, alph
     w_pre, w_post [d] float32.  h' goes to h_out (default: h itself when y is given), x is written
     when given."""
     what = "norm_residual"
-    if h.dim() != 2:
+    shape = h.shape
+    if len(shape) != 2:
         _refuse(what, "h is not [T][d]")
-    T, d = shape = h.shape
-    if h_out is None and y is not None:
-        h_out = h
-    ht = _type(what, "h", h)
-    hs, yt, ys, hos, xt, xs, gs, gc = _rows(what, "h", h, shape), 0, 0, 0, 0, 0, 0, 0
+    T, d = shape
+    dev = h.get_device()
+    hp, ht, hs = _matrix(what, "h", h, shape, dev)
+    yp = yt = ys = op = os_ = xp = xt = xs = gp = gs = gc = wo = wi = 0
     if y is not None:
-        yt, ys = _type(what, "y", y), _rows(what, "y", y, shape)
+        yp, yt, ys = _matrix(what, "y", y, shape, dev)
+        if h_out is None:
+            op, os_ = hp, hs
     if h_out is not None:
-        if h_out.dtype != h.dtype:
+        op, ot, os_ = _matrix(what, "h_out", h_out, shape, dev)
+        if ot != ht:
             _refuse(what, "h_out has another type than h")
-        hos = _rows(what, "h_out", h_out, shape)
     if x is not None:
-        xt, xs = _type(what, "x", x), _rows(what, "x", x, shape)
+        xp, xt, xs = _matrix(what, "x", x, shape, dev)
         if w_pre is None:
             _refuse(what, "x needs w_pre")
+    if w_pre is not None:
+        wi = _dense(what, "w_pre", w_pre, torch.float32, (d,), dev)
+    if w_post is not None:
+        wo = _dense(what, "w_post", w_post, torch.float32, (d,), dev)
     if gate is not None:
-        if (gate.dtype != torch.float32 or gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, d)
-                or (gate.shape[1] > 1 and gate.stride(1) != 1)):
-            _refuse(what, "gate is not float32 [T or 1][d or 1] with contiguous rows")
-        gs = gate.stride(0) if gate.shape[0] > 1 else 0
+        if gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, d):
+            _refuse(what, "gate is not [T or 1][d or 1]")
+        gp, gt, gs = _matrix(what, "gate", gate, gate.shape, dev)
+        if gt != F32:
+            _refuse(what, "gate is not float32")
+        if gate.shape[0] == 1:
+            gs = 0
         gc = gate.shape[1] > 1
-    wo = None if w_post is None else _dense(what, "w_post", w_post, torch.float32, (d,))
-    wi = None if w_pre is None else _dense(what, "w_pre", w_pre, torch.float32, (d,))
-    _launch(what, lib().bitsmoe_norm_residual, (h, y, w_post, gate, h_out, w_pre, x),
-            (T, d, h.data_ptr(), ht, hs, _ptr(y), yt, ys, wo, _ptr(gate), gs, gc, alpha, _ptr(h_out), hos, wi, _ptr(x), xt,
-             xs, eps), stream)
+    if dev < 0:
+        _refuse(what, "the tensors are not on one GPU")
+    _launch(what, lib().bitsmoe_norm_residual, dev, stream,
+            _NORM.pack(hp, yp, wo, gp, op, wi, xp, hs, ys, gs, os_, xs, T, d, ht, yt, xt, gc, alpha, eps))
 
 
 def topk_route_workspace_bytes(T: int, n_experts: int, top_k: int) -> int:
@@ -488,20 +505,26 @@ def topk_route(logits, topk_ids, gate_w, offsets=None, order=None, *, scoring: s
     into gate_w [T][top_k] float32; with offsets [E+1] and order [T*top_k] (int32) also the pairs
     t*top_k + slot grouped by expert."""
     what = "topk_route"
-    if logits.dim() != 2 or topk_ids.dim() != 2:
-        _refuse(what, "logits or topk_ids is not 2-D")
-    T, E = shape = logits.shape
-    K = topk_ids.shape[1]
-    if scoring not in SCORING:
+    shape, kshape = logits.shape, topk_ids.shape
+    if len(shape) != 2 or len(kshape) != 2 or kshape[0] != shape[0]:
+        _refuse(what, "logits or topk_ids is not [T][*]")
+    T, E = shape
+    K = kshape[1]
+    mode = SCORING.get(scoring)
+    if mode is None:
         _refuse(what, f"scoring {scoring!r} is neither softmax nor sigmoid")
-    lt, ls = _type(what, "logits", logits), _rows(what, "logits", logits, shape)
-    ids = _dense(what, "topk_ids", topk_ids, torch.int32, (T, K))
-    gw = _dense(what, "gate_w", gate_w, torch.float32, (T, K))
-    off = None if offsets is None else _dense(what, "offsets", offsets, torch.int32, (E + 1,))
-    od = None if order is None else _dense(what, "order", order, torch.int32, (T * K,))
-    _launch(what, lib().bitsmoe_topk_route, (logits, topk_ids, gate_w, offsets, order, workspace, status),
-            (logits.data_ptr(), lt, ls, T, E, K, SCORING[scoring], renormalise, scale, ids, gw, off, od, _ptr(workspace),
-             0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status)), stream)
+    dev = logits.get_device()
+    lp, lt, ls = _matrix(what, "logits", logits, shape, dev)
+    ids = _dense(what, "topk_ids", topk_ids, torch.int32, kshape, dev)
+    gw = _dense(what, "gate_w", gate_w, torch.float32, kshape, dev)
+    off = 0 if offsets is None else _dense(what, "offsets", offsets, torch.int32, (E + 1,), dev)
+    od = 0 if order is None else _dense(what, "order", order, torch.int32, (T * K,), dev)
+    ws = _extra(what, workspace, dev)
+    if dev < 0:
+        _refuse(what, "the tensors are not on one GPU")
+    _launch(what, lib().bitsmoe_topk_route, dev, stream,
+            _ROUTE.pack(lp, ids, gw, off, od, ws, _extra(what, status, dev), workspace.nbytes if ws else 0, ls, T, E, K, lt,
+                        mode, renormalise, scale, 0))
 
 
 def q4_bytes(n_experts: int, rows: int, cols: int, group: int) -> int:
@@ -511,16 +534,17 @@ def q4_bytes(n_experts: int, rows: int, cols: int, group: int) -> int:
 def q4_pack(W, group: int, blob, status=None, stream=None):
     """W [E][rows][cols] (float32, float16 or bfloat16) into 4 bits with a scale per `group` columns."""
     what = "q4_pack"
-    if W.dim() != 3 or not W.is_contiguous():
-        _refuse(what, "W is not a contiguous [E][rows][cols]")
+    if W.dim() != 3 or not W.is_contiguous() or W.dtype not in _TYPE:
+        _refuse(what, "W is not a contiguous float32, float16 or bfloat16 [E][rows][cols]")
     E, rows, cols = W.shape
     n = q4_bytes(E, rows, cols, group)
     if n == 0:
         _refuse(what, f"group {group} is not 32, 64 or 128, or W is empty")
     if blob.dtype != torch.uint8 or not blob.is_contiguous() or blob.numel() < n:
         raise BitsMoEError(ESIZE, f"{what}: blob is not {n} contiguous bytes")
-    _launch(what, lib().bitsmoe_q4_pack, (W, blob, status),
-            (W.data_ptr(), _type(what, "W", W), E, rows, cols, group, blob.data_ptr(), _ptr(status)), stream)
+    dev = _where(what, W)
+    _launch(what, lib().bitsmoe_q4_pack, dev, stream, W.data_ptr(), _TYPE[W.dtype], E, rows, cols, group,
+            _extra(what, blob, dev), _extra(what, status, dev))
 
 
 def q4_unpack(blob, group: int, W, stream=None):
@@ -529,11 +553,12 @@ def q4_unpack(blob, group: int, W, stream=None):
     if W.dim() != 3:
         _refuse(what, "W is not [E][rows][cols]")
     E, rows, cols = W.shape
-    wp = _dense(what, "W", W, torch.float32, (E, rows, cols))
     n = q4_bytes(E, rows, cols, group)
     if n == 0 or blob.numel() < n:
         raise BitsMoEError(ESIZE if n else EINVAL, f"{what}: blob of {blob.numel()} bytes, {n} needed")
-    _launch(what, lib().bitsmoe_q4_unpack, (blob, W), (blob.data_ptr(), E, rows, cols, group, wp), stream)
+    dev = _where(what, W)
+    wp = _dense(what, "W", W, torch.float32, (E, rows, cols), dev)
+    _launch(what, lib().bitsmoe_q4_unpack, dev, stream, _extra(what, blob, dev), E, rows, cols, group, wp)
 
 
 def ffn_down_q4_workspace_bytes(dims: FfnDims, group: int, T: int) -> int:
@@ -551,18 +576,22 @@ def ffn_down_q4(dims: FfnDims, blob, group: int, Y_gate, Y_up, topk_ids, gate_w,
                 workspace_bytes: int = 0, status=None, stream=None):
     """ffn_down with the down matrices in 4 bits (q4_pack).  Y_up None: h = Y_gate, no activation."""
     what = "ffn_down_q4"
-    K = dims.top_k
-    yg = _dense(what, "Y_gate", Y_gate, torch.float32, (T, K, dims.d_ff))
-    yu = None if Y_up is None else _dense(what, "Y_up", Y_up, torch.float32, (T, K, dims.d_ff))
-    ids = _dense(what, "topk_ids", topk_ids, torch.int32, (T, K))
-    gw = _dense(what, "gate_w", gate_w, torch.float32, (T, K))
-    op = _dense(what, "out", out, torch.float32, (T, dims.d_model))
-    n = q4_bytes(dims.n_experts, dims.d_model, dims.d_ff, group)
-    if n == 0 or blob.numel() < n:
-        raise BitsMoEError(ESIZE if n else EINVAL, f"{what}: blob of {blob.numel()} bytes, {n} needed")
-    _launch(what, lib().bitsmoe_ffn_down_q4, (blob, Y_gate, Y_up, topk_ids, gate_w, out, workspace, status),
-            (ctypes.byref(dims), blob.data_ptr(), group, yg, yu, ids, gw, T, op, _ptr(workspace), workspace_bytes,
-             _ptr(status)), stream)
+    d_model, d_ff, E, K = dims.d_model, dims.d_ff, dims.n_experts, dims.top_k
+    dev = blob.get_device()
+    shape = (T, K, d_ff)
+    yg = _dense(what, "Y_gate", Y_gate, torch.float32, shape, dev)
+    yu = 0 if Y_up is None else _dense(what, "Y_up", Y_up, torch.float32, shape, dev)
+    ids = _dense(what, "topk_ids", topk_ids, torch.int32, (T, K), dev)
+    gw = _dense(what, "gate_w", gate_w, torch.float32, (T, K), dev)
+    op = _dense(what, "out", out, torch.float32, (T, d_model), dev)
+    n = lib().bitsmoe_q4_bytes(E, d_model, d_ff, group)
+    if n == 0 or blob.nbytes < n:
+        raise BitsMoEError(ESIZE if n else EINVAL, f"{what}: blob of {blob.nbytes} bytes, {n} needed")
+    if dev < 0:
+        _refuse(what, "the tensors are not on one GPU")
+    _launch(what, lib().bitsmoe_ffn_down_q4, dev, stream,
+            _Q4.pack(d_model, d_ff, E, K, group, T, blob.data_ptr(), yg, yu, ids, gw, op, _extra(what, workspace, dev),
+                     _extra(what, status, dev), workspace_bytes))
 
 
 def grouped_matmul(A, W, offsets, out, *, W_up=None, rows=None, rows_per_a: int = 1, scatter: bool = False, status=None,
@@ -574,21 +603,26 @@ def grouped_matmul(A, W, offsets, out, *, W_up=None, rows=None, rows_per_a: int 
     a_i is row i of A, or with rows [n] int32 row rows[i] // rows_per_a; with scatter the result
     goes to row rows[i] of out."""
     what = "grouped_matmul"
-    if A.dim() != 2 or W.dim() != 3 or out.dim() != 2:
+    wshape, ashape, oshape = W.shape, A.shape, out.shape
+    if len(ashape) != 2 or len(wshape) != 3 or len(oshape) != 2:
         _refuse(what, "A, W and out are not [*][K], [E][N][K] and [n][N]")
-    E, N, K = W.shape
-    n = out.shape[0]
-    it, ot = _type(what, "A", A), _type(what, "out", out)
-    ap = A.data_ptr()
-    lda = _rows(what, "A", A, (A.shape[0], K)) if A.shape[0] > 1 else K
-    wp = _dense(what, "W", W, A.dtype, (E, N, K))
-    up = None if W_up is None else _dense(what, "W_up", W_up, A.dtype, (E, N, K))
-    op = _dense(what, "out", out, out.dtype, (n, N))
-    off = _dense(what, "offsets", offsets, torch.int32, (E + 1,))
-    rp = None if rows is None else _dense(what, "rows", rows, torch.int32, (n,))
-    dims = GmmDims(n, A.shape[0], N, K, E, it, ot)
-    _launch(what, lib().bitsmoe_grouped_matmul, (A, W, W_up, offsets, rows, out, status),
-            (ctypes.byref(dims), ap, lda, wp, up, off, rp, rows_per_a, scatter, op, _ptr(status)), stream)
+    E, N, K = wshape
+    n = oshape[0]
+    dev = A.get_device()
+    ap, it, lda = _matrix(what, "A", A, (ashape[0], K), dev)
+    if ashape[0] <= 1:
+        lda = K
+    wp = _dense(what, "W", W, A.dtype, wshape, dev)
+    up = 0 if W_up is None else _dense(what, "W_up", W_up, A.dtype, wshape, dev)
+    ot = _TYPE.get(out.dtype, -1)
+    op = _dense(what, "out", out, out.dtype, (n, N), dev)
+    off = _dense(what, "offsets", offsets, torch.int32, (E + 1,), dev)
+    rp = 0 if rows is None else _dense(what, "rows", rows, torch.int32, (n,), dev)
+    if dev < 0:
+        _refuse(what, "the tensors are not on one GPU")
+    _launch(what, lib().bitsmoe_grouped_matmul, dev, stream,
+            _GMM.pack(ap, wp, up, off, rp, op, _extra(what, status, dev), lda, n, ashape[0], N, K, E, it, ot, rows_per_a,
+                      scatter, 0))
 
 
 def read_status(status, stream=None) -> int:

@@ -99,6 +99,31 @@ __device__ __forceinline__ int cta_scan(int v, int* s_warp) {
     return v;
 }
 
+// A bounded wait of a whole warp on an mbarrier phase; every lane gets the same answer.
+// The clock is read once in 64 tries.
+constexpr long long kWarpWaitNs = 2000000000LL;  // 2 s, then BITSMOE_ST_TIMEOUT
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    long long t0 = 0;
+    for (int i = 1;; i++) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (i % 64 == 0) {
+            long long t;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+            t = __shfl_sync(0xffffffffu, t, 0);
+            if (t0 == 0)
+                t0 = t;
+            else if (t - t0 > kWarpWaitNs)
+                return false;
+        }
+    }
+}
+
 // Programmatic dependent launch: the wait returns when every kernel before this one
 // in the stream has finished and its writes are visible; the trigger lets the next
 // kernel (if it was launched the same way) start its own pre-wait part.

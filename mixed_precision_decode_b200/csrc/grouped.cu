@@ -82,12 +82,12 @@ template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     if constexpr (BF16)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -272,29 +272,6 @@ struct GmmTcParams {
     int vec;          // rows of out are whole 16-byte pieces
 };
 
-// A bounded wait of a whole warp; every lane gets the same answer.  The clock is read
-// once in 64 tries.
-__device__ __forceinline__ bool gt_wait(uint32_t bar, uint32_t parity) {
-    long long t0 = 0;
-    for (int i = 1;; i++) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (__all_sync(0xffffffffu, ok)) return true;
-        if (i % 64 == 0) {
-            long long t;
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-            t = __shfl_sync(0xffffffffu, t, 0);
-            if (t0 == 0)
-                t0 = t;
-            else if (t - t0 > kTcWaitNs)
-                return false;
-        }
-    }
-}
 // True in one lane of a converged warp.  The warp-wide roles below run their loops in
 // every lane and issue under this: ptxas then knows that one thread executes the TMA and
 // MMA instructions, whose operands are warp-uniform registers, and need not serialise
@@ -461,7 +438,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
             const CUtensorMap* tmA = &M.a[bi];
             const uint32_t bytes = 2u * (NW * kGtAStage + (GATHER ? 0u : 128u * (uint32_t)gt_box(bi)));
             for (int k = 0; k < Q.nst; k++) {
-                ok = gt_wait(tc_smem(&s_empty[s]), phase);
+                ok = warp_wait(tc_smem(&s_empty[s]), phase);
                 if (!ok) break;
                 if (gt_elect()) {
                     const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes, bar = full0 + 8u * (uint32_t)s;
@@ -490,11 +467,11 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
                 const GtTile t = gt_tile(Q, s_tab, item);
                 const uint32_t idesc = tc_idesc(2 * kGtM, t.n_mma) | (P.type == BITSMOE_BF16 ? (1u << 7) | (1u << 10) : 0u);
                 const uint32_t d = tmem + 256u * buf;
-                ok = gt_wait(tc_smem(&s_aempty[buf]), aphase);
+                ok = warp_wait(tc_smem(&s_aempty[buf]), aphase);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 for (int k = 0; k < Q.nst; k++) {
-                    ok = gt_wait(tc_smem(&s_full[s]), phase);
+                    ok = warp_wait(tc_smem(&s_full[s]), phase);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     if (gt_elect()) {
@@ -535,7 +512,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
                 dst_of[j] = row_pair(P, t.i0 + j, src, dst) ? (int)dst : -1;
             }
             __syncwarp();
-            if (!gt_wait(tc_smem(&s_afull[buf]), (uint32_t)(n >> 1) & 1u)) {
+            if (!warp_wait(tc_smem(&s_afull[buf]), (uint32_t)(n >> 1) & 1u)) {
                 *fail = 1;
                 break;
             }
@@ -608,7 +585,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
         bool ok = true;
         for (int item = first; item < total && ok; item += step)
             for (int k = 0; k < Q.nst; k++) {
-                ok = gt_wait(tc_smem(&s_rows[s]), phase);
+                ok = warp_wait(tc_smem(&s_rows[s]), phase);
                 if (!ok) break;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 if (gt_elect()) gt_arrive_cluster(full0 + 8u * (uint32_t)s);
@@ -638,7 +615,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
                 src_row[i] = r < half && j < t.cnt && row_pair(P, t.i0 + j, src, dst) ? P.a + src * P.lda + 8 * ch : nullptr;
             }
             for (int k = 0; k < Q.nst; k++) {
-                ok = gt_wait(tc_smem(&s_empty[s]), phase);
+                ok = warp_wait(tc_smem(&s_empty[s]), phase);
                 if (!ok) break;
                 const uint32_t b = b0 + (uint32_t)s * Q.stage_bytes;
                 const bool in_k = k * kGtK + 8 * ch < P.D;
@@ -719,45 +696,43 @@ static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
 
 using namespace bitsmoe;
 
-BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_dims* dims, const void* A, int64_t a_stride, const void* W,
-                                       const void* W_up, const int32_t* offsets, const int32_t* rows,
-                                       int32_t rows_per_a, int32_t scatter, void* out, int32_t* status, void* stream) {
-    if (!dims) return BITSMOE_EINVAL;
-    const bitsmoe_gmm_dims& d = *dims;
+BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* stream) {
+    if (!args) return BITSMOE_EINVAL;
+    const bitsmoe_gmm_args& d = *args;
     if (d.n_rows < 0 || d.n_a_rows < 0 || d.n_out < 1 || d.n_in < 8 || d.n_in % 8 || d.n_experts < 1 ||
         d.n_experts > BITSMOE_GMM_MAX_EXPERTS || (d.in_type != BITSMOE_F16 && d.in_type != BITSMOE_BF16) ||
-        (d.out_type != BITSMOE_F32 && d.out_type != d.in_type) || rows_per_a < 1 ||
+        (d.out_type != BITSMOE_F32 && d.out_type != d.in_type) || d.rows_per_a < 1 || d.reserved ||
         (int64_t)d.n_experts * d.n_out > 0x7fffffff)
         return BITSMOE_EINVAL;
-    if (!rows && (scatter || rows_per_a != 1 || d.n_a_rows < d.n_rows)) return BITSMOE_EINVAL;
+    if (!d.rows && (d.scatter || d.rows_per_a != 1 || d.n_a_rows < d.n_rows)) return BITSMOE_EINVAL;
     if (d.n_rows == 0) return BITSMOE_OK;
-    if (!A || !W || !offsets || !out || a_stride < d.n_in || a_stride % 8) return BITSMOE_EINVAL;
-    if ((uintptr_t)A % 16 || (uintptr_t)W % 16 || (uintptr_t)W_up % 16 || (uintptr_t)offsets % 4 || (uintptr_t)rows % 4 ||
-        (uintptr_t)out % 4)
+    if (!d.A || !d.W || !d.offsets || !d.out || d.a_stride < d.n_in || d.a_stride % 8) return BITSMOE_EINVAL;
+    if ((uintptr_t)d.A % 16 || (uintptr_t)d.W % 16 || (uintptr_t)d.W_up % 16 || (uintptr_t)d.offsets % 4 ||
+        (uintptr_t)d.rows % 4 || (uintptr_t)d.out % elem_bytes(d.out_type))
         return BITSMOE_EINVAL;
     GmmParams P{};
-    P.a = (const uint16_t*)A;
-    P.w = (const uint16_t*)W;
-    P.w_up = (const uint16_t*)W_up;
-    P.offsets = offsets;
-    P.rows = rows;
-    P.out = out;
-    P.status = status;
-    P.lda = a_stride;
+    P.a = (const uint16_t*)d.A;
+    P.w = (const uint16_t*)d.W;
+    P.w_up = (const uint16_t*)d.W_up;
+    P.offsets = d.offsets;
+    P.rows = d.rows;
+    P.out = d.out;
+    P.status = d.status;
+    P.lda = d.a_stride;
     P.P = d.n_rows;
     P.N = d.n_out;
     P.D = d.n_in;
     P.E = d.n_experts;
     P.n_a = d.n_a_rows;
-    P.div = rows_per_a;
+    P.div = d.rows_per_a;
     P.type = d.in_type;
     P.out_type = d.out_type;
-    P.scatter = scatter != 0;
+    P.scatter = d.scatter != 0;
     cudaStream_t s = (cudaStream_t)stream;
     if (d.n_rows > kGmmTcRows * (int64_t)d.n_experts) {
-        if (rows) return W_up ? launch_gmm_tc<true, true>(P, s) : launch_gmm_tc<false, true>(P, s);
-        return W_up ? launch_gmm_tc<true, false>(P, s) : launch_gmm_tc<false, false>(P, s);
+        if (d.rows) return d.W_up ? launch_gmm_tc<true, true>(P, s) : launch_gmm_tc<false, true>(P, s);
+        return d.W_up ? launch_gmm_tc<true, false>(P, s) : launch_gmm_tc<false, false>(P, s);
     }
-    if (d.in_type == BITSMOE_BF16) return W_up ? launch_gmm_mv<true, true>(P, s) : launch_gmm_mv<true, false>(P, s);
-    return W_up ? launch_gmm_mv<false, true>(P, s) : launch_gmm_mv<false, false>(P, s);
+    if (d.in_type == BITSMOE_BF16) return d.W_up ? launch_gmm_mv<true, true>(P, s) : launch_gmm_mv<true, false>(P, s);
+    return d.W_up ? launch_gmm_mv<false, true>(P, s) : launch_gmm_mv<false, false>(P, s);
 }

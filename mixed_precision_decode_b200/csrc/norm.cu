@@ -221,49 +221,51 @@ static int launch_norm(const NormParams& P, cudaStream_t s) {
 
 using namespace bitsmoe;
 
-BITSMOE_API int bitsmoe_norm_residual(int32_t T, int32_t d, const void* h, int32_t h_type, int64_t h_stride,
-                                      const void* y, int32_t y_type, int64_t y_stride, const float* w_post,
-                                      const float* gate, int64_t gate_stride, int32_t gate_per_channel, float alpha,
-                                      void* h_out, int64_t h_out_stride, const float* w_pre, void* x, int32_t x_type,
-                                      int64_t x_stride, float eps, void* stream) {
-    if (T < 0 || d < 1 || !elem_ok(h_type) || (y && !elem_ok(y_type)) || (x && !elem_ok(x_type))) return BITSMOE_EINVAL;
-    if (T == 0) return BITSMOE_OK;
-    if (!h || (!h_out && !x) || (x && !w_pre) || (!y && (w_post || gate))) return BITSMOE_EINVAL;
-    if (h_stride < 0 || (y && y_stride < 0) || gate_stride < 0 || !(eps >= 0.0f)) return BITSMOE_EINVAL;
-    // rows that are written must not overlap, and a row of h is read before its place is written
-    if (T > 1 && ((h_out && h_out_stride < d) || (x && x_stride < d) || (h_out == h && h_out_stride != h_stride)))
+BITSMOE_API int bitsmoe_norm_residual(const bitsmoe_norm_args* args, void* stream) {
+    if (!args) return BITSMOE_EINVAL;
+    const bitsmoe_norm_args& a = *args;
+    if (a.rows < 0 || a.d < 1 || !elem_ok(a.h_type) || (a.y && !elem_ok(a.y_type)) || (a.x && !elem_ok(a.x_type)))
         return BITSMOE_EINVAL;
-    const int hb = elem_bytes(h_type);
-    if ((uintptr_t)h % hb || (uintptr_t)h_out % hb || (y && (uintptr_t)y % elem_bytes(y_type)) ||
-        (x && (uintptr_t)x % elem_bytes(x_type)) || (uintptr_t)w_post % 4 || (uintptr_t)gate % 4 || (uintptr_t)w_pre % 4)
+    if (a.rows == 0) return BITSMOE_OK;
+    if (!a.h || (!a.h_out && !a.x) || (a.x && !a.w_pre) || (!a.y && (a.w_post || a.gate))) return BITSMOE_EINVAL;
+    if (a.h_stride < 0 || (a.y && a.y_stride < 0) || a.gate_stride < 0 || !(a.eps >= 0.0f)) return BITSMOE_EINVAL;
+    // rows that are written must not overlap, and a row of h is read before its place is written
+    if (a.rows > 1 && ((a.h_out && a.h_out_stride < a.d) || (a.x && a.x_stride < a.d) ||
+                       (a.h_out == a.h && a.h_out_stride != a.h_stride)))
+        return BITSMOE_EINVAL;
+    const int hb = elem_bytes(a.h_type);
+    if ((uintptr_t)a.h % hb || (uintptr_t)a.h_out % hb || (a.y && (uintptr_t)a.y % elem_bytes(a.y_type)) ||
+        (a.x && (uintptr_t)a.x % elem_bytes(a.x_type)) || (uintptr_t)a.w_post % 4 || (uintptr_t)a.gate % 4 ||
+        (uintptr_t)a.w_pre % 4)
         return BITSMOE_EINVAL;
     NormParams P{};
-    P.h = h;
-    P.y = y;
-    P.w_post = w_post;
-    P.gate = gate;
-    P.w_pre = w_pre;
-    P.h_out = h_out;
-    P.x = x;
-    P.h_ld = h_stride;
-    P.y_ld = y_stride;
-    P.ho_ld = h_out_stride;
-    P.x_ld = x_stride;
-    P.gate_t = gate_stride;
-    P.gate_i = gate_per_channel ? 1 : 0;
-    P.T = T;
-    P.d = d;
-    P.h_type = h_type;
-    P.y_type = y_type;
-    P.x_type = x_type;
-    P.alpha = alpha;
-    P.eps = eps;
+    P.h = a.h;
+    P.y = a.y;
+    P.w_post = a.w_post;
+    P.gate = a.gate;
+    P.w_pre = a.w_pre;
+    P.h_out = a.h_out;
+    P.x = a.x;
+    P.h_ld = a.h_stride;
+    P.y_ld = a.y_stride;
+    P.ho_ld = a.h_out_stride;
+    P.x_ld = a.x_stride;
+    P.gate_t = a.gate_stride;
+    P.gate_i = a.gate_per_channel ? 1 : 0;
+    P.T = a.rows;
+    P.d = a.d;
+    P.h_type = a.h_type;
+    P.y_type = a.y_type;
+    P.x_type = a.x_type;
+    P.alpha = a.alpha;
+    P.eps = a.eps;
     // 16-byte accesses where every row of every buffer starts on a 16-byte boundary
     auto vec = [](const void* p, int type, int64_t ld) {
         return !p || ((uintptr_t)p % 16 == 0 && (ld * elem_bytes(type)) % 16 == 0);
     };
-    const bool v8 = d % 8 == 0 && vec(h, h_type, h_stride) && vec(y, y_type, y_stride) &&
-                    vec(h_out, h_type, h_out_stride) && vec(x, x_type, x_stride) && vec(w_post, BITSMOE_F32, 0) &&
-                    vec(w_pre, BITSMOE_F32, 0) && (!gate_per_channel || vec(gate, BITSMOE_F32, gate_stride));
+    const bool v8 = a.d % 8 == 0 && vec(a.h, a.h_type, a.h_stride) && vec(a.y, a.y_type, a.y_stride) &&
+                    vec(a.h_out, a.h_type, a.h_out_stride) && vec(a.x, a.x_type, a.x_stride) &&
+                    vec(a.w_post, BITSMOE_F32, 0) && vec(a.w_pre, BITSMOE_F32, 0) &&
+                    (!a.gate_per_channel || vec(a.gate, BITSMOE_F32, a.gate_stride));
     return v8 ? launch_norm<8>(P, (cudaStream_t)stream) : launch_norm<1>(P, (cudaStream_t)stream);
 }

@@ -928,28 +928,29 @@ BITSMOE_API int bitsmoe_ffn_down_q4_launches(const bitsmoe_ffn_dims* dims, int32
     return T == 0 ? 0 : q4_single(dims, group, T) ? 1 : 3;
 }
 
-BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_ffn_dims* dims, const void* blob, int32_t group, const float* Y_gate,
-                                    const float* Y_up, const int32_t* topk_ids, const float* gate_w, int32_t T,
-                                    float* out, void* workspace, uint64_t workspace_bytes, int32_t* status,
-                                    void* stream) {
+BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_q4_args* args, void* stream) {
+    if (!args) return BITSMOE_EINVAL;
+    const bitsmoe_q4_args& a = *args;
+    const bitsmoe_ffn_dims* dims = &a.dims;
+    const int group = a.group, T = a.tokens;
     if (!q4_dims_ok(dims, group, T)) return BITSMOE_EINVAL;
     if (T == 0) return BITSMOE_OK;
-    if (!blob || !Y_gate || !topk_ids || !gate_w || !out) return BITSMOE_EINVAL;
-    if ((uintptr_t)blob % 16 || (uintptr_t)Y_gate % 16 || (uintptr_t)Y_up % 16 || (uintptr_t)out % 4 ||
-        (uintptr_t)topk_ids % 4 || (uintptr_t)gate_w % 4)
+    if (!a.blob || !a.Y_gate || !a.topk_ids || !a.gate_w || !a.out) return BITSMOE_EINVAL;
+    if ((uintptr_t)a.blob % 16 || (uintptr_t)a.Y_gate % 16 || (uintptr_t)a.Y_up % 16 || (uintptr_t)a.out % 4 ||
+        (uintptr_t)a.topk_ids % 4 || (uintptr_t)a.gate_w % 4)
         return BITSMOE_EINVAL;
     const uint64_t need = bitsmoe_ffn_down_q4_workspace_bytes(dims, group, T);
-    if (need > 0 && (!workspace || (uintptr_t)workspace % 256)) return BITSMOE_EINVAL;
-    if (workspace_bytes < need) return BITSMOE_ESIZE;
+    if (need > 0 && (!a.workspace || (uintptr_t)a.workspace % 256)) return BITSMOE_EINVAL;
+    if (a.workspace_bytes < need) return BITSMOE_ESIZE;
     cudaStream_t s = (cudaStream_t)stream;
     Q4Params P{};
-    P.M = q4_matrix(blob, dims->d_model, dims->d_ff, group);
-    P.yg = Y_gate;
-    P.yu = Y_up;
-    P.ids = topk_ids;
-    P.gw = gate_w;
-    P.out = out;
-    P.status = status;
+    P.M = q4_matrix(a.blob, dims->d_model, dims->d_ff, group);
+    P.yg = a.Y_gate;
+    P.yu = a.Y_up;
+    P.ids = a.topk_ids;
+    P.gw = a.gate_w;
+    P.out = a.out;
+    P.status = a.status;
     P.E = dims->n_experts;
     P.K = dims->top_k;
     P.T = T;
@@ -958,7 +959,7 @@ BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_ffn_dims* dims, const void* bl
         const size_t smem = q4_t1_smem(dims, group, kQ4Sms);
         return group == 32 ? launch_q4_t1<32>(P, smem, s) : group == 64 ? launch_q4_t1<64>(P, smem, s) : launch_q4_t1<128>(P, smem, s);
     }
-    const Q4WS w = q4_ws(dims, group, T, (uint8_t*)workspace);
+    const Q4WS w = q4_ws(dims, group, T, (uint8_t*)a.workspace);
     P.order = w.order;
     P.pieces = w.pieces;
     P.hb = w.hb;

@@ -324,42 +324,42 @@ BITSMOE_API uint64_t bitsmoe_topk_route_workspace_bytes(int32_t T, int32_t n_exp
     return nb == 1 ? 0 : 4ull * nb * n_experts;
 }
 
-BITSMOE_API int bitsmoe_topk_route(const void* logits, int32_t logits_type, int64_t logits_stride, int32_t T,
-                                   int32_t n_experts, int32_t top_k, int32_t scoring, int32_t renormalise, float scale,
-                                   int32_t* topk_ids, float* gate_w, int32_t* offsets, int32_t* order, void* workspace,
-                                   uint64_t workspace_bytes, int32_t* status, void* stream) {
+BITSMOE_API int bitsmoe_topk_route(const bitsmoe_route_args* args, void* stream) {
+    if (!args) return BITSMOE_EINVAL;
+    const bitsmoe_route_args& a = *args;
+    const int T = a.tokens, n_experts = a.n_experts, top_k = a.top_k;
     if (T < 0 || n_experts < 1 || n_experts > kRouteMaxE || top_k < 1 || top_k > n_experts || top_k > kRouteMaxK ||
-        !elem_ok(logits_type) || (scoring != BITSMOE_SCORE_SOFTMAX && scoring != BITSMOE_SCORE_SIGMOID) ||
-        (int64_t)T * top_k > 0x7fffffff)
+        !elem_ok(a.logits_type) || (a.scoring != BITSMOE_SCORE_SOFTMAX && a.scoring != BITSMOE_SCORE_SIGMOID) ||
+        (int64_t)T * top_k > 0x7fffffff || a.reserved)
         return BITSMOE_EINVAL;
-    if (T == 0 && !offsets) return BITSMOE_OK;
-    if (T > 0 && (!logits || !topk_ids || !gate_w || logits_stride < 0)) return BITSMOE_EINVAL;
-    if ((uintptr_t)logits % elem_bytes(logits_type) || (uintptr_t)topk_ids % 4 || (uintptr_t)gate_w % 4 ||
-        (uintptr_t)offsets % 4 || (uintptr_t)order % 4)
+    if (T == 0 && !a.offsets) return BITSMOE_OK;
+    if (T > 0 && (!a.logits || !a.topk_ids || !a.gate_w || a.logits_stride < 0)) return BITSMOE_EINVAL;
+    if ((uintptr_t)a.logits % elem_bytes(a.logits_type) || (uintptr_t)a.topk_ids % 4 || (uintptr_t)a.gate_w % 4 ||
+        (uintptr_t)a.offsets % 4 || (uintptr_t)a.order % 4)
         return BITSMOE_EINVAL;
     const int nb = T == 0 ? 1 : route_blocks(T);
-    const bool groups = offsets || order;
+    const bool groups = a.offsets || a.order;
     if (groups && nb > 1) {
-        if (!workspace || (uintptr_t)workspace % 256) return BITSMOE_EINVAL;
-        if (workspace_bytes < bitsmoe_topk_route_workspace_bytes(T, n_experts, top_k)) return BITSMOE_ESIZE;
+        if (!a.workspace || (uintptr_t)a.workspace % 256) return BITSMOE_EINVAL;
+        if (a.workspace_bytes < bitsmoe_topk_route_workspace_bytes(T, n_experts, top_k)) return BITSMOE_ESIZE;
     }
     cudaStream_t s = (cudaStream_t)stream;
     RouteParams P{};
-    P.logits = logits;
-    P.ld = logits_stride;
-    P.type = logits_type;
+    P.logits = a.logits;
+    P.ld = a.logits_stride;
+    P.type = a.logits_type;
     P.T = T;
     P.E = n_experts;
     P.K = top_k;
-    P.sigmoid = scoring == BITSMOE_SCORE_SIGMOID;
-    P.renorm = renormalise != 0;
-    P.scale = scale;
-    P.ids = topk_ids;
-    P.gw = gate_w;
-    P.offsets = offsets;
-    P.order = order;
-    P.hist = groups && nb > 1 ? (int32_t*)workspace : nullptr;
-    P.status = status;
+    P.sigmoid = a.scoring == BITSMOE_SCORE_SIGMOID;
+    P.renorm = a.renormalise != 0;
+    P.scale = a.scale;
+    P.ids = a.topk_ids;
+    P.gw = a.gate_w;
+    P.offsets = a.offsets;
+    P.order = a.order;
+    P.hist = groups && nb > 1 ? (int32_t*)a.workspace : nullptr;
+    P.status = a.status;
     P.tpb = (T + nb - 1) / nb;
     P.nw = std::max(1, std::min(kRtWarps, kRouteHistInts / n_experts));
     const unsigned grid = T == 0 ? 1u : (unsigned)((T + P.tpb - 1) / P.tpb);

@@ -73,6 +73,10 @@ __device__ __forceinline__ void store_elems(void* p, int type, int64_t i, const 
     }
 }
 
+// SiLU.  The approximate division (2 units of the last place) has no branch; its denominator is
+// at least 1, and it gives 0 where that leaves the range (v below about -88).
+__device__ __forceinline__ float silu_f(float v) { return __fdividef(v, 1.0f + expf(-v)); }
+
 // Inclusive scan over a CTA of THREADS threads, one value each; s_warp [32].
 template <int THREADS>
 __device__ __forceinline__ int cta_scan(int v, int* s_warp) {

@@ -49,10 +49,6 @@ __device__ __forceinline__ bool row_pair(const GmmParams& P, int i, int64_t& src
     return true;
 }
 
-// The approximate division (2 units of the last place) has no branch; its denominator is
-// at least 1, and it gives 0 where that leaves the range (v below about -88).
-__device__ __forceinline__ float silu_f(float v) { return __fdividef(v, 1.0f + expf(-v)); }
-
 // ---------------------------------------------------------------------------
 // few rows per expert
 // ---------------------------------------------------------------------------

@@ -182,7 +182,7 @@ __device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t& a0, uint32_t& a1)
 }
 
 __device__ __forceinline__ void q4_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -190,7 +190,7 @@ __device__ __forceinline__ void q4_mma(float (&c)[4], const uint32_t (&a)[4], ui
 
 // The same from c = (start, 0, start, 0).
 __device__ __forceinline__ void q4_mma_start(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float start) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(start), "f"(0.0f));
@@ -203,7 +203,7 @@ __device__ __forceinline__ void q4_h8(const float* yg, const float* yu, int64_t 
     float u[8];
     load_elems<8>(yu, BITSMOE_F32, i, u);
 #pragma unroll
-    for (int j = 0; j < 8; j++) h[j] = h[j] / (1.0f + expf(-h[j])) * u[j];
+    for (int j = 0; j < 8; j++) h[j] = silu_f(h[j]) * u[j];
 }
 
 // Power of two that brings values of magnitude up to m into [2^14, 2^15) (1 for 0 or
@@ -423,20 +423,31 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
             if (batches) tiles.load(codes, scales);
             const int64_t hrow = (int64_t)j * P.M.cols;
             const int c1 = min(8 * t1, P.M.cols / 8);
+            constexpr int KEEP = 2;  // chunks of 8 columns a lane keeps between the two passes
+            float kept[KEEP][8];
             float m = 0.0f;
-            for (int ch = 8 * t0 + lane; ch < c1; ch += 32) {
+            auto h_of = [&](int ch, float(&h)[8]) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) h[i] = 0.0f;
+                if (ch < c1) q4_h8(P.yg, P.yu, hrow + 8 * ch, h);
+            };
+#pragma unroll
+            for (int k = 0; k < KEEP; k++) h_of(8 * t0 + lane + 32 * k, kept[k]);
+#pragma unroll
+            for (int k = 0; k < KEEP; k++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(kept[k][i]));
+            for (int ch = 8 * t0 + lane + 32 * KEEP; ch < c1; ch += 32) {
                 float h[8];
-                q4_h8(P.yg, P.yu, hrow + 8 * ch, h);
+                h_of(ch, h);
 #pragma unroll
                 for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(h[i]));
             }
             scale = q4_h_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
             const float inv = 1.0f / scale;
             // whole warps: a group's chunks sit in neighbouring lanes
-            for (int ch = 8 * t0 + lane; ch - lane < 8 * t1; ch += 32) {
-                float h[8] = {};
+            auto put = [&](int ch, const float(&h)[8]) {
                 uint32_t hi[4], lo[4];
-                if (ch < c1) q4_h8(P.yg, P.yu, hrow + 8 * ch, h);
 #pragma unroll
                 for (int i = 0; i < 4; i++) q4_split(h[2 * i] * inv, h[2 * i + 1] * inv, hi[i], lo[i]);
                 const float sum = q4_group_half<G>(hi, lo);
@@ -449,6 +460,14 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
                     }
                     if (ch % (G / 8) == 0) s_sum[j * ngroups + ch / (G / 8)] = sum;
                 }
+            };
+#pragma unroll
+            for (int k = 0; k < KEEP; k++)
+                if (8 * t0 + 32 * k < 8 * t1) put(8 * t0 + lane + 32 * k, kept[k]);
+            for (int c0 = 8 * t0 + 32 * KEEP; c0 < 8 * t1; c0 += 32) {
+                float h[8];
+                h_of(c0 + lane, h);
+                put(c0 + lane, h);
             }
             __syncwarp();
         }

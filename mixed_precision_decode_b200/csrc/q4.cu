@@ -14,12 +14,14 @@
 // its A operand, so a lane's 32 codes of a tile are one 16-byte load and no code
 // moves between lanes; then the group scales.
 //
-// Arithmetic: q - 8 is exact in fp16, two codes by one mask and one addition (from the
-// bit pattern 0x6400 | q = 1024 + q) or fused multiply-add (0x6400 | 16 q = 1024 + 16 q).
-// h is split into an fp16 high part and the fp16 rest after a power-of-two scaling into
-// fp16's range; the two are two columns of the B operand, so a product keeps fp32's
-// precision.  A group's fp32 sum starts from half the sum of its h, which makes its
-// codes q - 7.5, and is multiplied by its scale in fp32.
+// Arithmetic: integer products, exact.  h is taken as a 32-bit fixed-point number relative
+// to a power of two above the row's largest |h| (an error of 2^-32 of that) and cut into
+// four signed digits of 8 bits, which are four columns of the B operand of mma.sync
+// m16n8k32 (u8 x s8, 32-bit sums); the codes are its u8 operand after one mask, or a
+// shift and a mask, per four of them.  Two digits' sums over a group are one integer,
+// which becomes fp32, takes its share of -7.5 sum h, and is multiplied by the group's
+// scale.  With fp16 operands (two columns a row of h) the conversion of the codes alone
+// took 36 instructions a tile, most of them at half rate, and the step 1.6 times as long.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -169,31 +171,15 @@ __global__ void k_q4_unpack(const Q4Matrix M, int64_t n, float* __restrict__ out
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
-// Two registers of the A operand of a k step: q - 8 in fp16, exact, of the nibbles at
-// bits 0 and 16 and at bits 4 and 20.
-__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t& a0, uint32_t& a1) {
-    const uint32_t l = (w & 0x000f000fu) | 0x64006400u, h = (w & 0x00f000f0u) | 0x64006400u;
-    const __half2 m1032 = __half2half2(__ushort_as_half(0xe408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
-                  m72 = __half2half2(__ushort_as_half(0xd480));
-    const __half2 lo = __hadd2(*reinterpret_cast<const __half2*>(&l), m1032);
-    const __half2 hi = __hfma2(*reinterpret_cast<const __half2*>(&h), sixteenth, m72);
-    a0 = *reinterpret_cast<const uint32_t*>(&lo);
-    a1 = *reinterpret_cast<const uint32_t*>(&hi);
-}
-
-__device__ __forceinline__ void q4_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+__device__ __forceinline__ void q4_mma(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// The same from c = (start, 0, start, 0).
-__device__ __forceinline__ void q4_mma_start(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float start) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(start), "f"(0.0f));
+__device__ __forceinline__ void q4_mma_zero(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
 }
 
 // SiLU(yg) * yu of 8 values (yu NULL: yg itself).
@@ -206,24 +192,60 @@ __device__ __forceinline__ void q4_h8(const float* yg, const float* yu, int64_t 
     for (int j = 0; j < 8; j++) h[j] = silu_f(h[j]) * u[j];
 }
 
-// Power of two that brings values of magnitude up to m into [2^14, 2^15) (1 for 0 or
-// a non-finite m), kept where its reciprocal is finite.
-__device__ __forceinline__ float q4_h_scale(float m) {
-    return m > 0.0f && m <= 3.0e38f ? ldexpf(1.0f, max(ilogbf(m) - 14, -100)) : 1.0f;
+// The exponent e of a power of two above a row's largest |h| (m): |h| 2^(30 - e) < 2^30.
+// (A row below 2^-95 keeps fewer bits: its unit is 2^-125.)
+// m holds the bits of the largest |h|, so a NaN counts as larger than all.
+__device__ __forceinline__ int q4_exponent(float m) {
+    const int e = (int)(__float_as_uint(m) >> 23) - 126;
+    return e > 128 ? 0 : max(e, -95);
 }
+__device__ __forceinline__ float q4_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// hi + lo = v, both fp16, for two neighbouring values.
-__device__ __forceinline__ void q4_split(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-    const __half a0 = __float2half_rn(v0), a1 = __float2half_rn(v1);
-    const __half b0 = __float2half_rn(v0 - __half2float(a0)), b1 = __float2half_rn(v1 - __half2float(a1));
-    hi = (uint32_t)__half_as_ushort(a0) | ((uint32_t)__half_as_ushort(a1) << 16);
-    lo = (uint32_t)__half_as_ushort(b0) | ((uint32_t)__half_as_ushort(b1) << 16);
+// The value of the fixed-point unit 2^(e - 30); a row with a NaN or an infinity gets NaN,
+// and so do its results.
+__device__ __forceinline__ float q4_unit(float m, int e) { return m <= 3.4028235e38f ? q4_pow2(e - 30) : NAN; }
+
+// 16 neighbouring columns of h as digits: out[d][c] is word c of digit d (0: the most
+// significant) of the half step they are, bytes in the order of the codes' bytes -- columns
+// 2c, 2c + 8, 2c + 1, 2c + 9; hi, lo: the sums of digits 0 and 1 and of digits 2 and 3 as
+// numbers of 16 bits.  v = round(h 2^(30 - e)) = 2^16 hi + lo per column, digits signed: adding
+// 128 to a byte and flipping its top bit subtracts it again.
+__device__ __forceinline__ void q4_digits(const float (&h)[16], float to_fixed, uint32_t (&out)[4][4], int& hi, int& lo) {
+    uint32_t w[16];
+    hi = lo = 0;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const int v = __float2int_rn(h[i] * to_fixed);
+        const int top = (v + 0x8080) >> 16;
+        hi += top;
+        lo += v - (top << 16);
+        w[i] = ((uint32_t)v + 0x00808080u) ^ 0x00808080u;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; c++) {  // 4 x 4 bytes transposed
+        const uint32_t a = w[2 * c], b = w[2 * c + 8], e = w[2 * c + 1], f = w[2 * c + 9];
+        const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
+        const uint32_t ef0 = __byte_perm(e, f, 0x5140), ef1 = __byte_perm(e, f, 0x7362);
+        out[3][c] = __byte_perm(ab0, ef0, 0x5410);
+        out[2][c] = __byte_perm(ab0, ef0, 0x7632);
+        out[1][c] = __byte_perm(ab1, ef1, 0x5410);
+        out[0][c] = __byte_perm(ab1, ef1, 0x7632);
+    }
 }
-
-// The B operand of a 64-column tile for one column (the high or the low part of a
-// row of h): lane column c reads words [c][t][u] (u = 0: k = 16t + 2c + {0, 1}, u = 1:
-// 8 more), 32 bytes.  Word of the pair of columns (k, k + 1), k even, inside the tile:
-__host__ __device__ constexpr int q4_b_word(int k) { return (k % 8) / 2 * 8 + k / 16 * 2 + k % 16 / 8; }
+// The sums of hi and lo over a group of G columns, from its chunks of 16 in neighbouring lanes.
+template <int G>
+__device__ __forceinline__ void q4_group_sums(int& hi, int& lo) {
+#pragma unroll
+    for (int o = 1; o < G / 16; o <<= 1) {
+        hi += __shfl_xor_sync(0xffffffffu, hi, o);
+        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+    }
+}
+// The B operand of a tile for one column (a digit of a row of h): word [c][t] at 4 c + t is
+// the half step t (16 columns) of lane column c.  A row of h has [tile][digit][16] words.
+constexpr int kQ4BTile = 64;  // words of a row per tile
+// Where chunk ch (16 columns) of a row puts digit d of lane column c.
+__device__ __forceinline__ int q4_b_at(int ch, int d, int c) { return ch / 4 * kQ4BTile + 16 * d + 4 * c + ch % 4; }
 
 struct Q4Params {
     Q4Matrix M;
@@ -233,16 +255,20 @@ struct Q4Params {
     const float* gw;     // [pairs]
     float* out;          // [T][rows]
     int32_t* status;
-    int32_t* order;      // [pairs] grouped by expert
-    int4* pieces;        // [slots] expert (-1: none), first place in order, pairs
-    uint32_t* hb;        // [pairs][cols_p / 64][2][32] B operands (high part, low part)
-    float* hsum;         // [pairs][cols_p / G] half the sums of h / hscale over the groups
-    float* hscale;       // [pairs]
-    float* y;            // [pairs][rows]
+    int32_t* pieces;     // [1 + slots][kQ4Rec]: the first record holds their number; then expert, pairs, pair indexes
+    uint32_t* hb;        // [pairs][cols_p / 64][4][16] B operands
+    float* hsum;         // [pairs][cols_p / G][2]: -7.5 times the groups' sums of hi and of lo
+    float* hscale;       // [pairs] value of the fixed-point unit
+    float* y;            // [ranges of columns][pairs][rows]
     int E, K, T, pairs, slots;
     int tok;             // pairs per piece
-    int ksplit;          // warps that share row blocks along the columns
+    int ksplit;          // ranges of columns (one token: per slot)
+    int kper;            // tiles of a range
 };
+constexpr int kQ4Rec = 12;   // ints of a piece's record: expert, pairs in it, cost of the pieces before it, unused, 8 pair indexes
+constexpr int kQ4Slot0 = 4;
+// Cost of a unit of a piece with np pairs: unpacking the codes, and 2 pairs a block of columns.
+__host__ __device__ constexpr int q4_cost(int np) { return 3 + 2 * (np <= 2 ? 1 : np <= 4 ? 2 : 4); }
 
 // 16 weight bytes of a lane, read once.
 __device__ __forceinline__ uint4 q4_ld(const uint8_t* p) {
@@ -287,56 +313,51 @@ __device__ __forceinline__ void q4_advance(const uint8_t* (&codes)[RB], const ui
     }
 }
 
-// One tile times its B operands (NB of the NL column groups that acc has), added to the
-// row block's sums.  start: half the sum of h over each group that begins here, for the
-// pair of this lane's accumulator columns.  With G = 128 a group is two tiles: `part`
-// carries its sum from the first (half = 0) to the second, where its scale is applied.
+// One tile times the B operands of NB blocks of 8 columns (2 rows of h), added to the row
+// block's sums acc (rows g and g + 8 of this lane's two digits).  start: the lane's share of
+// -7.5 sum h for each group that ends here.  With G = 128 a group is two tiles: `part` carries
+// its sums from the first (half = 0) to the second, where it is scaled.
 template <int G, int NB, int NL>
-__device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], const uint32_t (&bw)[NL][8],
-                                        const float (*start)[NL], int half, float (&part)[NL][4], float (&acc)[NL][4]) {
+__device__ __forceinline__ void q4_tile(const uint4 w, const uint16_t (*s)[2], const uint4 (&bw)[NL],
+                                        const float (*start)[NL], int half, int (&part)[NL][4], float (&acc)[NL][2]) {
     const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int t = 0; t < 4; t++) {
+    for (int m = 0; m < 2; m++) {  // 32 columns
         uint32_t a[4];
-        q4_pairs(word[t], a[0], a[1]);
-        q4_pairs(word[t] >> 8, a[2], a[3]);
-        const bool begins = G <= 32 ? (t & 1) == 0 : t == 0;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            a[2 * i] = word[2 * m + i] & 0x0f0f0f0fu;             // row g
+            a[2 * i + 1] = (word[2 * m + i] >> 4) & 0x0f0f0f0fu;  // row g + 8
+        }
+        const bool begins = G <= 32 || (m == 0 && (G <= kQ4Cols || half == 0));
+        const bool ends = G <= 32 || (m == 1 && (G <= kQ4Cols || half == 1));
+        const int n = G <= 32 ? m : 0;
+        float s0 = 0.0f, s1 = 0.0f;
+        if (ends) {
+            s0 = __half2float(__ushort_as_half(s[n][0]));
+            s1 = __half2float(__ushort_as_half(s[n][1]));
+        }
 #pragma unroll
         for (int j = 0; j < NB; j++) {
-            if (begins && (G <= kQ4Cols || half == 0))
-                q4_mma_start(part[j], a, bw[j][2 * t], bw[j][2 * t + 1], start[G <= 32 ? t >> 1 : 0][j]);
+            const uint32_t b0 = m ? bw[j].z : bw[j].x, b1 = m ? bw[j].w : bw[j].y;
+            if (begins)
+                q4_mma_zero(part[j], a, b0, b1);
             else
-                q4_mma(part[j], a, bw[j][2 * t], bw[j][2 * t + 1]);
-        }
-        const bool ends = G <= 32 ? (t & 1) : t == 3;
-        if (ends && (G <= kQ4Cols || half == 1)) {
-            const int n = G <= 32 ? t >> 1 : 0;
-            const float s0 = __half2float(__ushort_as_half(s[n][0])), s1 = __half2float(__ushort_as_half(s[n][1]));
-#pragma unroll
-            for (int j = 0; j < NB; j++) {
-                acc[j][0] = fmaf(s0, part[j][0], acc[j][0]);
-                acc[j][1] = fmaf(s0, part[j][1], acc[j][1]);
-                acc[j][2] = fmaf(s1, part[j][2], acc[j][2]);
-                acc[j][3] = fmaf(s1, part[j][3], acc[j][3]);
+                q4_mma(part[j], a, b0, b1);
+            if (ends) {  // at most 128 x 15 x 128 x 257 < 2^26
+                acc[j][0] = fmaf(s0, (float)(part[j][0] * 256 + part[j][1]) + start[n][j], acc[j][0]);
+                acc[j][1] = fmaf(s1, (float)(part[j][2] * 256 + part[j][3]) + start[n][j], acc[j][1]);
             }
         }
     }
 }
-
-// Half the sum of a group's h from the group's chunks of 8 columns, one per lane, in
-// neighbouring lanes: returned in every one of them.
-template <int G>
-__device__ __forceinline__ float q4_group_half(const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
-    float v = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&lo[j]));
-        v += (a.x + b.x) + (a.y + b.y);
-    }
-#pragma unroll
-    for (int o = 1; o < G / 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return 0.5f * v;
+// A lane's sums of its two digits, joined with the other two digits' in the neighbouring
+// lane: the results of rows g (even lanes) and g + 8 (odd lanes) in fixed-point units.
+__device__ __forceinline__ float q4_join(const float (&acc)[2], int lane) {
+    const bool odd = lane & 1;
+    const float r0 = odd ? acc[0] : acc[0] * 65536.0f, r1 = odd ? acc[1] : acc[1] * 65536.0f;
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? r0 : r1, 1);
+    return (odd ? r1 : r0) + other;
 }
 
 // ---------------------------------------------------------------------------
@@ -355,20 +376,15 @@ constexpr size_t kQ4T1Smem = 200 * 1024;
 // U tiles of one row block times h; sums: of the first tile's group.
 template <int G, int U>
 __device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, 1, U>& tiles, const uint32_t* hb, const float* sums, int g,
-                                            int c, float (&part)[1][4], float (&acc)[1][4]) {
+                                            int c, int (&part)[1][4], float (&acc)[1][2]) {
+    constexpr int NS = Q4Tiles<G, 1, U>::NS;
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        uint32_t bw[1][8] = {};
-        if (g < 2) {  // column 0: the high part, column 1: the rest; the others are zero
-            const uint4* src = reinterpret_cast<const uint4*>(hb + u * 64 + 32 * g + 8 * c);
-            const uint4 lo = src[0], hi = src[1];
-            bw[0][0] = lo.x; bw[0][1] = lo.y; bw[0][2] = lo.z; bw[0][3] = lo.w;
-            bw[0][4] = hi.x; bw[0][5] = hi.y; bw[0][6] = hi.z; bw[0][7] = hi.w;
-        }
-        constexpr int NS = Q4Tiles<G, 1, U>::NS;
+        uint4 bw[1] = {make_uint4(0, 0, 0, 0)};
+        if (g < 4) bw[0] = *reinterpret_cast<const uint4*>(hb + u * kQ4BTile + 16 * g + 4 * c);  // column g: digit g
         float start[NS][1];
 #pragma unroll
-        for (int n = 0; n < NS; n++) start[n][0] = c == 0 ? sums[u * kQ4Cols / G + n] : 0.0f;
+        for (int n = 0; n < NS; n++) start[n][0] = sums[(u * kQ4Cols / G + n) * 2 + (c & 1)];
         q4_tile<G, 1, 1>(tiles.w[u][0], tiles.s[u][0], bw, start, u & 1, part, acc);
     }
 }
@@ -376,13 +392,13 @@ __device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, 1, U>& tiles, const
 template <int G>
 __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
     constexpr int U = 6, V = G > kQ4Cols ? 2 : 1;  // tiles per batch, and per step of what is left
-    extern __shared__ __align__(16) uint32_t s_h[];  // [K][tiles][2][32], then [K][groups], [row blocks][unit][16], ids, weights
+    extern __shared__ __align__(16) uint32_t s_h[];  // [K][tiles][4][16], then [K][groups][2], [row blocks][unit][16], ids, weights
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int ntiles = P.M.cols_p / kQ4Cols, nblk = P.M.nblk;
     const int nrb = (nblk - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // row blocks blockIdx + i gridDim
     const int ngroups = P.M.cols_p / G;
     float* s_sum = reinterpret_cast<float*>(s_h + (size_t)P.K * P.M.cols_p);
-    float* s_part = s_sum + P.K * ngroups;
+    float* s_part = s_sum + 2 * P.K * ngroups;
     int* s_e = reinterpret_cast<int*>(s_part + (size_t)nrb * P.K * P.ksplit * kQ4Rows);
     float* s_g = reinterpret_cast<float*>(s_e + P.K);
     const int64_t bb = q4_block_bytes(P.M.cols_p, G), scale_off = (int64_t)P.M.cols_p * 8;
@@ -411,7 +427,7 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
         const int j = unit / P.ksplit, t0 = min(ntiles, unit % P.ksplit * per), t1 = min(ntiles, t0 + per);
         const int e = s_e[j];
         uint32_t* hb = s_h + ((size_t)j * ntiles) * 64;
-        const float* sums = s_sum + j * ngroups;
+        const float* sums = s_sum + j * ngroups * 2;
         float scale = 1.0f;
         Q4Tiles<G, 1, U> tiles;
         const bool batches = t1 - t0 >= U;
@@ -421,58 +437,60 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
             const uint16_t* scales[1] = {reinterpret_cast<const uint16_t*>(base + scale_off) + g};
             q4_advance<G>(codes, scales, t0);
             if (batches) tiles.load(codes, scales);
+            // chunks of 16 columns, one a lane: the whole range in most layers, else the first 32 stay in registers
             const int64_t hrow = (int64_t)j * P.M.cols;
-            const int c1 = min(8 * t1, P.M.cols / 8);
-            constexpr int KEEP = 2;  // chunks of 8 columns a lane keeps between the two passes
-            float kept[KEEP][8];
-            float m = 0.0f;
-            auto h_of = [&](int ch, float(&h)[8]) {
+            auto h_of = [&](int ch, float(&h)[16]) {
+                float v[8];
 #pragma unroll
-                for (int i = 0; i < 8; i++) h[i] = 0.0f;
-                if (ch < c1) q4_h8(P.yg, P.yu, hrow + 8 * ch, h);
-            };
+                for (int q = 0; q < 2; q++) {
+                    const bool in = ch < 4 * t1 && 16 * ch + 8 * q < P.M.cols;  // columns are a multiple of 8
+                    if (in) q4_h8(P.yg, P.yu, hrow + 16 * ch + 8 * q, v);
 #pragma unroll
-            for (int k = 0; k < KEEP; k++) h_of(8 * t0 + lane + 32 * k, kept[k]);
-#pragma unroll
-            for (int k = 0; k < KEEP; k++)
-#pragma unroll
-                for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(kept[k][i]));
-            for (int ch = 8 * t0 + lane + 32 * KEEP; ch < c1; ch += 32) {
-                float h[8];
-                h_of(ch, h);
-#pragma unroll
-                for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(h[i]));
-            }
-            scale = q4_h_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
-            const float inv = 1.0f / scale;
-            // whole warps: a group's chunks sit in neighbouring lanes
-            auto put = [&](int ch, const float(&h)[8]) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) q4_split(h[2 * i] * inv, h[2 * i + 1] * inv, hi[i], lo[i]);
-                const float sum = q4_group_half<G>(hi, lo);
-                if (ch < 8 * t1) {
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int w = q4_b_word(ch % 8 * 8 + 2 * i);
-                        hb[(ch / 8) * 64 + w] = hi[i];
-                        hb[(ch / 8) * 64 + 32 + w] = lo[i];
-                    }
-                    if (ch % (G / 8) == 0) s_sum[j * ngroups + ch / (G / 8)] = sum;
+                    for (int i = 0; i < 8; i++) h[8 * q + i] = in ? v[i] : 0.0f;
                 }
             };
+            float kept[16];
+            unsigned bits = 0u;  // of the absolute values: ordered like the values, NaN above all
+            h_of(4 * t0 + lane, kept);
 #pragma unroll
-            for (int k = 0; k < KEEP; k++)
-                if (8 * t0 + 32 * k < 8 * t1) put(8 * t0 + lane + 32 * k, kept[k]);
-            for (int c0 = 8 * t0 + 32 * KEEP; c0 < 8 * t1; c0 += 32) {
-                float h[8];
+            for (int i = 0; i < 16; i++) bits = max(bits, __float_as_uint(fabsf(kept[i])));
+            for (int ch = 4 * t0 + lane + 32; ch < 4 * t1; ch += 32) {
+                float h[16];
+                h_of(ch, h);
+#pragma unroll
+                for (int i = 0; i < 16; i++) bits = max(bits, __float_as_uint(fabsf(h[i])));
+            }
+            const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, bits));
+            const int ex = q4_exponent(m);
+            scale = q4_unit(m, ex);
+            const float to_fixed = q4_pow2(30 - ex);
+            auto put = [&](int ch, const float(&h)[16]) {
+                uint32_t w[4][4];
+                int hi, lo;
+                q4_digits(h, to_fixed, w, hi, lo);
+                q4_group_sums<G>(hi, lo);
+                if (ch >= 4 * t1) return;
+#pragma unroll
+                for (int d = 0; d < 4; d++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) hb[q4_b_at(ch, d, k)] = w[d][k];
+                if (ch % (G / 16) == 0) {
+                    float* sm = s_sum + (j * ngroups + ch / (G / 16)) * 2;
+                    sm[0] = -7.5f * (float)hi;
+                    sm[1] = -7.5f * (float)lo;
+                }
+            };
+            put(4 * t0 + lane, kept);
+            for (int c0 = 4 * t0 + 32; c0 < 4 * t1; c0 += 32) {
+                float h[16];
                 h_of(c0 + lane, h);
                 put(c0 + lane, h);
             }
             __syncwarp();
         }
         for (int i = 0; i < nrb; i++) {
-            float acc[1][4] = {}, part[1][4] = {};
+            float acc[1][2] = {};
+            int part[1][4];
             if (e >= 0 && t0 < t1) {
                 const uint8_t* base = P.M.blob + ((int64_t)e * nblk + blockIdx.x + (int64_t)i * gridDim.x) * bb;
                 const uint8_t* codes[1] = {base + 16 * lane};
@@ -481,21 +499,18 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
                 int tb = t0;
                 for (; tb + U <= t1; tb += U) {
                     if (i > 0 || tb > t0) tiles.load(codes, scales);
-                    q4_t1_batch<G, U>(tiles, hb + tb * 64, sums + tb * kQ4Cols / G, g, c, part, acc);
+                    q4_t1_batch<G, U>(tiles, hb + tb * 64, sums + tb * kQ4Cols / G * 2, g, c, part, acc);
                     q4_advance<G>(codes, scales, U);
                 }
                 for (; tb < t1; tb += V) {
                     Q4Tiles<G, 1, V> one;
                     one.load(codes, scales);
-                    q4_t1_batch<G, V>(one, hb + tb * 64, sums + tb * kQ4Cols / G, g, c, part, acc);
+                    q4_t1_batch<G, V>(one, hb + tb * 64, sums + tb * kQ4Cols / G * 2, g, c, part, acc);
                     q4_advance<G>(codes, scales, V);
                 }
             }
-            if (c == 0) {
-                float* o = s_part + ((size_t)i * P.K * P.ksplit + unit) * kQ4Rows;
-                o[g] = (acc[0][0] + acc[0][1]) * scale;
-                o[g + 8] = (acc[0][2] + acc[0][3]) * scale;
-            }
+            const float r = q4_join(acc[0], lane);
+            if (c < 2) s_part[((size_t)i * P.K * P.ksplit + unit) * kQ4Rows + g + 8 * c] = r * scale;
         }
     }
     __syncthreads();
@@ -520,50 +535,78 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
 // First launch: the first CTA groups the pairs by expert and cuts the groups into
 // pieces of `tok` pairs; every other CTA forms h, its scale and its B operands for one
 // pair (independent of the grouping).
-constexpr int kQ4PrepThreads = 512;
+constexpr int kQ4PrepThreads = 256;
 
 __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
     __shared__ int s_warp[32];
-    __shared__ int s_carry[2];
+    __shared__ int s_carry, s_cost;
+    constexpr int KEEP = 8;  // pairs whose expert a thread keeps
     const int tid = threadIdx.x;
+    int* s_first = s_cnt + P.E;  // the expert's first piece
+    int mine[KEEP];
+#pragma unroll
+    for (int i = 0; i < KEEP; i++) {
+        const int p = tid + i * kQ4PrepThreads;
+        mine[i] = p < P.pairs ? P.ids[p] : -1;
+    }
     for (int e = tid; e < P.E; e += kQ4PrepThreads) s_cnt[e] = 0;
-    if (tid < 2) s_carry[tid] = 0;
+    if (tid == 0) s_carry = s_cost = 0;
     __syncthreads();
     bool bad = false;
-    for (int p = tid; p < P.pairs; p += kQ4PrepThreads) {
-        const int e = P.ids[p];
-        if (e >= 0 && e < P.E)
+    auto each = [&](auto&& f) {  // every pair of this thread with its expert, -1 for a bad one
+#pragma unroll
+        for (int i = 0; i < KEEP; i++)
+            if (tid + i * kQ4PrepThreads < P.pairs) f(tid + i * kQ4PrepThreads, mine[i] < P.E ? mine[i] : -1);
+        for (int p = tid + KEEP * kQ4PrepThreads; p < P.pairs; p += kQ4PrepThreads) {
+            const int e = P.ids[p];
+            f(p, e < P.E ? e : -1);
+        }
+    };
+    each([&](int, int e) {
+        if (e >= 0)
             atomicAdd(&s_cnt[e], 1);
         else
             bad = true;
-    }
+    });
     if (bad && P.status) atomicOr(P.status, BITSMOE_ST_BADEXPERT);
     __syncthreads();
     for (int e0 = 0; e0 < P.E; e0 += kQ4PrepThreads) {
         const int e = e0 + tid, n = e < P.E ? s_cnt[e] : 0, np = (n + P.tok - 1) / P.tok;
-        const int end = cta_scan<kQ4PrepThreads>(n, s_warp) + s_carry[0];
-        const int pend = cta_scan<kQ4PrepThreads>(np, s_warp) + s_carry[1];
-        if (e < P.E) s_cnt[e] = end - n;  // becomes the place of the expert's next pair
-        for (int i = 0; i < np; i++)
-            P.pieces[pend - np + i] = make_int4(e, end - n + i * P.tok, min(P.tok, n - i * P.tok), 0);
+        const int first = cta_scan<kQ4PrepThreads>(np, s_warp) + s_carry - np;
+        if (e < P.E) {
+            s_cnt[e] = 0;  // becomes the place of the expert's next pair
+            s_first[e] = first;
+        }
+        const int cost = np > 0 ? (np - 1) * q4_cost(P.tok) + q4_cost(n - (np - 1) * P.tok) : 0;
+        const int before = cta_scan<kQ4PrepThreads>(cost, s_warp) + s_cost - cost;
+        for (int i = 0; i < np; i++) {
+            int32_t* rec = P.pieces + (int64_t)(1 + first + i) * kQ4Rec;
+            rec[0] = e;
+            rec[1] = min(P.tok, n - i * P.tok);
+            rec[2] = before + i * q4_cost(P.tok);
+        }
         __syncthreads();
         if (tid == kQ4PrepThreads - 1) {
-            s_carry[0] = end;
-            s_carry[1] = pend;
+            s_carry = first + np;
+            s_cost = before + cost;
         }
         __syncthreads();
     }
-    for (int i = s_carry[1] + tid; i < P.slots; i += kQ4PrepThreads) P.pieces[i] = make_int4(-1, 0, 0, 0);
-    // a pair's place inside its group may vary; its result does not depend on it
-    for (int p = tid; p < P.pairs; p += kQ4PrepThreads) {
-        const int e = P.ids[p];
-        if (e >= 0 && e < P.E) P.order[atomicAdd(&s_cnt[e], 1)] = p;
+    if (tid == 0) {
+        P.pieces[0] = s_carry;
+        P.pieces[2] = s_cost;
     }
+    // a pair's place inside its group may vary; its result does not depend on it
+    each([&](int p, int e) {
+        if (e < 0) return;
+        const int at = atomicAdd(&s_cnt[e], 1);
+        P.pieces[(int64_t)(1 + s_first[e] + at / P.tok) * kQ4Rec + kQ4Slot0 + at % P.tok] = p;
+    });
 }
 
 template <int G>
 __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
-    extern __shared__ int32_t s_cnt[];
+    extern __shared__ int32_t s_cnt[];  // [E] counts, [E] first pieces (the grouping CTA)
     __shared__ unsigned s_max;
     const int tid = threadIdx.x;
     pdl_wait();
@@ -577,219 +620,301 @@ __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
     if (tid == 0) s_max = 0u;
     __syncthreads();
     const int64_t base = (int64_t)pair * P.M.cols;
-    const int nch = P.M.cols / 8;
-    constexpr int KEEP = 2;  // chunks of 8 a thread keeps between the two passes
-    float h[KEEP][8];
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < KEEP; i++) {
-        const int c = tid + i * kQ4PrepThreads;
-#pragma unroll
-        for (int j = 0; j < 8; j++) h[i][j] = 0.0f;
-        if (c < nch) q4_h8(P.yg, P.yu, base + 8 * c, h[i]);
-#pragma unroll
-        for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(h[i][j]));
-    }
-    for (int c = tid + KEEP * kQ4PrepThreads; c < nch; c += kQ4PrepThreads) {
+    const int nch = P.M.cols_p / 16;  // chunks of 16 columns, one a thread at a time
+    auto h_of = [&](int ch, float(&h)[16]) {
         float v[8];
-        q4_h8(P.yg, P.yu, base + 8 * c, v);
 #pragma unroll
-        for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
-    }
-    const unsigned wm = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // non-negative: ordered like their bits
-    if ((tid & 31) == 0) atomicMax(&s_max, wm);
-    __syncthreads();
-    const float scale = q4_h_scale(__uint_as_float(s_max)), inv = 1.0f / scale;
-    if (tid == 0) P.hscale[pair] = scale;
-    uint32_t* hb = P.hb + (int64_t)pair * P.M.cols_p;
-    // whole warps: a group's chunks sit in neighbouring lanes
-    auto put = [&](int c, const float(&v)[8]) {
-        uint32_t hi[4], lo[4];
+        for (int q = 0; q < 2; q++) {
+            const bool in = 16 * ch + 8 * q < P.M.cols;  // columns are a multiple of 8
+            if (in) q4_h8(P.yg, P.yu, base + 16 * ch + 8 * q, v);
 #pragma unroll
-        for (int j = 0; j < 4; j++) q4_split(v[2 * j] * inv, v[2 * j + 1] * inv, hi[j], lo[j]);
-        const float sum = q4_group_half<G>(hi, lo);
-        if (c >= P.M.cols_p / 8) return;
-        uint32_t* tile = hb + (int64_t)(c / 8) * 64;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int w = q4_b_word(c % 8 * 8 + 2 * j);
-            tile[w] = hi[j];
-            tile[32 + w] = lo[j];
+            for (int i = 0; i < 8; i++) h[8 * q + i] = in ? v[i] : 0.0f;
         }
-        if (c % (G / 8) == 0) P.hsum[(int64_t)pair * (P.M.cols_p / G) + c / (G / 8)] = sum;
     };
+    float kept[16];
+    unsigned m = 0u;  // of the absolute values' bits: ordered like the values, NaN above all
+    h_of(tid, kept);
 #pragma unroll
-    for (int i = 0; i < KEEP; i++)
-        if (i * kQ4PrepThreads < P.M.cols_p / 8) put(tid + i * kQ4PrepThreads, h[i]);
-    for (int c0 = KEEP * kQ4PrepThreads; c0 < P.M.cols_p / 8; c0 += kQ4PrepThreads) {
-        const int c = c0 + tid;
-        float v[8] = {};
-        if (c < nch) q4_h8(P.yg, P.yu, base + 8 * c, v);
-        put(c, v);
+    for (int i = 0; i < 16; i++) m = max(m, __float_as_uint(fabsf(kept[i])));
+    for (int ch = tid + kQ4PrepThreads; ch < nch; ch += kQ4PrepThreads) {
+        float v[16];
+        h_of(ch, v);
+#pragma unroll
+        for (int i = 0; i < 16; i++) m = max(m, __float_as_uint(fabsf(v[i])));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((tid & 31) == 0) atomicMax(&s_max, m);
+    __syncthreads();
+    const float largest = __uint_as_float(s_max);
+    const int ex = q4_exponent(largest);
+    const float to_fixed = q4_pow2(30 - ex);
+    if (tid == 0) P.hscale[pair] = q4_unit(largest, ex);
+    uint32_t* hb = P.hb + (int64_t)pair * P.M.cols_p;
+    auto put = [&](int ch, const float(&v)[16]) {
+        uint32_t w[4][4];
+        int hi, lo;
+        q4_digits(v, to_fixed, w, hi, lo);
+        q4_group_sums<G>(hi, lo);
+        if (ch >= nch) return;
+#pragma unroll
+        for (int d = 0; d < 4; d++)
+#pragma unroll
+            for (int k = 0; k < 4; k++) hb[q4_b_at(ch, d, k)] = w[d][k];
+        if (ch % (G / 16) == 0) {
+            float* sm = P.hsum + ((int64_t)pair * (P.M.cols_p / G) + ch / (G / 16)) * 2;
+            sm[0] = -7.5f * (float)hi;
+            sm[1] = -7.5f * (float)lo;
+        }
+    };
+    put(tid, kept);
+    for (int c0 = kQ4PrepThreads; c0 < nch; c0 += kQ4PrepThreads) {  // whole warps
+        float v[16];
+        h_of(c0 + tid, v);
+        put(c0 + tid, v);
     }
 }
 
-// Second launch: CTA = (a piece of up to 4 NTL pairs of one expert, (8 / ksplit) RB
-// blocks of 16 rows); its 8 warps are row groups x ranges of columns.  A warp's next U
-// tiles are loaded while it multiplies the last ones; the B operands come through L1.
-// Bound by instructions as much as by HBM: a tile of 512 bytes takes 44 to turn its
-// codes into fp16, 4 MMAs per column group and about 12 for loads and scales.
+// Second launch: the pieces times their expert's rows.  The work is cut into units of one
+// piece, one range of columns and one block of 16 rows, in that order, and every CTA takes
+// a contiguous run of them of equal cost for its 8 warps: its units share a piece and a
+// range, whose B operands stay in L1.  A warp streams its units' tiles through a ring of
+// its own in shared memory, filled by bulk copies of up to 8 tiles, a stage ahead and
+// across the borders of units (without the products this reads at HBM's rate).  Results go
+// from registers to memory, a row of y per pair and range; no CTA barrier is met.
 constexpr int kQ4Warps = 8;
 constexpr int kQ4Threads = 32 * kQ4Warps;
+constexpr int kQ4CT = 8;                                        // tiles per stage, at most
+constexpr int kQ4StageBytes = kQ4CT * (kQ4TileBytes + 2 * 32);  // their codes, and up to 2 groups' scales each
+constexpr int kQ4Stages = 2;
 
-// U tiles of a warp's row blocks times the first NB of NTL column groups; hb: B operands
-// of the first tile, sums: half sums of its group.
-template <int G, int NB, int NTL, int RB, int U>
-__device__ __forceinline__ void q4_batch(const Q4Tiles<G, RB, U>& tiles, const uint32_t* const (&hb)[NTL],
-                                         const float* const (&sums)[NTL], float (&part)[RB][NTL][4],
-                                         float (&acc)[RB][NTL][4]) {
-    constexpr int NS = Q4Tiles<G, RB, U>::NS;
+__device__ __forceinline__ void q4_bulk(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// A warp's ring.  The producer cursor and the consumer cursor see the same sequence of
+// stages; stage q uses slot q mod kQ4Stages.
+template <int G>
+struct Q4Ring {
+    uint8_t* slots;
+    uint32_t base, bars;  // shared-memory addresses of the slots and their barriers
+    int in_slot, out_slot;
+    uint32_t out_phase;
+
+    __device__ __forceinline__ void init(uint8_t* smem, uint64_t* bar, int lane) {
+        slots = smem;
+        base = (uint32_t)__cvta_generic_to_shared(smem);
+        bars = (uint32_t)__cvta_generic_to_shared(bar);
+        in_slot = out_slot = 0;
+        out_phase = 0;
+        if (lane < kQ4Stages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * lane));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+    }
+    // Tiles t .. t + n - 1 of the row block at `block`: codes, then scales; one copy when that is the whole block.
+    __device__ __forceinline__ void fill(const Q4Params& P, const uint8_t* block, int t, int n, int lane) {
+        const uint32_t slot = base + in_slot * kQ4StageBytes, bar = bars + 8 * in_slot;
+        const uint32_t cb = n * kQ4TileBytes, sb = n * (kQ4Cols * 32) / G;
+        const bool whole = n * kQ4Cols == P.M.cols_p;
+        if (lane == 0) {
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(cb + sb) : "memory");
+            q4_bulk(slot, block + (int64_t)t * kQ4TileBytes, whole ? cb + sb : cb, bar);
+            if (!whole) q4_bulk(slot + cb, block + (int64_t)P.M.cols_p * 8 + (int64_t)t * (kQ4Cols * 32) / G, sb, bar);
+        }
+        __syncwarp();
+        in_slot = in_slot == kQ4Stages - 1 ? 0 : in_slot + 1;
+    }
+    __device__ __forceinline__ bool wait() { return warp_wait(bars + 8 * out_slot, out_phase); }
+    __device__ __forceinline__ const uint8_t* slot() const { return slots + out_slot * kQ4StageBytes; }
+    __device__ __forceinline__ void pop() {  // every lane has read the slot
+        __syncwarp();
+        if (++out_slot == kQ4Stages) {
+            out_slot = 0;
+            out_phase ^= 1u;
+        }
+    }
+};
+
+// What a lane holds of one piece: NTL blocks of 2 pairs (8 columns: 4 digits each).
+template <int G, int NTL>
+struct Q4Piece {
+    const uint32_t* hb[NTL];  // B operands of column g: digit g mod 4 of pair g / 4; past the last pair, that one
+    const float* sums[NTL];   // -7.5 sum h of the accumulator columns 2c and 2c + 1: 2 digits of pair c / 2
+    int pair[NTL];            // that pair
+
+    __device__ __forceinline__ void set(const Q4Params& P, const int32_t* rec, int np, int t0, int lane) {
+        const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int j = 0; j < NTL; j++) {
+            const int col = rec[kQ4Slot0 + min(2 * j + g / 4, np - 1)];
+            pair[j] = rec[kQ4Slot0 + min(2 * j + c / 2, np - 1)];
+            hb[j] = P.hb + (int64_t)col * P.M.cols_p + 16 * (g & 3) + 4 * c + t0 * kQ4BTile;
+            sums[j] = P.hsum + ((int64_t)pair[j] * (P.M.cols_p / G) + t0 * kQ4Cols / G) * 2 + (c & 1);
+        }
+    }
+};
+
+// U tiles of a stage times the first NB of NTL blocks of columns.
+template <int G, int NB, int NTL, int U>
+__device__ __forceinline__ void q4_tiles(const uint8_t* codes, const uint16_t* scales, Q4Piece<G, NTL>& piece,
+                                         int (&part)[NTL][4], float (&acc)[NTL][2]) {
+    constexpr int NS = G < kQ4Cols ? kQ4Cols / G : 1;
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        uint32_t bw[NTL][8];
+        uint4 bw[NTL];
         float start[NS][NTL];
 #pragma unroll
         for (int j = 0; j < NB; j++) {
-            const uint4* src = reinterpret_cast<const uint4*>(hb[j] + u * 64);
-            const uint4 lo = src[0], hi = src[1];
-            bw[j][0] = lo.x; bw[j][1] = lo.y; bw[j][2] = lo.z; bw[j][3] = lo.w;
-            bw[j][4] = hi.x; bw[j][5] = hi.y; bw[j][6] = hi.z; bw[j][7] = hi.w;
+            bw[j] = *reinterpret_cast<const uint4*>(piece.hb[j] + u * kQ4BTile);
 #pragma unroll
-            for (int n = 0; n < NS; n++) start[n][j] = sums[j][u * kQ4Cols / G + n];
+            for (int k = 0; k < NS; k++) start[k][j] = piece.sums[j][(u * kQ4Cols / G + k) * 2];
         }
+        uint16_t s[NS][2];
 #pragma unroll
-        for (int r = 0; r < RB; r++)
-            q4_tile<G, NB, NTL>(tiles.w[u][r], tiles.s[u][r], bw, start, u & 1, part[r], acc[r]);
+        for (int k = 0; k < NS; k++) {
+            s[k][0] = scales[(G > kQ4Cols ? u / 2 : u * NS + k) * kQ4Rows];
+            s[k][1] = scales[(G > kQ4Cols ? u / 2 : u * NS + k) * kQ4Rows + 8];
+        }
+        const uint4 w = *reinterpret_cast<const uint4*>(codes + u * kQ4TileBytes);
+        q4_tile<G, NB, NTL>(w, s, bw, start, u & 1, part, acc);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; j++) {
+        piece.hb[j] += U * kQ4BTile;
+        piece.sums[j] += U * kQ4Cols / G * 2;
     }
 }
-
-// n tiles of a warp's row blocks; while one batch of U is multiplied the next is loaded.
-template <int G, int NB, int NTL, int RB, int U>
-__device__ __forceinline__ void q4_range(const uint8_t* (&codes)[RB], const uint16_t* (&scales)[RB],
-                                         const uint32_t* (&hb)[NTL], const float* (&sums)[NTL], int n,
-                                         float (&acc)[RB][NTL][4]) {
-    constexpr int V = G > kQ4Cols ? 2 : 1;
-    float part[RB][NTL][4];
-    Q4Tiles<G, RB, U> one, two;
-    int left = n / U;
-    auto next = [&](Q4Tiles<G, RB, U>& t) {
-        t.load(codes, scales);
-        q4_advance<G>(codes, scales, U);
-    };
-    auto use = [&](const Q4Tiles<G, RB, U>& t) {
-        q4_batch<G, NB, NTL, RB, U>(t, hb, sums, part, acc);
-#pragma unroll
-        for (int j = 0; j < NB; j++) {
-            hb[j] += U * 64;
-            sums[j] += U * kQ4Cols / G;
-        }
-        left--;
-    };
-    if (left > 0) next(one);
-    while (left > 0) {
-        if (left > 1) next(two);
-        use(one);
-        if (left == 0) break;
-        if (left > 1) next(one);
-        use(two);
+// The n tiles of a stage (codes, then scales) times the first NB of NTL blocks of columns.
+template <int G, int NB, int NTL>
+__device__ __forceinline__ void q4_stage(const uint8_t* slot, int n, Q4Piece<G, NTL>& piece, float (&acc)[NTL][2], int lane) {
+    constexpr int U = NB > 2 ? 2 : 4, V = G > kQ4Cols ? 2 : 1;
+    int part[NTL][4];
+    const uint8_t* codes = slot + 16 * lane;
+    const uint16_t* scales = reinterpret_cast<const uint16_t*>(slot + n * kQ4TileBytes) + (lane >> 2);
+    for (; n >= U; n -= U) {
+        q4_tiles<G, NB, NTL, U>(codes, scales, piece, part, acc);
+        codes += U * kQ4TileBytes;
+        scales += U * kQ4Cols / G * kQ4Rows;
     }
-    for (int k = n % U; k > 0; k -= V) {
-        Q4Tiles<G, RB, V> t;
-        t.load(codes, scales);
-        q4_advance<G>(codes, scales, V);
-        q4_batch<G, NB, NTL, RB, V>(t, hb, sums, part, acc);
-#pragma unroll
-        for (int j = 0; j < NB; j++) {
-            hb[j] += V * 64;
-            sums[j] += V * kQ4Cols / G;
-        }
+    for (; n > 0; n -= V) {
+        q4_tiles<G, NB, NTL, V>(codes, scales, piece, part, acc);
+        codes += V * kQ4TileBytes;
+        scales += V * kQ4Cols / G * kQ4Rows;
     }
 }
+template <int G, int NTL>
+__device__ __forceinline__ void q4_stage_any(const uint8_t* slot, int n, int np, Q4Piece<G, NTL>& piece,
+                                             float (&acc)[NTL][2], int lane) {
+    if (NTL > 2 && np > 4)
+        q4_stage<G, NTL, NTL>(slot, n, piece, acc, lane);
+    else if (np > 2)
+        q4_stage<G, 2, NTL>(slot, n, piece, acc, lane);
+    else
+        q4_stage<G, 1, NTL>(slot, n, piece, acc, lane);
+}
 
-template <int G, int NTL, int RB, int U>
+template <int G, int NTL>
 __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_mt(const Q4Params P) {
-    __shared__ float s_part[kQ4Warps][RB * kQ4Rows][4 * NTL + 1];
-    __shared__ int s_pair[4 * NTL];
+    extern __shared__ __align__(128) uint8_t s_ring[];
+    __shared__ uint64_t s_bar[kQ4Warps][kQ4Stages];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int ntiles = P.M.cols_p / kQ4Cols, nblk = P.M.nblk;
+    const int64_t bb = q4_block_bytes(P.M.cols_p, G);
+    Q4Ring<G> ring;
+    ring.init(s_ring + warp * (kQ4Stages * kQ4StageBytes), s_bar[warp], lane);
     pdl_wait();
     pdl_trigger();
-    const int4 piece = P.pieces[blockIdx.y];
-    const int e = piece.x, np = piece.z;
-    if (e < 0) return;
-    const int ntiles = P.M.cols_p / kQ4Cols;
-    const int wk = warp % P.ksplit, wr = warp / P.ksplit, nwr = kQ4Warps / P.ksplit;
-    constexpr int TG = G > kQ4Cols ? G / kQ4Cols : 1;  // ranges of whole groups
-    const int per = ((ntiles / TG + P.ksplit - 1) / P.ksplit) * TG;
-    const int t0 = min(ntiles, wk * per), t1 = min(ntiles, t0 + per);
-    const int64_t bb = q4_block_bytes(P.M.cols_p, G);
-    const int blk0 = (int)blockIdx.x * nwr * RB;
-    const uint8_t* codes[RB];
-    const uint16_t* scales[RB];
-#pragma unroll
-    for (int r = 0; r < RB; r++) {
-        const uint8_t* base = P.M.blob + ((int64_t)e * P.M.nblk + min(blk0 + wr * RB + r, P.M.nblk - 1)) * bb;
-        codes[r] = base + 16 * lane;
-        scales[r] = reinterpret_cast<const uint16_t*>(base + (int64_t)P.M.cols_p * 8) + g;
-    }
-    // this lane's column g of each 8-column B operand: pair g / 2, high part for even g; columns past the last pair
-    // repeat it and are not stored
-    const uint32_t* hb[NTL];
-    const float* sums[NTL];  // of the pair of its accumulator columns 2c (high part) and 2c + 1
-#pragma unroll
-    for (int j = 0; j < NTL; j++) {
-        const int i = min(4 * j + g / 2, np - 1), k = min(4 * j + c, np - 1);
-        hb[j] = P.hb + (int64_t)P.order[piece.y + i] * P.M.cols_p + 32 * (g & 1) + 8 * c + t0 * 64;
-        sums[j] = P.hsum + (int64_t)P.order[piece.y + k] * (P.M.cols_p / G) + t0 * kQ4Cols / G;
-    }
-    if (threadIdx.x < np) s_pair[threadIdx.x] = P.order[piece.y + threadIdx.x];
-    float acc[RB][NTL][4];
-#pragma unroll
-    for (int r = 0; r < RB; r++)
-#pragma unroll
-        for (int j = 0; j < NTL; j++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) acc[r][j][q] = 0.0f;
-    q4_advance<G>(codes, scales, t0);
-    if (NTL > 2 && np > 8)
-        q4_range<G, NTL, NTL, RB, U>(codes, scales, hb, sums, t1 - t0, acc);
-    else if (NTL > 1 && np > 4)
-        q4_range<G, NTL < 2 ? 1 : 2, NTL, RB, U>(codes, scales, hb, sums, t1 - t0, acc);
-    else
-        q4_range<G, 1, NTL, RB, U>(codes, scales, hb, sums, t1 - t0, acc);
-    // columns 2c and 2c + 1 of a fragment are the high and the low part of pair c
-#pragma unroll
-    for (int r = 0; r < RB; r++)
+    const int npieces = P.pieces[0];
+    const int per_piece = P.ksplit * nblk;  // units of a piece
+    // first unit (numbered over the pieces) at or after a share b / gridDim.x of the cost
+    auto unit_at = [&](int b) -> int {
+        const int64_t at = (int64_t)P.pieces[2] * per_piece * b / gridDim.x;
+        int lo = 0;  // the last piece that starts at or before `at` is one of n from lo on
+        for (int n = npieces; n > 1;) {
+            const int w = (n + 31) / 32, i = lane * w;
+            const bool below = i < n && P.pieces[(int64_t)(1 + lo + i) * kQ4Rec + 2] * (int64_t)per_piece <= at;
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));  // lane 0 is always below
+            lo += k * w;
+            n = min(w, n - k * w);
+        }
+        const int32_t* rec = P.pieces + (int64_t)(1 + lo) * kQ4Rec;
+        const int64_t off = at - rec[2] * (int64_t)per_piece;
+        const int w = q4_cost(rec[1]);
+        return lo * per_piece + (int)min((int64_t)per_piece, (off + w - 1) / w);
+    };
+    if (npieces == 0) return;
+    const int u0 = unit_at(blockIdx.x) + warp;
+    const int u1 = blockIdx.x + 1 == gridDim.x ? npieces * per_piece : unit_at(blockIdx.x + 1);
+    // producer: the next stage to fill starts at tile pt (below pt1) of unit pu
+    int pu = u0;
+    int pt = 0, pt1 = 0;
+    const uint8_t* pblock = nullptr;
+    auto fill = [&]() {
+        if (pu >= u1) return;
+        if (pt == pt1) {
+            const int part = pu / nblk, e = P.pieces[(int64_t)(1 + part / P.ksplit) * kQ4Rec];
+            pblock = P.M.blob + ((int64_t)e * nblk + pu % nblk) * bb;
+            pt = part % P.ksplit * P.kper;
+            pt1 = min(ntiles, pt + P.kper);
+        }
+        const int n = min(kQ4CT, pt1 - pt);
+        ring.fill(P, pblock, pt, n, lane);
+        pt += n;
+        if (pt == pt1) pu += kQ4Warps;
+    };
+    for (int i = 0; i < kQ4Stages; i++) fill();
+    for (int u = u0; u < u1; u += kQ4Warps) {
+        const int part = u / nblk, kp = part % P.ksplit;
+        const int32_t* rec = P.pieces + (int64_t)(1 + part / P.ksplit) * kQ4Rec;
+        const int np = rec[1], t0 = kp * P.kper, t1 = min(ntiles, t0 + P.kper);
+        Q4Piece<G, NTL> piece;
+        piece.set(P, rec, np, t0, lane);
+        float acc[NTL][2] = {};
+        for (int t = t0; t < t1; t += kQ4CT) {
+            if (!ring.wait()) {
+                if (lane == 0 && P.status) atomicOr(P.status, BITSMOE_ST_TIMEOUT);
+                return;
+            }
+            q4_stage_any<G, NTL>(ring.slot(), min(kQ4CT, t1 - t), np, piece, acc, lane);
+            ring.pop();
+            fill();
+        }
+        const int row = u % nblk * kQ4Rows + g + 8 * (c & 1);
 #pragma unroll
         for (int j = 0; j < NTL; j++) {
-            s_part[warp][r * kQ4Rows + g][4 * j + c] = acc[r][j][0] + acc[r][j][1];
-            s_part[warp][r * kQ4Rows + g + 8][4 * j + c] = acc[r][j][2] + acc[r][j][3];
+            const float r = q4_join(acc[j], lane);
+            if (2 * j + c / 2 < np && row < P.M.rows)
+                P.y[((int64_t)kp * P.pairs + piece.pair[j]) * P.M.rows + row] = r * P.hscale[piece.pair[j]];
         }
-    __syncthreads();
-    const int rows_cta = nwr * RB * kQ4Rows;
-    for (int v = threadIdx.x; v < rows_cta * np; v += kQ4Threads) {
-        const int r = v % rows_cta, i = v / rows_cta;
-        const int row = blk0 * kQ4Rows + r;
-        if (row >= P.M.rows) continue;
-        float sum = 0.0f;
-        for (int k = 0; k < P.ksplit; k++) sum += s_part[r / (RB * kQ4Rows) * P.ksplit + k][r % (RB * kQ4Rows)][i];
-        const int pair = s_pair[i];
-        P.y[(int64_t)pair * P.M.rows + row] = sum * P.hscale[pair];
     }
 }
 
-// Third launch: each token's sum over its slots, in order.
+// Third launch: each token's sum over its slots, in order, and over a slot's ranges of columns.
 __global__ void __launch_bounds__(256) k_q4_sum(const Q4Params P) {
     pdl_wait();
     pdl_trigger();
-    const int64_t n = (int64_t)P.T * P.M.rows;
+    const int64_t n = (int64_t)P.T * P.M.rows, range = (int64_t)P.pairs * P.M.rows;
     for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < n; x += (int64_t)gridDim.x * blockDim.x) {
         const int64_t t = x / P.M.rows;
-        const int row = (int)(x % P.M.rows);
+        const float* y = P.y + t * P.K * P.M.rows + x % P.M.rows;
         float acc = 0.0f;
-        for (int j = 0; j < P.K; j++) {
-            const int64_t pair = t * P.K + j;
-            const int e = P.ids[pair];
-            if (e >= 0 && e < P.E) acc = fmaf(P.gw[pair], P.y[pair * P.M.rows + row], acc);
+        for (int j0 = 0; j0 < P.K; j0 += 8) {  // a slot's rows are read whether or not its id is one: they are not used then
+            float v[8], w[8];
+            int e[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int k = min(j0 + j, P.K - 1);
+                v[j] = y[(int64_t)k * P.M.rows];
+                w[j] = P.gw[t * P.K + k];
+                e[j] = P.ids[t * P.K + k];
+            }
+            for (int r = 1; r < P.ksplit; r++)
+#pragma unroll
+                for (int j = 0; j < 8; j++) v[j] += y[r * range + (int64_t)min(j0 + j, P.K - 1) * P.M.rows];
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (j0 + j < P.K && e[j] >= 0 && e[j] < P.E) acc = fmaf(w[j], v[j], acc);
         }
         P.out[x] = acc;
     }
@@ -798,13 +923,11 @@ __global__ void __launch_bounds__(256) k_q4_sum(const Q4Params P) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-constexpr int kQ4MaxE = 8192;  // the grouping counts them in shared memory (32 KB)
+constexpr int kQ4Sms = 148;    // SMs the launches are sized for
+constexpr int kQ4MaxE = 4096;  // the grouping counts them in shared memory (32 KB)
 
-// Pairs per piece: 4, 8 or 16, by the expected group size.
-static int q4_tok(int pairs, int E) {
-    const int avg = pairs / E;
-    return avg <= 3 ? 4 : avg <= 6 ? 8 : 16;
-}
+// Pairs per piece, by the expected group size.  8 at most: the sums of more do not fit the registers.
+static int q4_tok(int pairs, int E) { return pairs / E <= 3 ? 4 : 8; }
 static int q4_slots(int pairs, int E) { return std::min(pairs, E) + pairs / q4_tok(pairs, E); }
 
 // The single-token kernel: h and the partial sums of a CTA's row blocks fit its shared memory.
@@ -812,22 +935,34 @@ static size_t q4_t1_smem(const bitsmoe_ffn_dims* d, int group, int sms) {
     const int nblk = (d->d_model + kQ4Rows - 1) / kQ4Rows, grid = std::min(nblk, sms), nrb = (nblk + grid - 1) / grid;
     const size_t units = (size_t)d->top_k * std::max(1, kQ4T1Warps / d->top_k);
     const size_t cols_p = q4_cols_padded(d->d_ff, group);
-    return 4ull * d->top_k * (cols_p + cols_p / group) + 4ull * nrb * units * kQ4Rows + 8ull * d->top_k;
+    return 4ull * d->top_k * (cols_p + 2 * (cols_p / group)) + 4ull * nrb * units * kQ4Rows + 8ull * d->top_k;
 }
-constexpr int kQ4Sms = 148;  // CTAs of the single-token kernel: one per SM
 static bool q4_single(const bitsmoe_ffn_dims* d, int group, int T) {
     return T == 1 && d->top_k <= 64 && q4_t1_smem(d, group, kQ4Sms) <= kQ4T1Smem;
 }
 
 struct Q4WS {
-    int32_t* order;
-    int4* pieces;
+    int32_t* pieces;
     uint32_t* hb;
     float* hsum;
     float* hscale;
     float* y;
     uint64_t used;
 };
+
+// Ranges of columns of the grouped form.  Enough for 4 units for each of the 16 resident
+// warps of an SM when few row blocks are touched, of 4 tiles or more each, and with
+// partial sums (4 bytes per pair, row and further range) that take no more memory than
+// the B operands and half a MB.
+static void q4_ranges(const bitsmoe_ffn_dims* d, int group, int64_t pairs, int& ksplit, int& kper) {
+    const int64_t nblk = (d->d_model + kQ4Rows - 1) / kQ4Rows, ntiles = q4_cols_padded(d->d_ff, group) / kQ4Cols;
+    const int64_t units = std::min<int64_t>(pairs, d->n_experts) * nblk;
+    int64_t ks = std::max<int64_t>(1, (4 * 16 * kQ4Sms + units - 1) / units);
+    ks = std::min(ks, std::max<int64_t>(1, ntiles / 4));
+    ks = std::min(ks, 1 + (d->d_ff + (1 << 17) / pairs) / d->d_model);
+    kper = (int)roundup((uint64_t)((ntiles + ks - 1) / ks), 2);  // whole groups, also where one is two tiles
+    ksplit = (int)((ntiles + kper - 1) / kper);
+}
 
 static Q4WS q4_ws(const bitsmoe_ffn_dims* d, int group, int T, uint8_t* base) {
     Q4WS w{};
@@ -838,12 +973,13 @@ static Q4WS q4_ws(const bitsmoe_ffn_dims* d, int group, int T, uint8_t* base) {
         return base ? base + off : nullptr;
     };
     const uint64_t pairs = (uint64_t)T * d->top_k, dp = q4_cols_padded(d->d_ff, group);
-    w.order = (int32_t*)take(4 * pairs);
-    w.pieces = (int4*)take(16ull * q4_slots((int)pairs, d->n_experts));
+    int ksplit, kper;
+    q4_ranges(d, group, (int64_t)pairs, ksplit, kper);
+    w.pieces = (int32_t*)take(4ull * kQ4Rec * (1 + q4_slots((int)pairs, d->n_experts)));
     w.hb = (uint32_t*)take(4 * pairs * dp);
-    w.hsum = (float*)take(4 * pairs * (dp / group));
+    w.hsum = (float*)take(8 * pairs * (dp / group));
     w.hscale = (float*)take(4 * pairs);
-    w.y = (float*)take(4 * pairs * d->d_model);
+    w.y = (float*)take(4 * pairs * d->d_model * ksplit);
     w.used = used;
     return w;
 }
@@ -854,19 +990,21 @@ static bool q4_dims_ok(const bitsmoe_ffn_dims* d, int group, int T) {
            d->d_ff <= (1 << 30) && d->d_model <= (1 << 30);
 }
 
+template <int G, int NTL>
+static int launch_q4_form(Q4Params& P, cudaStream_t s) {
+    const int64_t most = (int64_t)P.slots * P.ksplit * P.M.nblk;
+    if (most > 0x7fffffff) return BITSMOE_EINVAL;
+    const int smem = kQ4Warps * kQ4Stages * kQ4StageBytes;
+    const cudaError_t e = cudaFuncSetAttribute(k_q4_mt<G, NTL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    const unsigned grid = (unsigned)std::min<int64_t>(2 * kQ4Sms, (most + kQ4Warps - 1) / kQ4Warps);
+    return launch_pdl(k_q4_mt<G, NTL>, dim3(grid), dim3(kQ4Threads), smem, s, P);
+}
+
 template <int G>
 static int launch_q4_mt(Q4Params& P, cudaStream_t s) {
-    // warps along the columns: enough of them to fill the SMs when few row blocks are touched
-    const int rb = P.tok == 16 ? 1 : 2;
-    const int64_t tasks = (int64_t)std::min(P.pairs, P.E) * ((P.M.nblk + rb - 1) / rb);
-    const int64_t want = 148 * 24;
-    P.ksplit = tasks >= want ? 1 : 2 * tasks >= want ? 2 : 4 * tasks >= want ? 4 : 8;
-    const int per_cta = kQ4Warps / P.ksplit * rb;
-    if (P.slots > 65535) return BITSMOE_EINVAL;
-    const dim3 grid((unsigned)((P.M.nblk + per_cta - 1) / per_cta), (unsigned)P.slots), block(kQ4Threads);
-    if (P.tok == 4) return launch_pdl(k_q4_mt<G, 1, 2, 2>, grid, block, 0, s, P);
-    if (P.tok == 8) return launch_pdl(k_q4_mt<G, 2, 2, 2>, grid, block, 0, s, P);
-    return launch_pdl(k_q4_mt<G, 4, 1, 4>, grid, block, 0, s, P);
+    if (P.tok == 4) return launch_q4_form<G, 2>(P, s);
+    return launch_q4_form<G, 4>(P, s);
 }
 
 template <int G>
@@ -979,7 +1117,6 @@ BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_q4_args* args, void* stream) {
         return group == 32 ? launch_q4_t1<32>(P, smem, s) : group == 64 ? launch_q4_t1<64>(P, smem, s) : launch_q4_t1<128>(P, smem, s);
     }
     const Q4WS w = q4_ws(dims, group, T, (uint8_t*)a.workspace);
-    P.order = w.order;
     P.pieces = w.pieces;
     P.hb = w.hb;
     P.hsum = w.hsum;
@@ -987,10 +1124,11 @@ BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_q4_args* args, void* stream) {
     P.y = w.y;
     P.tok = q4_tok(P.pairs, P.E);
     P.slots = q4_slots(P.pairs, P.E);
+    q4_ranges(dims, group, P.pairs, P.ksplit, P.kper);
     const dim3 pgrid((unsigned)P.pairs + 1), pblock(kQ4PrepThreads);
-    int rc = group == 32   ? launch_pdl(k_q4_prep<32>, pgrid, pblock, 4ull * P.E, s, P)
-             : group == 64 ? launch_pdl(k_q4_prep<64>, pgrid, pblock, 4ull * P.E, s, P)
-                           : launch_pdl(k_q4_prep<128>, pgrid, pblock, 4ull * P.E, s, P);
+    int rc = group == 32   ? launch_pdl(k_q4_prep<32>, pgrid, pblock, 8ull * P.E, s, P)
+             : group == 64 ? launch_pdl(k_q4_prep<64>, pgrid, pblock, 8ull * P.E, s, P)
+                           : launch_pdl(k_q4_prep<128>, pgrid, pblock, 8ull * P.E, s, P);
     if (rc) return rc;
     rc = group == 32 ? launch_q4_mt<32>(P, s) : group == 64 ? launch_q4_mt<64>(P, s) : launch_q4_mt<128>(P, s);
     if (rc) return rc;

@@ -495,7 +495,7 @@ int bitsmoe_ffn_down_q4_launches(const bitsmoe_ffn_dims* dims, int32_t group, in
 
 /* bitsmoe_ffn_down with the down matrices [d_model][d_ff] in 4 bits.  Routing errors and
  * the slot-order sum as there; products keep fp32 precision (a group's sum is scaled in
- * fp32).  At most 4096 experts. */
+ * fp32).  At most 2048 experts. */
 typedef struct {
     bitsmoe_ffn_dims dims;
     int32_t group, tokens;

@@ -255,7 +255,9 @@ struct Q4Params {
     const float* gw;     // [pairs]
     float* out;          // [T][rows]
     int32_t* status;
-    int32_t* pieces;     // [1 + slots][kQ4Rec]: the first record holds their number; then expert, pairs, pair indexes
+    int32_t* runs;       // [grid + 1] first unit of each CTA of the second launch
+    int grid;            // its CTAs
+    int32_t* pieces;     // [1 + slots][kQ4Rec]: after an unused record, expert, pairs, pair indexes
     uint32_t* hb;        // [pairs][cols_p / 64][4][16] B operands
     float* hsum;         // [pairs][cols_p / G][2]: -7.5 times the groups' sums of hi and of lo
     float* hscale;       // [pairs] value of the fixed-point unit
@@ -265,7 +267,7 @@ struct Q4Params {
     int ksplit;          // ranges of columns (one token: per slot)
     int kper;            // tiles of a range
 };
-constexpr int kQ4Rec = 12;   // ints of a piece's record: expert, pairs in it, cost of the pieces before it, unused, 8 pair indexes
+constexpr int kQ4Rec = 12;   // ints of a piece's record: expert, pairs in it, 2 unused, 8 pair indexes
 constexpr int kQ4Slot0 = 4;
 // Cost of a unit of a piece with np pairs: unpacking the codes, and 2 pairs a block of columns.
 __host__ __device__ constexpr int q4_cost(int np) { return 3 + 2 * (np <= 2 ? 1 : np <= 4 ? 2 : 4); }
@@ -542,7 +544,9 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
     __shared__ int s_carry, s_cost;
     constexpr int KEEP = 8;  // pairs whose expert a thread keeps
     const int tid = threadIdx.x;
-    int* s_first = s_cnt + P.E;  // the expert's first piece
+    int* s_first = s_cnt + P.E;      // the expert's first piece
+    int* s_count = s_cnt + 2 * P.E;  // its pairs
+    int* s_before = s_cnt + 3 * P.E; // the cost of the pieces before its own
     int mine[KEEP];
 #pragma unroll
     for (int i = 0; i < KEEP; i++) {
@@ -576,14 +580,15 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
         if (e < P.E) {
             s_cnt[e] = 0;  // becomes the place of the expert's next pair
             s_first[e] = first;
+            s_count[e] = n;
         }
         const int cost = np > 0 ? (np - 1) * q4_cost(P.tok) + q4_cost(n - (np - 1) * P.tok) : 0;
         const int before = cta_scan<kQ4PrepThreads>(cost, s_warp) + s_cost - cost;
+        if (e < P.E) s_before[e] = before;
         for (int i = 0; i < np; i++) {
             int32_t* rec = P.pieces + (int64_t)(1 + first + i) * kQ4Rec;
             rec[0] = e;
             rec[1] = min(P.tok, n - i * P.tok);
-            rec[2] = before + i * q4_cost(P.tok);
         }
         __syncthreads();
         if (tid == kQ4PrepThreads - 1) {
@@ -592,9 +597,29 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
         }
         __syncthreads();
     }
-    if (tid == 0) {
-        P.pieces[0] = s_carry;
-        P.pieces[2] = s_cost;
+    // Runs of equal cost: CTA b starts at the first unit at or after its share of the cost
+    // (units are numbered over the pieces).
+    const int per_piece = P.ksplit * P.M.nblk;
+    const int64_t all = (int64_t)s_cost * per_piece;  // cost of all units
+    for (int b = tid; b <= P.grid; b += kQ4PrepThreads) {
+        int unit = s_carry * per_piece;
+        const int64_t at = all / P.grid * b + all % P.grid * b / P.grid;
+        if (b < P.grid && s_carry > 0) {
+            int lo = 0, hi = P.E;  // the last expert whose pieces start at or before `at`: it has some
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_before[mid] * (int64_t)per_piece <= at)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int n = s_count[lo], np = (n + P.tok - 1) / P.tok, full = q4_cost(P.tok);
+            const int64_t off = at - s_before[lo] * (int64_t)per_piece;
+            const int i = (int)min((int64_t)np - 1, off / ((int64_t)full * per_piece));
+            const int cost = q4_cost(min(P.tok, n - i * P.tok));
+            unit = (s_first[lo] + i) * per_piece + (int)((off - (int64_t)i * full * per_piece + cost - 1) / cost);
+        }
+        P.runs[b] = unit;
     }
     // a pair's place inside its group may vary; its result does not depend on it
     each([&](int p, int e) {
@@ -606,7 +631,7 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
 
 template <int G>
 __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
-    extern __shared__ int32_t s_cnt[];  // [E] counts, [E] first pieces (the grouping CTA)
+    extern __shared__ int32_t s_cnt[];  // [4 E]: see q4_group
     __shared__ unsigned s_max;
     const int tid = threadIdx.x;
     pdl_wait();
@@ -741,9 +766,9 @@ template <int G, int NTL>
 struct Q4Piece {
     const uint32_t* hb[NTL];  // B operands of column g: digit g mod 4 of pair g / 4; past the last pair, that one
     const float* sums[NTL];   // -7.5 sum h of the accumulator columns 2c and 2c + 1: 2 digits of pair c / 2
-    int pair[NTL];            // that pair
 
-    __device__ __forceinline__ void set(const Q4Params& P, const int32_t* rec, int np, int t0, int lane) {
+    // pair: out, the pair c / 2 of each block.
+    __device__ __forceinline__ void set(const Q4Params& P, const int32_t* rec, int np, int t0, int lane, int (&pair)[NTL]) {
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
         for (int j = 0; j < NTL; j++) {
@@ -751,6 +776,13 @@ struct Q4Piece {
             pair[j] = rec[kQ4Slot0 + min(2 * j + c / 2, np - 1)];
             hb[j] = P.hb + (int64_t)col * P.M.cols_p + 16 * (g & 3) + 4 * c + t0 * kQ4BTile;
             sums[j] = P.hsum + ((int64_t)pair[j] * (P.M.cols_p / G) + t0 * kQ4Cols / G) * 2 + (c & 1);
+        }
+    }
+    __device__ __forceinline__ void back(int n) {  // n tiles
+#pragma unroll
+        for (int j = 0; j < NTL; j++) {
+            hb[j] -= n * kQ4BTile;
+            sums[j] -= n * kQ4Cols / G * 2;
         }
     }
 };
@@ -780,7 +812,7 @@ __device__ __forceinline__ void q4_tiles(const uint8_t* codes, const uint16_t* s
         q4_tile<G, NB, NTL>(w, s, bw, start, u & 1, part, acc);
     }
 #pragma unroll
-    for (int j = 0; j < NB; j++) {
+    for (int j = 0; j < NTL; j++) {  // of every block: back() takes them all back
         piece.hb[j] += U * kQ4BTile;
         piece.sums[j] += U * kQ4Cols / G * 2;
     }
@@ -825,51 +857,63 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_mt(const Q4Params P) {
     ring.init(s_ring + warp * (kQ4Stages * kQ4StageBytes), s_bar[warp], lane);
     pdl_wait();
     pdl_trigger();
-    const int npieces = P.pieces[0];
-    const int per_piece = P.ksplit * nblk;  // units of a piece
-    // first unit (numbered over the pieces) at or after a share b / gridDim.x of the cost
-    auto unit_at = [&](int b) -> int {
-        const int64_t at = (int64_t)P.pieces[2] * per_piece * b / gridDim.x;
-        int lo = 0;  // the last piece that starts at or before `at` is one of n from lo on
-        for (int n = npieces; n > 1;) {
-            const int w = (n + 31) / 32, i = lane * w;
-            const bool below = i < n && P.pieces[(int64_t)(1 + lo + i) * kQ4Rec + 2] * (int64_t)per_piece <= at;
-            const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));  // lane 0 is always below
-            lo += k * w;
-            n = min(w, n - k * w);
+    // this warp's units: block blk of part (piece, range), every kQ4Warps-th of the CTA's run
+    const int* run = P.runs + blockIdx.x;
+    const int u0 = run[0] + warp, left0 = (run[1] - u0 + kQ4Warps - 1) / kQ4Warps;
+    if (left0 <= 0) return;
+    struct Cursor {
+        int left, part, blk;
+        __device__ __forceinline__ bool next(int nblk) {  // true when the part changes
+            left--;
+            blk += kQ4Warps;
+            const bool moved = blk >= nblk;
+            while (blk >= nblk) {
+                blk -= nblk;
+                part++;
+            }
+            return moved;
         }
-        const int32_t* rec = P.pieces + (int64_t)(1 + lo) * kQ4Rec;
-        const int64_t off = at - rec[2] * (int64_t)per_piece;
-        const int w = q4_cost(rec[1]);
-        return lo * per_piece + (int)min((int64_t)per_piece, (off + w - 1) / w);
     };
-    if (npieces == 0) return;
-    const int u0 = unit_at(blockIdx.x) + warp;
-    const int u1 = blockIdx.x + 1 == gridDim.x ? npieces * per_piece : unit_at(blockIdx.x + 1);
-    // producer: the next stage to fill starts at tile pt (below pt1) of unit pu
-    int pu = u0;
+    Cursor in{left0, u0 / nblk, u0 % nblk}, cur = in;
+    // producer: the next stage to fill starts at tile pt (below pt1) of unit `in`
+    const uint8_t* experts = nullptr;
     int pt = 0, pt1 = 0;
-    const uint8_t* pblock = nullptr;
+    auto enter = [&]() {  // the part of `in`
+        experts = P.M.blob + (int64_t)P.pieces[(int64_t)(1 + in.part / P.ksplit) * kQ4Rec] * nblk * bb;
+        pt = in.part % P.ksplit * P.kper;
+        pt1 = min(ntiles, pt + P.kper);
+    };
+    enter();
     auto fill = [&]() {
-        if (pu >= u1) return;
-        if (pt == pt1) {
-            const int part = pu / nblk, e = P.pieces[(int64_t)(1 + part / P.ksplit) * kQ4Rec];
-            pblock = P.M.blob + ((int64_t)e * nblk + pu % nblk) * bb;
-            pt = part % P.ksplit * P.kper;
-            pt1 = min(ntiles, pt + P.kper);
-        }
+        if (in.left <= 0) return;
         const int n = min(kQ4CT, pt1 - pt);
-        ring.fill(P, pblock, pt, n, lane);
+        ring.fill(P, experts + in.blk * bb, pt, n, lane);
         pt += n;
-        if (pt == pt1) pu += kQ4Warps;
+        if (pt < pt1) return;
+        pt -= min(P.kper, ntiles - in.part % P.ksplit * P.kper);  // back to the range's first tile
+        if (in.next(nblk) && in.left > 0) enter();
     };
     for (int i = 0; i < kQ4Stages; i++) fill();
-    for (int u = u0; u < u1; u += kQ4Warps) {
-        const int part = u / nblk, kp = part % P.ksplit;
-        const int32_t* rec = P.pieces + (int64_t)(1 + part / P.ksplit) * kQ4Rec;
-        const int np = rec[1], t0 = kp * P.kper, t1 = min(ntiles, t0 + P.kper);
-        Q4Piece<G, NTL> piece;
-        piece.set(P, rec, np, t0, lane);
+    bool moved = true;
+    int np = 0, kp = 0, t0 = 0, t1 = 0;
+    Q4Piece<G, NTL> piece;
+    float unit[NTL];
+    float* y[NTL];
+    while (cur.left > 0) {
+        if (moved) {
+            const int32_t* rec = P.pieces + (int64_t)(1 + cur.part / P.ksplit) * kQ4Rec;
+            np = rec[1];
+            kp = cur.part % P.ksplit;
+            t0 = kp * P.kper;
+            t1 = min(ntiles, t0 + P.kper);
+            int pair[NTL];
+            piece.set(P, rec, np, t0, lane, pair);
+#pragma unroll
+            for (int j = 0; j < NTL; j++) {
+                unit[j] = P.hscale[pair[j]];
+                y[j] = 2 * j + c / 2 < np ? P.y + ((int64_t)kp * P.pairs + pair[j]) * P.M.rows + g + 8 * (c & 1) : nullptr;
+            }
+        }
         float acc[NTL][2] = {};
         for (int t = t0; t < t1; t += kQ4CT) {
             if (!ring.wait()) {
@@ -880,13 +924,15 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_mt(const Q4Params P) {
             ring.pop();
             fill();
         }
-        const int row = u % nblk * kQ4Rows + g + 8 * (c & 1);
+        piece.back(t1 - t0);
+        const int row0 = cur.blk * kQ4Rows;
+        const bool in_rows = row0 + g + 8 * (c & 1) < P.M.rows;
 #pragma unroll
         for (int j = 0; j < NTL; j++) {
             const float r = q4_join(acc[j], lane);
-            if (2 * j + c / 2 < np && row < P.M.rows)
-                P.y[((int64_t)kp * P.pairs + piece.pair[j]) * P.M.rows + row] = r * P.hscale[piece.pair[j]];
+            if (y[j] && in_rows) y[j][row0] = r * unit[j];
         }
+        moved = cur.next(nblk);
     }
 }
 
@@ -924,7 +970,7 @@ __global__ void __launch_bounds__(256) k_q4_sum(const Q4Params P) {
 // host side
 // ---------------------------------------------------------------------------
 constexpr int kQ4Sms = 148;    // SMs the launches are sized for
-constexpr int kQ4MaxE = 4096;  // the grouping counts them in shared memory (32 KB)
+constexpr int kQ4MaxE = 2048;  // the grouping keeps 4 numbers of each in shared memory (32 KB)
 
 // Pairs per piece, by the expected group size.  8 at most: the sums of more do not fit the registers.
 static int q4_tok(int pairs, int E) { return pairs / E <= 3 ? 4 : 8; }
@@ -942,6 +988,7 @@ static bool q4_single(const bitsmoe_ffn_dims* d, int group, int T) {
 }
 
 struct Q4WS {
+    int32_t* runs;
     int32_t* pieces;
     uint32_t* hb;
     float* hsum;
@@ -975,6 +1022,7 @@ static Q4WS q4_ws(const bitsmoe_ffn_dims* d, int group, int T, uint8_t* base) {
     const uint64_t pairs = (uint64_t)T * d->top_k, dp = q4_cols_padded(d->d_ff, group);
     int ksplit, kper;
     q4_ranges(d, group, (int64_t)pairs, ksplit, kper);
+    w.runs = (int32_t*)take(4ull * (2 * kQ4Sms + 1));
     w.pieces = (int32_t*)take(4ull * kQ4Rec * (1 + q4_slots((int)pairs, d->n_experts)));
     w.hb = (uint32_t*)take(4 * pairs * dp);
     w.hsum = (float*)take(8 * pairs * (dp / group));
@@ -992,13 +1040,10 @@ static bool q4_dims_ok(const bitsmoe_ffn_dims* d, int group, int T) {
 
 template <int G, int NTL>
 static int launch_q4_form(Q4Params& P, cudaStream_t s) {
-    const int64_t most = (int64_t)P.slots * P.ksplit * P.M.nblk;
-    if (most > 0x7fffffff) return BITSMOE_EINVAL;
     const int smem = kQ4Warps * kQ4Stages * kQ4StageBytes;
     const cudaError_t e = cudaFuncSetAttribute(k_q4_mt<G, NTL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return set_cuda_error(e);
-    const unsigned grid = (unsigned)std::min<int64_t>(2 * kQ4Sms, (most + kQ4Warps - 1) / kQ4Warps);
-    return launch_pdl(k_q4_mt<G, NTL>, dim3(grid), dim3(kQ4Threads), smem, s, P);
+    return launch_pdl(k_q4_mt<G, NTL>, dim3((unsigned)P.grid), dim3(kQ4Threads), smem, s, P);
 }
 
 template <int G>
@@ -1117,6 +1162,7 @@ BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_q4_args* args, void* stream) {
         return group == 32 ? launch_q4_t1<32>(P, smem, s) : group == 64 ? launch_q4_t1<64>(P, smem, s) : launch_q4_t1<128>(P, smem, s);
     }
     const Q4WS w = q4_ws(dims, group, T, (uint8_t*)a.workspace);
+    P.runs = w.runs;
     P.pieces = w.pieces;
     P.hb = w.hb;
     P.hsum = w.hsum;
@@ -1125,10 +1171,13 @@ BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_q4_args* args, void* stream) {
     P.tok = q4_tok(P.pairs, P.E);
     P.slots = q4_slots(P.pairs, P.E);
     q4_ranges(dims, group, P.pairs, P.ksplit, P.kper);
+    const int64_t most = (int64_t)P.slots * P.ksplit * P.M.nblk;  // units, at least as many as there are
+    if (most > 0x7fffffff) return BITSMOE_EINVAL;
+    P.grid = (int)std::min<int64_t>(2 * kQ4Sms, (most + kQ4Warps - 1) / kQ4Warps);
     const dim3 pgrid((unsigned)P.pairs + 1), pblock(kQ4PrepThreads);
-    int rc = group == 32   ? launch_pdl(k_q4_prep<32>, pgrid, pblock, 8ull * P.E, s, P)
-             : group == 64 ? launch_pdl(k_q4_prep<64>, pgrid, pblock, 8ull * P.E, s, P)
-                           : launch_pdl(k_q4_prep<128>, pgrid, pblock, 8ull * P.E, s, P);
+    int rc = group == 32   ? launch_pdl(k_q4_prep<32>, pgrid, pblock, 16ull * P.E, s, P)
+             : group == 64 ? launch_pdl(k_q4_prep<64>, pgrid, pblock, 16ull * P.E, s, P)
+                           : launch_pdl(k_q4_prep<128>, pgrid, pblock, 16ull * P.E, s, P);
     if (rc) return rc;
     rc = group == 32 ? launch_q4_mt<32>(P, s) : group == 64 ? launch_q4_mt<64>(P, s) : launch_q4_mt<128>(P, s);
     if (rc) return rc;

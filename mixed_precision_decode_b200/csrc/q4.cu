@@ -537,12 +537,12 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
 // First launch: the first CTA groups the pairs by expert and cuts the groups into
 // pieces of `tok` pairs; every other CTA forms h, its scale and its B operands for one
 // pair (independent of the grouping).
-constexpr int kQ4PrepThreads = 256;
 
+template <int THREADS>
 __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
     __shared__ int s_warp[32];
     __shared__ int s_carry, s_cost;
-    constexpr int KEEP = 8;  // pairs whose expert a thread keeps
+    constexpr int KEEP = 2048 / THREADS;  // pairs whose expert a thread keeps
     const int tid = threadIdx.x;
     int* s_first = s_cnt + P.E;      // the expert's first piece
     int* s_count = s_cnt + 2 * P.E;  // its pairs
@@ -550,18 +550,18 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
     int mine[KEEP];
 #pragma unroll
     for (int i = 0; i < KEEP; i++) {
-        const int p = tid + i * kQ4PrepThreads;
+        const int p = tid + i * THREADS;
         mine[i] = p < P.pairs ? P.ids[p] : -1;
     }
-    for (int e = tid; e < P.E; e += kQ4PrepThreads) s_cnt[e] = 0;
+    for (int e = tid; e < P.E; e += THREADS) s_cnt[e] = 0;
     if (tid == 0) s_carry = s_cost = 0;
     __syncthreads();
     bool bad = false;
     auto each = [&](auto&& f) {  // every pair of this thread with its expert, -1 for a bad one
 #pragma unroll
         for (int i = 0; i < KEEP; i++)
-            if (tid + i * kQ4PrepThreads < P.pairs) f(tid + i * kQ4PrepThreads, mine[i] < P.E ? mine[i] : -1);
-        for (int p = tid + KEEP * kQ4PrepThreads; p < P.pairs; p += kQ4PrepThreads) {
+            if (tid + i * THREADS < P.pairs) f(tid + i * THREADS, mine[i] < P.E ? mine[i] : -1);
+        for (int p = tid + KEEP * THREADS; p < P.pairs; p += THREADS) {
             const int e = P.ids[p];
             f(p, e < P.E ? e : -1);
         }
@@ -574,16 +574,16 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
     });
     if (bad && P.status) atomicOr(P.status, BITSMOE_ST_BADEXPERT);
     __syncthreads();
-    for (int e0 = 0; e0 < P.E; e0 += kQ4PrepThreads) {
+    for (int e0 = 0; e0 < P.E; e0 += THREADS) {
         const int e = e0 + tid, n = e < P.E ? s_cnt[e] : 0, np = (n + P.tok - 1) / P.tok;
-        const int first = cta_scan<kQ4PrepThreads>(np, s_warp) + s_carry - np;
+        const int first = cta_scan<THREADS>(np, s_warp) + s_carry - np;
         if (e < P.E) {
             s_cnt[e] = 0;  // becomes the place of the expert's next pair
             s_first[e] = first;
             s_count[e] = n;
         }
         const int cost = np > 0 ? (np - 1) * q4_cost(P.tok) + q4_cost(n - (np - 1) * P.tok) : 0;
-        const int before = cta_scan<kQ4PrepThreads>(cost, s_warp) + s_cost - cost;
+        const int before = cta_scan<THREADS>(cost, s_warp) + s_cost - cost;
         if (e < P.E) s_before[e] = before;
         for (int i = 0; i < np; i++) {
             int32_t* rec = P.pieces + (int64_t)(1 + first + i) * kQ4Rec;
@@ -591,7 +591,7 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
             rec[1] = min(P.tok, n - i * P.tok);
         }
         __syncthreads();
-        if (tid == kQ4PrepThreads - 1) {
+        if (tid == THREADS - 1) {
             s_carry = first + np;
             s_cost = before + cost;
         }
@@ -601,7 +601,7 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
     // (units are numbered over the pieces).
     const int per_piece = P.ksplit * P.M.nblk;
     const int64_t all = (int64_t)s_cost * per_piece;  // cost of all units
-    for (int b = tid; b <= P.grid; b += kQ4PrepThreads) {
+    for (int b = tid; b <= P.grid; b += THREADS) {
         int unit = s_carry * per_piece;
         const int64_t at = all / P.grid * b + all % P.grid * b / P.grid;
         if (b < P.grid && s_carry > 0) {
@@ -629,15 +629,15 @@ __device__ void q4_group(const Q4Params& P, int32_t* s_cnt) {
     });
 }
 
-template <int G>
-__global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
+template <int G, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_q4_prep(const Q4Params P) {
     extern __shared__ int32_t s_cnt[];  // [4 E]: see q4_group
     __shared__ unsigned s_max;
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0) {
-        q4_group(P, s_cnt);
+        q4_group<THREADS>(P, s_cnt);
         return;
     }
     const int pair = (int)blockIdx.x - 1, e = P.ids[pair];
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
     h_of(tid, kept);
 #pragma unroll
     for (int i = 0; i < 16; i++) m = max(m, __float_as_uint(fabsf(kept[i])));
-    for (int ch = tid + kQ4PrepThreads; ch < nch; ch += kQ4PrepThreads) {
+    for (int ch = tid + THREADS; ch < nch; ch += THREADS) {
         float v[16];
         h_of(ch, v);
 #pragma unroll
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(kQ4PrepThreads) k_q4_prep(const Q4Params P) {
         }
     };
     put(tid, kept);
-    for (int c0 = kQ4PrepThreads; c0 < nch; c0 += kQ4PrepThreads) {  // whole warps
+    for (int c0 = THREADS; c0 < nch; c0 += THREADS) {  // whole warps
         float v[16];
         h_of(c0 + tid, v);
         put(c0 + tid, v);
@@ -1038,6 +1038,16 @@ static bool q4_dims_ok(const bitsmoe_ffn_dims* d, int group, int T) {
            d->d_ff <= (1 << 30) && d->d_model <= (1 << 30);
 }
 
+// A thread per 16 columns of a pair, in one pass where 1024 threads are enough: 14,336 columns
+// took 5 us more with 256.
+template <int G>
+static int launch_q4_prep(const Q4Params& P, cudaStream_t s) {
+    const dim3 grid((unsigned)P.pairs + 1);
+    const size_t smem = 16ull * P.E;
+    return P.M.cols_p / 16 <= 256 ? launch_pdl(k_q4_prep<G, 256>, grid, dim3(256), smem, s, P)
+                                  : launch_pdl(k_q4_prep<G, 1024>, grid, dim3(1024), smem, s, P);
+}
+
 template <int G, int NTL>
 static int launch_q4_form(Q4Params& P, cudaStream_t s) {
     const int smem = kQ4Warps * kQ4Stages * kQ4StageBytes;
@@ -1174,10 +1184,7 @@ BITSMOE_API int bitsmoe_ffn_down_q4(const bitsmoe_q4_args* args, void* stream) {
     const int64_t most = (int64_t)P.slots * P.ksplit * P.M.nblk;  // units, at least as many as there are
     if (most > 0x7fffffff) return BITSMOE_EINVAL;
     P.grid = (int)std::min<int64_t>(2 * kQ4Sms, (most + kQ4Warps - 1) / kQ4Warps);
-    const dim3 pgrid((unsigned)P.pairs + 1), pblock(kQ4PrepThreads);
-    int rc = group == 32   ? launch_pdl(k_q4_prep<32>, pgrid, pblock, 16ull * P.E, s, P)
-             : group == 64 ? launch_pdl(k_q4_prep<64>, pgrid, pblock, 16ull * P.E, s, P)
-                           : launch_pdl(k_q4_prep<128>, pgrid, pblock, 16ull * P.E, s, P);
+    int rc = group == 32 ? launch_q4_prep<32>(P, s) : group == 64 ? launch_q4_prep<64>(P, s) : launch_q4_prep<128>(P, s);
     if (rc) return rc;
     rc = group == 32 ? launch_q4_mt<32>(P, s) : group == 64 ? launch_q4_mt<64>(P, s) : launch_q4_mt<128>(P, s);
     if (rc) return rc;

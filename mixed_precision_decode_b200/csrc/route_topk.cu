@@ -11,14 +11,18 @@
 // Groups: pairs p = t top_k + slot sorted by expert, ascending p inside an expert
 // (a stable counting sort, so the order does not depend on timing), -1 behind them.
 //
-// A warp owns a token: logits in registers as order-preserving integers, one pick =
-// a lane-local maximum, one warp-wide integer maximum and, among the lanes that
-// hold it, one warp-wide minimum of the expert index (two `redux` instructions).
-// The sort counts with warp matches instead of atomics.  Up to kRouteOneTokens tokens
-// one CTA does both (one launch); beyond, the picks and each CTA's expert counts are
-// one launch and the placement -- every CTA sums the counts of the CTAs before it --
-// a second.  Both are latency-bound: the bytes (T E logits, T top_k x 12 out) are
-// a microsecond of HBM at 16,384 tokens.
+// A warp owns a token: logits in registers as order-preserving integers.  Up to 128
+// experts a lane sorts its four first, a pick is one warp-wide integer maximum of the
+// lanes' heads and a vote for who holds it, and two tokens go through a warp together,
+// so that one's instructions run in the other's latencies; with more experts a pick is a
+// lane-local maximum, a warp-wide one and, among the lanes that hold it, a warp-wide
+// minimum of the expert index.
+// The sort: a token's experts differ, so a pair's place inside its group is the number of
+// earlier tokens that picked the same expert: a bit per token and expert in shared memory,
+// and population counts.  Up to kRouteOneTokens tokens one CTA does both (one launch);
+// beyond, the picks and each CTA's expert counts are one launch and the placement -- every
+// CTA sums the counts of the CTAs before it -- a second.  Both are latency-bound: the bytes
+// (T E logits, T top_k x 12 out) are a microsecond of HBM at 16,384 tokens.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -28,10 +32,10 @@ namespace bitsmoe {
 constexpr int kRtThreads = 1024;
 constexpr int kRtWarps = kRtThreads / 32;
 constexpr int kRouteOneTokens = 128;  // tokens one CTA routes and groups
-constexpr int kRouteMaxBlocks = 296;  // CTAs of the two-launch path: two per SM
+constexpr int kRouteMaxBlocks = 148;  // CTAs of the two-launch path: one per SM (each sums the others' counts)
 constexpr int kRouteMaxE = 8192;
 constexpr int kRouteMaxK = 1024;
-constexpr int kRouteHistInts = 11264;  // ints of shared memory for the per-warp expert counts (44 KB)
+constexpr int kRouteBitInts = 8192;   // ints of shared memory for the bits (32 KB), if 32 tokens' fit them
 
 struct RouteParams {
     const void* logits;
@@ -43,10 +47,10 @@ struct RouteParams {
     float* gw;         // [T][K]
     int32_t* offsets;  // [E+1] or NULL
     int32_t* order;    // [T*K] or NULL
-    int32_t* hist;     // [nb][E] expert counts of each CTA's tokens (two-launch path)
+    int32_t* hist;     // [E][nb] expert counts of each CTA's tokens (two-launch path)
     int32_t* status;
     int tpb;  // tokens per CTA
-    int nw;   // warps that count in the placement (their counts fit shared memory)
+    int words;  // 32-token words of bits per expert
 };
 
 // Order-preserving integer of a finite logit or -inf (-0 and +0 are equal).
@@ -195,63 +199,150 @@ __device__ void route_token(const RouteParams& P, int t, int lane) {
     }
 }
 
-__device__ __forceinline__ int pair_expert(const RouteParams& P, int p, int p1) { return p < p1 ? P.ids[p] : -1; }
-
-// Counts (or places) the pairs [p0, p1) of one warp's share in ascending order; cnt
-// [E]: the warp's counts, or the position of its next pair of each expert.
-template <bool PLACE>
-__device__ void walk_pairs(const RouteParams& P, int p0, int p1, int32_t* cnt, int lane) {
-    for (int q = p0; q < p1; q += 32) {
-        const int e = pair_expert(P, q + lane, p1);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        if (e >= 0) {
-            const int base = cnt[e];
-            if (PLACE) P.order[base + before] = q + lane;
+// R tokens by one warp: at most 32 NV <= 128 experts and 32 picks.  A row that is not
+// finite is routed as if every expert were closed.  t[r] < 0: no token.
+template <int NV, int R>
+__device__ __forceinline__ void route_tokens(const RouteParams& P, const int (&t)[R], int lane) {
+    uint32_t key[R][NV];
+    int from[R][NV];  // the keys' experts, / 32
+    float m[R], my_l[R];
+    int my_id[R];
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const int e = lane + 32 * j;
+            key[r][j] = __float_as_uint(t[r] >= 0 && e < P.E ? load_logit(P, (int64_t)t[r] * P.ld, e) : -INFINITY);
         }
-        __syncwarp();
-        if (e >= 0 && before == 0) cnt[e] += __popc(same);
-        __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const float v = __uint_as_float(key[r][j]);
+            bad |= !(v < INFINITY);
+            key[r][j] = lane + 32 * j < P.E ? logit_key(v) : 0u;
+            from[r][j] = j;
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad && lane == 0 && P.status) atomicOr(P.status, BITSMOE_ST_NONFINITE);
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+            if (bad) key[r][j] = 0u;
+        // descending; equal keys stay in ascending order of their experts
+#pragma unroll
+        for (int i = 0; i + 1 < NV; i++)
+#pragma unroll
+            for (int j = NV - 2; j >= i; j--) {
+                const bool swap = key[r][j + 1] > key[r][j];
+                const uint32_t hi = swap ? key[r][j + 1] : key[r][j], lo = swap ? key[r][j] : key[r][j + 1];
+                const int fh = swap ? from[r][j + 1] : from[r][j], fl = swap ? from[r][j] : from[r][j + 1];
+                key[r][j] = hi;
+                key[r][j + 1] = lo;
+                from[r][j] = fh;
+                from[r][j + 1] = fl;
+            }
+        my_id[r] = -1;
+        my_l[r] = m[r] = -INFINITY;
+    }
+    for (int k = 0; k < P.K; k++) {
+        uint32_t top[R];
+        unsigned who[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) top[r] = __reduce_max_sync(0xffffffffu, key[r][0]);
+#pragma unroll
+        for (int r = 0; r < R; r++) who[r] = __ballot_sync(0xffffffffu, key[r][0] == top[r]);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const int be = lane + 32 * from[r][0];
+            int e;
+            if (who[r] & (who[r] - 1u))  // equal logits: the lowest expert
+                e = (int)__reduce_min_sync(0xffffffffu, key[r][0] == top[r] ? (uint32_t)be : 0x7fffffffu);
+            else
+                e = __shfl_sync(0xffffffffu, be, __ffs(who[r]) - 1);
+            const bool open = top[r] > kKeyClosed;
+            const float l = open ? key_logit(top[r]) : -INFINITY;
+            if (k == 0) m[r] = l;
+            if (lane == k) {
+                my_id[r] = open ? e : -1;
+                my_l[r] = l;
+            }
+            if (open && be == e) {
+#pragma unroll
+                for (int j = 0; j + 1 < NV; j++) {
+                    key[r][j] = key[r][j + 1];
+                    from[r][j] = from[r][j + 1];
+                }
+                key[r][NV - 1] = 0u;
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const float s = my_id[r] >= 0 ? score_of(P, my_l[r], m[r]) : 0.0f;
+        float total = 1.0f;
+        if (P.renorm) {
+            total = warp_sum(s);
+        } else if (!P.sigmoid) {  // softmax over every expert: the picked ones, and what is left
+            float sum = s;
+#pragma unroll
+            for (int j = 0; j < NV; j++)
+                if (key[r][j] > kKeyClosed) sum += expf(key_logit(key[r][j]) - m[r]);
+            total = warp_sum(sum);
+        }
+        if (t[r] >= 0 && lane < P.K) {
+            P.ids[(int64_t)t[r] * P.K + lane] = my_id[r];
+            P.gw[(int64_t)t[r] * P.K + lane] = my_id[r] >= 0 ? P.scale * (s / total) : 0.0f;
+        }
     }
 }
 
-// Groups the pairs of the CTA's tokens [t0, t1).  nb > 1: the counts of the other
-// CTAs' tokens are in P.hist.  s_cnt [nw][E].
-__device__ void group_pairs(const RouteParams& P, int t0, int t1, int b, int nb, int32_t* s_cnt, int* s_warp) {
+// Groups the pairs of the CTA's tokens [t0, t1).  nb > 1: the counts of every CTA's tokens
+// are in P.hist.  s_base [E], s_bits [E][words].
+__device__ void group_pairs(const RouteParams& P, int t0, int t1, int b, int nb, int32_t* s_base, uint32_t* s_bits,
+                            int* s_warp) {
+    __shared__ int s_total[kRtThreads], s_before[kRtThreads];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int p0 = t0 * P.K, n = (t1 - t0) * P.K;
-    const int share = (int)roundup((uint64_t)((n + P.nw - 1) / P.nw), 32);
-    const int w0 = min(n, warp * share), w1 = min(n, (warp + 1) * share);
-    for (int i = tid; i < P.nw * P.E; i += kRtThreads) s_cnt[i] = 0;
-    __syncthreads();
-    if (warp < P.nw && P.order) walk_pairs<false>(P, p0 + w0, p0 + w1, s_cnt + warp * P.E, lane);
-    if (!P.order && warp == 0) walk_pairs<false>(P, p0, p0 + n, s_cnt, lane);  // offsets alone
-    __syncthreads();
-    // per expert: the pairs of the CTAs before this one, of all CTAs, and of the warps before each
+    if (nb == 1) {
+        for (int e = tid; e < P.E; e += kRtThreads) s_base[e] = 0;
+        __syncthreads();
+        for (int p = t0 * P.K + tid; p < t1 * P.K; p += kRtThreads) {
+            const int e = P.ids[p];
+            if (e >= 0) atomicAdd(&s_base[e], 1);  // counts: the order of the additions does not matter
+        }
+        __syncthreads();
+    }
+    // per expert: the pairs of all CTAs, and of the CTAs before this one; then where its first pair goes
     int carry = 0;
     for (int e0 = 0; e0 < P.E; e0 += kRtThreads) {
         const int e = e0 + tid;
-        int before = 0, total = 0, mine = 0;
-        if (e < P.E) {
-            for (int w = 0; w < P.nw; w++) mine += s_cnt[w * P.E + e];
-            total = mine;
-            if (nb > 1) {
-                total = 0;
-                for (int q = 0; q < nb; q++) {
-                    const int c = P.hist[(int64_t)q * P.E + e];
-                    total += c;
-                    if (q < b) before += c;
+        if (nb > 1) {  // a warp sums four experts' counts at a time, lanes over the CTAs
+            const int ne = min(kRtThreads, P.E - e0);
+            for (int i = warp; i < ne; i += 4 * kRtWarps) {
+                int total[4] = {}, before[4] = {};
+#pragma unroll 2
+                for (int q = lane; q < nb; q += 32)
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        const int c = i + x * kRtWarps < ne ? P.hist[(int64_t)(e0 + i + x * kRtWarps) * nb + q] : 0;
+                        total[x] += c;
+                        if (q < b) before[x] += c;
+                    }
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    const int t = __reduce_add_sync(0xffffffffu, total[x]), f = __reduce_add_sync(0xffffffffu, before[x]);
+                    if (lane == 0 && i + x * kRtWarps < ne) {
+                        s_total[i + x * kRtWarps] = t;
+                        s_before[i + x * kRtWarps] = f;
+                    }
                 }
             }
+            __syncthreads();
         }
+        const int total = e >= P.E ? 0 : nb > 1 ? s_total[tid] : s_base[e];
         const int end = carry + cta_scan<kRtThreads>(total, s_warp);
         if (e < P.E) {
-            int run = end - total + before;
-            for (int w = 0; w < P.nw; w++) {
-                const int c = s_cnt[w * P.E + e];
-                s_cnt[w * P.E + e] = run;
-                run += c;
-            }
+            s_base[e] = end - total + (nb > 1 ? s_before[tid] : 0);
             if (b == 0 && P.offsets) {
                 P.offsets[e + 1] = end;
                 if (e == 0) P.offsets[0] = 0;
@@ -263,7 +354,30 @@ __device__ void group_pairs(const RouteParams& P, int t0, int t1, int b, int nb,
         __syncthreads();
     }
     if (!P.order) return;
-    if (warp < P.nw) walk_pairs<true>(P, p0 + w0, p0 + w1, s_cnt + warp * P.E, lane);
+    const int span = 32 * P.words;  // tokens whose bits fit
+    for (int c0 = t0; c0 < t1; c0 += span) {
+        const int p0 = c0 * P.K, p1 = min(t1, c0 + span) * P.K;
+        for (int i = tid; i < P.E * P.words; i += kRtThreads) s_bits[i] = 0u;
+        __syncthreads();
+        for (int p = p0 + tid; p < p1; p += kRtThreads) {
+            const int e = P.ids[p], t = p / P.K - c0;
+            if (e >= 0) atomicOr(&s_bits[e * P.words + (t >> 5)], 1u << (t & 31));
+        }
+        __syncthreads();
+        for (int p = p0 + tid; p < p1; p += kRtThreads) {
+            const int e = P.ids[p], t = p / P.K - c0;
+            if (e < 0) continue;
+            const uint32_t* w = s_bits + e * P.words;
+            int at = s_base[e] + __popc(w[t >> 5] & ((1u << (t & 31)) - 1u));
+            for (int i = 0; i < t >> 5; i++) at += __popc(w[i]);
+            P.order[at] = p;
+        }
+        if (c0 + span >= t1) break;
+        __syncthreads();
+        for (int e = tid; e < P.E; e += kRtThreads)
+            for (int i = 0; i < P.words; i++) s_base[e] += __popc(s_bits[e * P.words + i]);
+        __syncthreads();
+    }
     if (b == nb - 1)  // the places behind the last pair
         for (int p = carry + tid; p < P.T * P.K; p += kRtThreads) P.order[p] = -1;
 }
@@ -272,36 +386,49 @@ __device__ void group_pairs(const RouteParams& P, int t0, int t1, int b, int nb,
 // each expert's count in P.hist.
 template <int NV>
 __global__ void __launch_bounds__(kRtThreads) k_topk_route(const RouteParams P) {
-    extern __shared__ int32_t s_cnt[];
+    extern __shared__ int32_t s_base[];
     __shared__ int s_warp[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = (int)blockIdx.x * P.tpb, t1 = min(P.T, t0 + P.tpb);
     pdl_wait();
     pdl_trigger();
-    for (int t = t0 + warp; t < t1; t += kRtWarps) route_token<NV>(P, t, lane);
+    if (NV >= 1 && NV <= 4 && P.K <= 32) {
+        constexpr int N = NV < 1 ? 1 : NV > 4 ? 4 : NV;
+        int t = t0 + warp;
+        for (; t + kRtWarps < t1; t += 2 * kRtWarps) {
+            const int two[2] = {t, t + kRtWarps};
+            route_tokens<N, 2>(P, two, lane);
+        }
+        if (t < t1) {
+            const int one[1] = {t};
+            route_tokens<N, 1>(P, one, lane);
+        }
+    } else {
+        for (int t = t0 + warp; t < t1; t += kRtWarps) route_token<NV>(P, t, lane);
+    }
     if (!P.offsets && !P.order) return;
     __syncthreads();  // the CTA's ids are written
     if (gridDim.x == 1) {
-        group_pairs(P, t0, t1, 0, 1, s_cnt, s_warp);
+        group_pairs(P, t0, t1, 0, 1, s_base, reinterpret_cast<uint32_t*>(s_base + P.E), s_warp);
         return;
     }
-    for (int e = threadIdx.x; e < P.E; e += kRtThreads) s_cnt[e] = 0;
+    for (int e = threadIdx.x; e < P.E; e += kRtThreads) s_base[e] = 0;
     __syncthreads();
     for (int p = t0 * P.K + threadIdx.x; p < t1 * P.K; p += kRtThreads) {
         const int e = P.ids[p];
-        if (e >= 0) atomicAdd(&s_cnt[e], 1);  // counts: the order of the additions does not matter
+        if (e >= 0) atomicAdd(&s_base[e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < P.E; e += kRtThreads) P.hist[(int64_t)blockIdx.x * P.E + e] = s_cnt[e];
+    for (int e = threadIdx.x; e < P.E; e += kRtThreads) P.hist[(int64_t)e * gridDim.x + blockIdx.x] = s_base[e];
 }
 
 __global__ void __launch_bounds__(kRtThreads) k_group_pairs(const RouteParams P) {
-    extern __shared__ int32_t s_cnt[];
+    extern __shared__ int32_t s_base[];
     __shared__ int s_warp[32];
     const int t0 = (int)blockIdx.x * P.tpb, t1 = min(P.T, t0 + P.tpb);
     pdl_wait();
     pdl_trigger();
-    group_pairs(P, t0, t1, (int)blockIdx.x, (int)gridDim.x, s_cnt, s_warp);
+    group_pairs(P, t0, t1, (int)blockIdx.x, (int)gridDim.x, s_base, reinterpret_cast<uint32_t*>(s_base + P.E), s_warp);
 }
 
 static int route_blocks(int T) {
@@ -309,8 +436,19 @@ static int route_blocks(int T) {
     return std::min(kRouteMaxBlocks, (T + kRtWarps - 1) / kRtWarps);
 }
 
+constexpr int kRouteSmem = 80 * 1024;  // dynamic shared memory at most (8192 experts)
+
+template <typename K>
+static int grant_route_smem(K kernel, size_t smem) {
+    if (smem <= 36 * 1024) return BITSMOE_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem);
+    return e == cudaSuccess ? BITSMOE_OK : set_cuda_error(e);
+}
+
 template <int NV>
 static int launch_route_kernel(const RouteParams& P, unsigned grid, size_t smem, cudaStream_t s) {
+    const int rc = grant_route_smem(k_topk_route<NV>, smem);
+    if (rc) return rc;
     return launch_pdl(k_topk_route<NV>, dim3(grid), dim3(kRtThreads), smem, s, P);
 }
 
@@ -361,10 +499,10 @@ BITSMOE_API int bitsmoe_topk_route(const bitsmoe_route_args* args, void* stream)
     P.hist = groups && nb > 1 ? (int32_t*)a.workspace : nullptr;
     P.status = a.status;
     P.tpb = (T + nb - 1) / nb;
-    P.nw = std::max(1, std::min(kRtWarps, kRouteHistInts / n_experts));
+    P.words = std::max(1, std::min((P.tpb + 31) / 32, kRouteBitInts / n_experts));
     const unsigned grid = T == 0 ? 1u : (unsigned)((T + P.tpb - 1) / P.tpb);
-    // expert counts: of every counting warp where this CTA places pairs, else one set
-    const size_t smem_group = 4ull * P.nw * n_experts;
+    // the experts' places and, where this CTA places pairs, the bits
+    const size_t smem_group = 4ull * n_experts * (1 + P.words);
     const size_t smem = !groups ? 0 : grid == 1 ? smem_group : 4ull * n_experts;
     int rc;
     if (n_experts <= 32)
@@ -380,5 +518,7 @@ BITSMOE_API int bitsmoe_topk_route(const bitsmoe_route_args* args, void* stream)
     else
         rc = launch_route_kernel<0>(P, grid, smem, s);
     if (rc || !groups || grid == 1) return rc;
+    rc = grant_route_smem(k_group_pairs, smem_group);
+    if (rc) return rc;
     return launch_pdl(k_group_pairs, dim3(grid), dim3(kRtThreads), smem_group, s, P);
 }

@@ -549,6 +549,37 @@ typedef struct {
 /* Errors: EINVAL, ECUDA. */
 int bitsmoe_grouped_matmul(const bitsmoe_gmm_args *args, void *stream);
 
+/* ---- dense experts ----
+ * The routed FFN of experts whose three matrices are dense (a layer before, or without,
+ * the decomposition), from the routing of bitsmoe_topk_route, in three launches:
+ *   h[t][j]   = SiLU(W_gate[e] x[t]) (W_up[e] x[t]),        e = topk_ids[t][j],
+ *   out[t]    = sum_j gate_w[t][j] W_down[e] h[t][j]
+ * -- the gated grouped product of the gathered tokens, the grouped product of h, and the
+ * slot-order sum.  h is rounded to the matrices' type; sums are fp32. */
+typedef struct {
+    bitsmoe_ffn_dims dims;     /* d_model and d_ff multiples of 8 */
+    int32_t tokens;
+    int32_t type;              /* BITSMOE_F16 or BITSMOE_BF16: x and the matrices */
+    const void *x;             /* dev [tokens] rows of d_model elements, x_stride apart (a multiple of 8, >= d_model) */
+    const void *W_gate, *W_up; /* dev [E][d_ff][d_model] */
+    const void *W_down;        /* dev [E][d_model][d_ff]; x and the matrices are 16-byte aligned */
+    const int32_t *topk_ids;   /* dev [tokens][top_k]; a slot without an expert (-1) contributes nothing */
+    const float *gate_w;       /* dev [tokens][top_k] */
+    const int32_t *offsets;    /* dev [E + 1], and */
+    const int32_t *order;      /* dev [tokens top_k]: the grouping of topk_ids */
+    float *out;                /* dev [tokens][d_model] */
+    void *workspace;           /* dev, 256-byte aligned, no initialisation */
+    int32_t *status;           /* dev or NULL */
+    uint64_t workspace_bytes;
+    int64_t x_stride;
+} bitsmoe_dense_ffn_args;
+
+/* Workspace bytes for T tokens (0 for bad dims or T = 0). */
+uint64_t bitsmoe_dense_ffn_workspace_bytes(const bitsmoe_ffn_dims *dims, int32_t T);
+
+/* tokens = 0 is a no-op.  Errors: EINVAL, ESIZE, ECUDA. */
+int bitsmoe_dense_ffn_forward(const bitsmoe_dense_ffn_args *args, void *stream);
+
 /* Waits for `stream`, then copies the device status word to *out_host.
  * Errors: EINVAL, ECUDA. */
 int bitsmoe_read_status(const int32_t *status_dev, void *stream, int32_t *out_host);

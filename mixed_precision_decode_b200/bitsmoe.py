@@ -38,7 +38,7 @@ EXPORTS = (
     "bitsmoe_fqcm_eps", "bitsmoe_fqcm_beta", "bitsmoe_allocate_widths",
     "bitsmoe_norm_residual", "bitsmoe_topk_route_workspace_bytes", "bitsmoe_topk_route", "bitsmoe_q4_bytes",
     "bitsmoe_q4_pack", "bitsmoe_q4_unpack", "bitsmoe_ffn_down_q4_workspace_bytes", "bitsmoe_ffn_down_q4_launches",
-    "bitsmoe_ffn_down_q4", "bitsmoe_grouped_matmul",
+    "bitsmoe_ffn_down_q4", "bitsmoe_grouped_matmul", "bitsmoe_dense_ffn_workspace_bytes", "bitsmoe_dense_ffn_forward",
     "bitsmoe_read_status", "bitsmoe_strerror", "bitsmoe_version",
 )
 
@@ -122,6 +122,8 @@ def lib() -> ctypes.CDLL:
             "bitsmoe_ffn_down_q4_launches": ([ctypes.POINTER(FfnDims), i32, i32], ctypes.c_int),
             "bitsmoe_ffn_down_q4": ([vp, vp], ctypes.c_int),
             "bitsmoe_grouped_matmul": ([vp, vp], ctypes.c_int),
+            "bitsmoe_dense_ffn_workspace_bytes": ([ctypes.POINTER(FfnDims), i32], u64),
+            "bitsmoe_dense_ffn_forward": ([vp, vp], ctypes.c_int),
             "bitsmoe_read_status": ([vp, vp, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
             "bitsmoe_strerror": ([ctypes.c_int], ctypes.c_char_p),
             "bitsmoe_version": ([], ctypes.c_int),
@@ -394,6 +396,7 @@ _NORM = struct.Struct("@7P5q6i2f")         # bitsmoe_norm_args
 _ROUTE = struct.Struct("@7PQq6ifi")        # bitsmoe_route_args
 _Q4 = struct.Struct("@6i8PQ")              # bitsmoe_q4_args
 _GMM = struct.Struct("@7Pq10i")            # bitsmoe_gmm_args
+_DENSE = struct.Struct("@6i11PQq")         # bitsmoe_dense_ffn_args
 
 
 def _refuse(what: str, why: str):
@@ -623,6 +626,35 @@ def grouped_matmul(A, W, offsets, out, *, W_up=None, rows=None, rows_per_a: int 
     _launch(what, lib().bitsmoe_grouped_matmul, dev, stream,
             _GMM.pack(ap, wp, up, off, rp, op, _extra(what, status, dev), lda, n, ashape[0], N, K, E, it, ot, rows_per_a,
                       scatter, 0))
+
+
+def dense_ffn_workspace_bytes(dims: FfnDims, T: int) -> int:
+    return int(lib().bitsmoe_dense_ffn_workspace_bytes(ctypes.byref(dims), T))
+
+
+def dense_ffn_forward(dims: FfnDims, w_gate, w_up, w_down, x, topk_ids, gate_w, offsets, order, out, workspace,
+                      status=None, stream=None):
+    """The routed FFN of dense experts: w_gate, w_up [E][d_ff][d_model], w_down [E][d_model][d_ff] and
+    x [T][d_model] in float16 or bfloat16, the routing of topk_route, out [T][d_model] float32."""
+    what = "dense_ffn_forward"
+    d_model, d_ff, E, K = dims.d_model, dims.d_ff, dims.n_experts, dims.top_k
+    T = x.shape[0]
+    dev = x.get_device()
+    xp, kind, xs = _matrix(what, "x", x, (T, d_model), dev)
+    wg = _dense(what, "w_gate", w_gate, x.dtype, (E, d_ff, d_model), dev)
+    wu = _dense(what, "w_up", w_up, x.dtype, (E, d_ff, d_model), dev)
+    wd = _dense(what, "w_down", w_down, x.dtype, (E, d_model, d_ff), dev)
+    ids = _dense(what, "topk_ids", topk_ids, torch.int32, (T, K), dev)
+    gw = _dense(what, "gate_w", gate_w, torch.float32, (T, K), dev)
+    off = _dense(what, "offsets", offsets, torch.int32, (E + 1,), dev)
+    od = _dense(what, "order", order, torch.int32, (T * K,), dev)
+    op = _dense(what, "out", out, torch.float32, (T, d_model), dev)
+    ws = _extra(what, workspace, dev)
+    if dev < 0:
+        _refuse(what, "the tensors are not on one GPU")
+    _launch(what, lib().bitsmoe_dense_ffn_forward, dev, stream,
+            _DENSE.pack(d_model, d_ff, E, K, T, kind, xp, wg, wu, wd, ids, gw, off, od, op, ws, _extra(what, status, dev),
+                        workspace.nbytes if ws else 0, xs if T > 1 else d_model))
 
 
 def read_status(status, stream=None) -> int:

@@ -13,6 +13,9 @@
 
 namespace bitsmoe {
 
+int launch_combine(const int32_t* ids, const float* gw, float* Ye, float* Ysum, int T, int K, int E, int d_out,
+                   cudaStream_t s);
+
 struct GmmParams {
     const uint16_t* a;
     const uint16_t* w;
@@ -731,4 +734,67 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* strea
     }
     if (d.in_type == BITSMOE_BF16) return d.W_up ? launch_gmm_mv<true, true>(P, s) : launch_gmm_mv<true, false>(P, s);
     return d.W_up ? launch_gmm_mv<false, true>(P, s) : launch_gmm_mv<false, false>(P, s);
+}
+
+// ---------------------------------------------------------------------------
+// the routed FFN of dense experts
+// ---------------------------------------------------------------------------
+static bool dense_dims_ok(const bitsmoe_ffn_dims* d, int32_t T) {
+    return d && T >= 0 && d->d_model >= 8 && d->d_model % 8 == 0 && d->d_ff >= 8 && d->d_ff % 8 == 0 && d->n_experts >= 1 &&
+           d->n_experts <= BITSMOE_GMM_MAX_EXPERTS && d->top_k >= 1 && (int64_t)T * d->top_k <= 0x7fffffff;
+}
+
+BITSMOE_API uint64_t bitsmoe_dense_ffn_workspace_bytes(const bitsmoe_ffn_dims* dims, int32_t T) {
+    if (!dense_dims_ok(dims, T) || T == 0) return 0;
+    const uint64_t pairs = (uint64_t)T * dims->top_k;
+    return roundup(2 * pairs * dims->d_ff, 256) + 4 * pairs * dims->d_model;  // h, then every pair's output row
+}
+
+BITSMOE_API int bitsmoe_dense_ffn_forward(const bitsmoe_dense_ffn_args* args, void* stream) {
+    if (!args) return BITSMOE_EINVAL;
+    const bitsmoe_dense_ffn_args& a = *args;
+    const bitsmoe_ffn_dims& d = a.dims;
+    if (!dense_dims_ok(&d, a.tokens) || (a.type != BITSMOE_F16 && a.type != BITSMOE_BF16)) return BITSMOE_EINVAL;
+    if (a.tokens == 0) return BITSMOE_OK;
+    if (!a.x || !a.W_gate || !a.W_up || !a.W_down || !a.topk_ids || !a.gate_w || !a.offsets || !a.order || !a.out)
+        return BITSMOE_EINVAL;
+    if ((uintptr_t)a.topk_ids % 4 || (uintptr_t)a.gate_w % 4 || (uintptr_t)a.out % 4 || !a.workspace ||
+        (uintptr_t)a.workspace % 256)
+        return BITSMOE_EINVAL;
+    if (a.workspace_bytes < bitsmoe_dense_ffn_workspace_bytes(&d, a.tokens)) return BITSMOE_ESIZE;
+    const int pairs = a.tokens * d.top_k;
+    uint8_t* h = (uint8_t*)a.workspace;
+    float* y = (float*)(h + roundup(2ull * pairs * d.d_ff, 256));
+    bitsmoe_gmm_args g{};
+    g.A = a.x;
+    g.W = a.W_gate;
+    g.W_up = a.W_up;
+    g.offsets = a.offsets;
+    g.rows = a.order;
+    g.out = h;
+    g.status = a.status;
+    g.a_stride = a.x_stride;
+    g.n_rows = pairs;
+    g.n_a_rows = a.tokens;
+    g.n_out = d.d_ff;
+    g.n_in = d.d_model;
+    g.n_experts = d.n_experts;
+    g.in_type = g.out_type = a.type;
+    g.rows_per_a = d.top_k;
+    g.scatter = 1;
+    int rc = bitsmoe_grouped_matmul(&g, stream);
+    if (rc) return rc;
+    g.A = h;
+    g.W = a.W_down;
+    g.W_up = nullptr;
+    g.out = y;
+    g.a_stride = d.d_ff;
+    g.n_a_rows = pairs;
+    g.n_out = d.d_model;
+    g.n_in = d.d_ff;
+    g.out_type = BITSMOE_F32;
+    g.rows_per_a = 1;
+    rc = bitsmoe_grouped_matmul(&g, stream);
+    if (rc) return rc;
+    return launch_combine(a.topk_ids, a.gate_w, y, a.out, a.tokens, d.top_k, d.n_experts, d.d_model, (cudaStream_t)stream);
 }

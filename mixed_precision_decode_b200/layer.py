@@ -1,5 +1,5 @@
-"""User-facing objects over the C ABI: a packed projection and a spectral MoE
-gate/up layer.  torch provides device memory and streams; every computation
+"""User-facing objects over the C ABI: a packed projection, a spectral MoE gate/up
+layer, expert FFNs, routing and the block around them.  torch provides device memory and streams; every computation
 is a libbitsmoe kernel."""
 from __future__ import annotations
 
@@ -157,21 +157,47 @@ class SpectralMoELayer:
         return out
 
 
+class Q4Down:
+    """Down matrices [E][d_model][d_ff] held in 4 bits, a scale per `group` (32, 64 or
+    128) columns of a row."""
+
+    def __init__(self, blob: torch.Tensor, shape: tuple, group: int):
+        assert blob.dtype == torch.uint8 and blob.numel() >= B.q4_bytes(*shape, group) > 0
+        self.blob, self.shape, self.group = blob, tuple(shape), group
+
+    @classmethod
+    def pack(cls, w_down: torch.Tensor, group: int = 64, status: torch.Tensor | None = None, stream=None) -> "Q4Down":
+        """Quantise w_down [E][d_model][d_ff] (float32, float16 or bfloat16, on the GPU)."""
+        n = B.q4_bytes(*w_down.shape, group)
+        blob = torch.empty(n, dtype=torch.uint8, device=w_down.device)
+        B.q4_pack(w_down.contiguous(), group, blob, status, stream)
+        return cls(blob, w_down.shape, group)
+
+    def unpack(self, stream=None) -> torch.Tensor:
+        """The stored values, [E][d_model][d_ff] f32."""
+        w = torch.empty(self.shape, dtype=torch.float32, device=self.blob.device)
+        B.q4_unpack(self.blob, self.group, w, stream)
+        return w
+
+
 class SpectralMoEFFN:
     """A routed expert FFN: the gate and up projections in shared-spectral form
-    (SpectralMoELayer), then SiLU(gate) * up and a dense fp16 down projection per
-    expert, summed over each token's slots with its gate weights -- one
-    bitsmoe_ffn_forward call.
+    (SpectralMoELayer), then SiLU(gate) * up and a down projection per expert, summed
+    over each token's slots with its gate weights -- one bitsmoe_ffn_forward call with
+    dense fp16 down matrices, the layer call and bitsmoe_ffn_down_q4 with 4-bit ones.
 
-    w_down [E][d_model][d_ff] fp16 on the GPU, d_model = the layer's d_in and
-    d_ff = the gate/up d_out."""
+    w_down [E][d_model][d_ff] fp16 on the GPU, or a Q4Down of that shape; d_model = the
+    layer's d_in and d_ff = the gate/up d_out."""
 
-    def __init__(self, layer: SpectralMoELayer, w_down: torch.Tensor):
+    def __init__(self, layer: SpectralMoELayer, w_down: "torch.Tensor | Q4Down"):
         g = layer.gate
         assert layer.up.d_out == g.d_out
-        assert w_down.dtype == torch.float16 and tuple(w_down.shape) == (g.n_experts, g.d_in, g.d_out)
+        assert tuple(w_down.shape) == (g.n_experts, g.d_in, g.d_out)
         self.layer = layer
-        self.w_down = w_down.contiguous()
+        self.q4 = w_down if isinstance(w_down, Q4Down) else None
+        if self.q4 is None:
+            assert w_down.dtype == torch.float16
+            self.w_down = w_down.contiguous()
         self.dims = B.ffn_dims(g.d_in, g.d_out, g.n_experts, g.top_k)
         self._ws = {}
 
@@ -180,13 +206,19 @@ class SpectralMoEFFN:
         zero-filled once on first use: its head keeps the fused path's counters."""
         ws = self._ws.get(T)
         if ws is None:
-            n = B.ffn_workspace_bytes(self.layer.gate.plan, self.layer.up.plan, T)
-            ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.w_down.device)
+            if self.q4 is None:
+                n = B.ffn_workspace_bytes(self.layer.gate.plan, self.layer.up.plan, T)
+            else:  # the down step's alone: the layer keeps its own
+                n = B.ffn_down_q4_workspace_bytes(self.dims, self.q4.group, T)
+            ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.layer.gate.blob.device)
             self._ws[T] = ws
         return ws
 
     def launches(self, T: int) -> int:
         """Kernels one forward launches for T tokens (the layer's, then the down step's)."""
+        if self.q4 is not None:
+            return (B.layer_launches(self.layer.gate.plan, self.layer.up.plan, T)
+                    + B.ffn_down_q4_launches(self.dims, self.q4.group, T))
         return B.ffn_launches(self.layer.gate.plan, self.layer.up.plan, T)
 
     def gate_up_buffers(self, T: int, device) -> dict:
@@ -206,7 +238,99 @@ class SpectralMoEFFN:
             out = torch.empty((T, self.dims.d_model), dtype=torch.float32, device=x.device)
         if gate_up is None:
             gate_up = self.gate_up_buffers(T, x.device)
+        if self.q4 is not None:
+            self.layer.forward(x, topk_ids, gate_w, out=gate_up, status=status, stream=stream)
+            ws = self.workspace(T)
+            B.ffn_down_q4(self.dims, self.q4.blob, self.q4.group, gate_up["Y_experts_gate"], gate_up["Y_experts_up"],
+                          topk_ids, gate_w, T, out, ws, ws.numel(), status, stream)
+            return out
         ios = self.layer._proj_ios(gate_up)
         ws = self.workspace(T)
         B.ffn_forward(ios[0], ios[1], self.w_down, x, topk_ids, gate_w, T, out, ws, ws.numel(), status, stream)
         return out
+
+
+class Routing:
+    """The routing of T tokens: topk_ids [T][top_k] int32 and gate_w [T][top_k] f32, and
+    the (token, slot) pairs grouped by expert: offsets [E + 1] and order [T * top_k] int32."""
+
+    def __init__(self, topk_ids, gate_w, offsets, order):
+        self.topk_ids, self.gate_w, self.offsets, self.order = topk_ids, gate_w, offsets, order
+
+
+def route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+          status: torch.Tensor | None = None, stream=None) -> Routing:
+    """Top-k routing of router logits [T][E] (f32, f16 or bf16, on the GPU)."""
+    T, E = logits.shape
+    i32 = {"dtype": torch.int32, "device": logits.device}
+    r = Routing(torch.empty((T, top_k), **i32), torch.empty((T, top_k), dtype=torch.float32, device=logits.device),
+                torch.empty(E + 1, **i32), torch.empty(T * top_k, **i32))
+    n = B.topk_route_workspace_bytes(T, E, top_k)
+    ws = torch.empty(n, dtype=torch.uint8, device=logits.device) if n else None
+    B.topk_route(logits, r.topk_ids, r.gate_w, r.offsets, r.order, scoring=scoring, renormalise=renormalise, scale=scale,
+                 workspace=ws, status=status, stream=stream)
+    return r
+
+
+class DenseMoEFFN:
+    """The routed FFN of experts with dense matrices (before the decomposition, or in a
+    layer left without it): w_gate, w_up [E][d_ff][d_model] and w_down [E][d_model][d_ff],
+    fp16 or bf16 on the GPU.  Grouped products: made for many tokens as for few."""
+
+    def __init__(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, top_k: int):
+        E, d_ff, d_model = w_gate.shape
+        assert w_up.shape == w_gate.shape and tuple(w_down.shape) == (E, d_model, d_ff)
+        assert w_gate.dtype == w_up.dtype == w_down.dtype and w_gate.dtype in (torch.float16, torch.bfloat16)
+        self.w_gate, self.w_up, self.w_down = w_gate.contiguous(), w_up.contiguous(), w_down.contiguous()
+        self.dims = B.ffn_dims(d_model, d_ff, E, top_k)
+
+    def forward(self, x: torch.Tensor, routing: Routing, out: torch.Tensor | None = None,
+                status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x [T][d_model] in the matrices' type -> out [T][d_model] f32."""
+        T = x.shape[0]
+        if out is None:
+            out = torch.empty((T, self.dims.d_model), dtype=torch.float32, device=x.device)
+        ws = torch.empty(B.dense_ffn_workspace_bytes(self.dims, T), dtype=torch.uint8, device=x.device)
+        B.dense_ffn_forward(self.dims, self.w_gate, self.w_up, self.w_down, x, routing.topk_ids, routing.gate_w,
+                            routing.offsets, routing.order, out, ws, status, stream)
+        return out
+
+
+class MoEBlock:
+    """A pre-norm MoE block around an expert FFN:
+
+        h <- h + alpha * gate * (the previous block's output, normalised with w_post if given)
+        x  = rmsnorm(h) w_norm,  logits = w_router x,  y = FFN(x, top-k routing of the logits)
+
+    y is added to h by the next block's forward (or by finish), fused with that block's
+    norm.  w_norm, w_post [d_model] f32, w_router [E][d_model] fp16; ffn a SpectralMoEFFN or
+    an fp16 DenseMoEFFN; gate f32 [T or 1][d_model or 1]."""
+
+    def __init__(self, ffn: "SpectralMoEFFN | DenseMoEFFN", w_norm: torch.Tensor, w_router: torch.Tensor,
+                 w_post: torch.Tensor | None = None, alpha: float = 1.0, eps: float = 1e-6, scoring: str = "softmax",
+                 renormalise: bool = True, scale: float = 1.0):
+        d = ffn.dims
+        assert w_router.dtype == torch.float16 and tuple(w_router.shape) == (d.n_experts, d.d_model)
+        self.ffn, self.w_norm, self.w_router, self.w_post = ffn, w_norm, w_router.contiguous(), w_post
+        self.alpha, self.eps, self.scoring, self.renormalise, self.scale = alpha, eps, scoring, renormalise, scale
+
+    def forward(self, h: torch.Tensor, y: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """h [T][d_model] (the residual stream, f32, f16 or bf16), y: the output of the block
+        before, added to h in place first.  Returns this block's output, f32."""
+        T, d = h.shape
+        E = self.ffn.dims.n_experts
+        x = torch.empty((T, d), dtype=torch.float16, device=h.device)
+        B.norm_residual(h, y, self.w_norm, x, w_post=None if y is None else self.w_post, gate=gate, alpha=self.alpha,
+                        eps=self.eps, stream=stream)
+        logits = torch.empty((T, E), dtype=torch.float32, device=h.device)
+        B.shared_proj(self.w_router, x, logits, T, d, E, stream)
+        r = route(logits, self.ffn.dims.top_k, self.scoring, self.renormalise, self.scale, status, stream)
+        if isinstance(self.ffn, DenseMoEFFN):
+            return self.ffn.forward(x, r, status=status, stream=stream)
+        return self.ffn.forward(x, r.topk_ids, r.gate_w, status=status, stream=stream)
+
+    def finish(self, h: torch.Tensor, y: torch.Tensor, gate: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Adds the last block's output to h in place."""
+        B.norm_residual(h, y, w_post=self.w_post, gate=gate, alpha=self.alpha, eps=self.eps, stream=stream)
+        return h

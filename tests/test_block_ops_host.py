@@ -131,6 +131,25 @@ def test_grouped_matmul_refusals(B):
     assert B.lib().bitsmoe_grouped_matmul(None, None) == B.EINVAL
 
 
+def test_dense_ffn_refusals(B):
+    d = B.ffn_dims(64, 32, 4, 2)
+    n = B.dense_ffn_workspace_bytes(d, 3)
+    assert n >= 3 * 2 * (32 * 2 + 64 * 4) and B.dense_ffn_workspace_bytes(d, 0) == 0
+    assert B.dense_ffn_workspace_bytes(B.ffn_dims(60, 32, 4, 2), 3) == 0
+    ok = dict(d_model=64, d_ff=32, E=4, K=2, tokens=3, type=1, x=256, wg=256, wu=256, wd=256, ids=256, gw=256, off=256, od=256,
+              out=256, ws=512, st=None, nb=n, xs=64)
+
+    def call(**kw):
+        return _call(B.lib().bitsmoe_dense_ffn_forward, "@6i11PQq", {**ok, **kw})
+
+    for bad in (dict(d_model=60), dict(d_ff=4), dict(E=0), dict(E=4097), dict(K=0), dict(tokens=-1), dict(type=0), dict(x=None),
+                dict(wg=None), dict(wu=None), dict(wd=None), dict(ids=None), dict(gw=None), dict(off=None), dict(od=None),
+                dict(out=None), dict(ws=None), dict(ws=520), dict(xs=56), dict(x=264)):
+        assert call(**bad) == B.EINVAL, bad
+    assert call(nb=n - 1) == B.ESIZE and call(tokens=0, x=None) == B.OK
+    assert B.lib().bitsmoe_dense_ffn_forward(None, None) == B.EINVAL
+
+
 def test_packed_structures_match_the_header(tmp_path, B):
     """The binding's packed layouts have the sizes and field offsets of the header's structures."""
     fields = {
@@ -143,6 +162,9 @@ def test_packed_structures_match_the_header(tmp_path, B):
         "bitsmoe_q4_args": (B._Q4, ["dims.d_model", "dims.d_ff", "dims.n_experts", "dims.top_k", "group", "tokens", "blob",
                                     "Y_gate", "Y_up", "topk_ids", "gate_w", "out", "workspace", "status",
                                     "workspace_bytes"]),
+        "bitsmoe_dense_ffn_args": (B._DENSE, ["dims.d_model", "dims.d_ff", "dims.n_experts", "dims.top_k", "tokens", "type",
+                                              "x", "W_gate", "W_up", "W_down", "topk_ids", "gate_w", "offsets", "order",
+                                              "out", "workspace", "status", "workspace_bytes", "x_stride"]),
         "bitsmoe_gmm_args": (B._GMM, ["A", "W", "W_up", "offsets", "rows", "out", "status", "a_stride", "n_rows", "n_a_rows",
                                       "n_out", "n_in", "n_experts", "in_type", "out_type", "rows_per_a", "scatter",
                                       "reserved"]),

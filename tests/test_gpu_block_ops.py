@@ -573,3 +573,221 @@ def test_grouped_matmul_non_finite_rows_stay_apart():
         want[1] = want[sizes[0]] = False
         want[sizes[0] + sizes[1]:] = False
         assert torch.equal(fin, want)
+
+
+# ---------------------------------------------------------------------------
+# as they are used: other streams, graphs, shared workspaces, a block
+# ---------------------------------------------------------------------------
+def _rel(got, ref):
+    """Largest error of a row over the row's largest value."""
+    got, ref = got.double(), ref.double()
+    return float(((got - ref).abs().amax(-1) / ref.abs().amax(-1).clamp_min(1e-30)).max())
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_operators_on_another_stream_and_in_a_graph(T):
+    """Each operator on a side stream and in a replayed graph whose inputs change between replays equals its
+    plain call bit for bit (no operator's result depends on timing)."""
+    g = _gen(T)
+    E, K, d, d_ff = 16, 3, 256, 192
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    h, y, w = _randn(g, T, d), _randn(g, T, d), 1 + 0.1 * _randn(g, d)
+    w_router = _randn(g, T, E)
+    blob, _ = _q4_blob(_randn(g, E, d, d_ff), 64)
+    wg, wu = _randn(g, E, d_ff, d).half() * 0.1, _randn(g, E, d_ff, d).half() * 0.1
+    yg, yu = _randn(g, T, K, d_ff), _randn(g, T, K, d_ff)
+    dims = B.ffn_dims(d, d_ff, E, K)
+    bufs = {"h_out": torch.empty_like(h), "x": torch.empty(T, d, dtype=F16, device="cuda"),
+            "ids": torch.empty(T, K, **i32), "gw": torch.empty(T, K, device="cuda"), "off": torch.empty(E + 1, **i32),
+            "order": torch.empty(T * K, **i32), "act": torch.zeros(T * K, d_ff, dtype=F16, device="cuda"),
+            "out": torch.empty(T, d, device="cuda")}
+    nr, nq = B.topk_route_workspace_bytes(T, E, K), B.ffn_down_q4_workspace_bytes(dims, 64, T)
+    ws_r = torch.empty(max(nr, 256), dtype=torch.uint8, device="cuda")
+    ws_q = torch.empty(max(nq, 256), dtype=torch.uint8, device="cuda")
+
+    def run():
+        B.norm_residual(h, y, w, bufs["x"], h_out=bufs["h_out"])
+        B.topk_route(w_router, bufs["ids"], bufs["gw"], bufs["off"], bufs["order"], workspace=ws_r)
+        B.grouped_matmul(bufs["x"], wg, bufs["off"], bufs["act"], W_up=wu, rows=bufs["order"], rows_per_a=K, scatter=True)
+        B.ffn_down_q4(dims, blob, 64, yg, yu, bufs["ids"], bufs["gw"], T, bufs["out"], ws_q, nq)
+
+    def snap():
+        torch.cuda.synchronize()
+        got = {k: v.clone() for k, v in bufs.items()}
+        for v in bufs.values():
+            v.zero_()
+        torch.cuda.synchronize()
+        return got
+
+    run()
+    first = snap()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        run()
+    other = snap()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    graph.replay()
+    replay = snap()
+    for k, v in first.items():
+        assert torch.equal(v, other[k]) and torch.equal(v, replay[k]), k
+    keep = [t.clone() for t in (y, w_router, yg)]
+    for t in (y, w_router, yg):
+        t.copy_(torch.flip(t, [-1]) * 1.5)
+    graph.replay()
+    changed = snap()
+    run()
+    plain = snap()
+    for k, v in plain.items():
+        assert torch.equal(v, changed[k]), k
+    assert not torch.equal(changed["x"], first["x"]) and not torch.equal(changed["out"], first["out"])
+    for t, v in zip((y, w_router, yg), keep):
+        t.copy_(v)
+    graph.replay()
+    again = snap()
+    for k, v in first.items():
+        assert torch.equal(v, again[k]), k
+
+
+def test_concurrent_calls_with_their_own_workspaces():
+    """Two streams at once, each with its own buffers: the same results as alone."""
+    E, K, d, d_ff = 24, 4, 512, 256
+    g = _gen(8)
+    blob, _ = _q4_blob(_randn(g, E, d, d_ff), 32)
+    W = _randn(g, E, d, d_ff).half()
+    dims = B.ffn_dims(d, d_ff, E, K)
+    sets = []
+    for k in range(2):
+        T = 300 + 33 * k
+        ids = torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :K].to(torch.int32).contiguous()
+        logits = _randn(g, T, E)
+        i32 = {"dtype": torch.int32, "device": "cuda"}
+        n = B.ffn_down_q4_workspace_bytes(dims, 32, T)
+        sets.append({"T": T, "logits": logits, "yg": _randn(g, T, K, d_ff), "a": _randn(g, T * K, d_ff).half(),
+                     "ids": torch.empty(T, K, **i32), "gw": torch.empty(T, K, device="cuda"), "off": torch.empty(E + 1, **i32),
+                     "order": torch.empty(T * K, **i32), "out": torch.empty(T, d, device="cuda"),
+                     "y": torch.zeros(T * K, d, device="cuda"), "n": n, "ws": torch.empty(n, dtype=torch.uint8, device="cuda"),
+                     "wr": torch.empty(B.topk_route_workspace_bytes(T, E, K), dtype=torch.uint8, device="cuda")})
+
+    def run(s):
+        B.topk_route(s["logits"], s["ids"], s["gw"], s["off"], s["order"], workspace=s["wr"])
+        B.grouped_matmul(s["a"], W, s["off"], s["y"], rows=s["order"], scatter=True)
+        B.ffn_down_q4(dims, blob, 32, s["yg"], None, s["ids"], s["gw"], s["T"], s["out"], s["ws"], s["n"])
+
+    alone = []
+    for s in sets:
+        run(s)
+        torch.cuda.synchronize()
+        alone.append({k: s[k].clone() for k in ("ids", "gw", "off", "order", "out", "y")})
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                run(s)
+    torch.cuda.synchronize()
+    for s, want in zip(sets, alone):
+        for k, v in want.items():
+            assert torch.equal(s[k], v), k
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T", [1, 7, 260])
+def test_dense_ffn(T, dtype):
+    """The routed FFN of dense experts against 64 bits, one expert closed to every token and one token without any.
+
+    h is rounded to the matrices' type once (eps / 2 of itself, which the down product turns into at most eps / 2
+    sum|w h|); the rest as for the products themselves."""
+    from mixed_precision_decode_b200.layer import DenseMoEFFN, route
+    E, K, d, d_ff = 6, 2, 136, 200
+    g = _gen(50 + T)
+    ffn = DenseMoEFFN((_randn(g, E, d_ff, d) * d ** -0.5).to(dtype), (_randn(g, E, d_ff, d) * d ** -0.5).to(dtype),
+                      (_randn(g, E, d, d_ff) * d_ff ** -0.5).to(dtype), K)
+    x = _randn(g, T, d).to(dtype)
+    logits = _randn(g, T, E)
+    logits[:, 4] = float("-inf")
+    if T > 1:
+        logits[T // 2] = float("-inf")
+    r = route(logits, K)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = ffn.forward(x, r, status=st)
+    assert B.read_status(st) == 0
+    ref, tol = torch.zeros(T, d, dtype=torch.float64, device="cuda"), torch.zeros(T, d, dtype=torch.float64, device="cuda")
+    for t in range(T):
+        for j in range(K):
+            e, w = int(r.topk_ids[t, j]), float(r.gate_w[t, j])
+            assert e != 4
+            if e < 0:
+                continue
+            a, b = ffn.w_gate[e].double(), ffn.w_up[e].double()
+            v = x[t].double()
+            n = (d // 16 + 24) * U23
+            gate, up = a @ v, b @ v
+            eg, eu = n * (a.abs() @ v.abs()), n * (b.abs() @ v.abs())
+            h = gate * torch.sigmoid(gate) * up
+            eh = 1.1 * eg * up.abs() + (gate * torch.sigmoid(gate)).abs() * eu + h.abs() * (16 * U24)
+            eh = eh + _rounding(h, dtype)
+            wd = ffn.w_down[e].double()
+            ref[t] += w * (wd @ h)
+            tol[t] += abs(w) * (wd.abs() @ eh + (d_ff // 16 + 24) * U23 * (wd.abs() @ h.abs()))
+    _within(out, ref, tol * 1.01 + 4 * U24 * ref.abs() + 1e-30, "dense ffn")
+    if T > 1:
+        assert bool((out[T // 2] == 0).all())
+
+
+@pytest.mark.parametrize("T", [1, 12])
+@pytest.mark.parametrize("kind", ["spectral", "spectral_q4", "dense"])
+def test_moe_block_stack(kind, T):
+    """Three blocks as a decoder runs them -- norm, router, routed FFN, the residual added by the next block's norm --
+    against the same steps from the operators' plain forms on the routing that the block chose: every output of the
+    chain within the outputs' 2e-3 bound, every choice of experts one that the logits allow."""
+    from cases import SMALL, get_case
+    from mixed_precision_decode_b200 import synth
+    from mixed_precision_decode_b200.layer import DenseMoEFFN, MoEBlock, Q4Down, SpectralMoEFFN, route
+    case = get_case("tiny")
+    cfg = SMALL["tiny"]
+    E, K, d = cfg.n_experts, cfg.top_k, cfg.d_in
+    g = _gen(60 + T)
+    h = _randn(g, T, d)
+    blocks, downs = [], []
+    for b in range(3):
+        wd = synth.make_down(cfg, synth.make_generator(70 + b, torch.device("cuda")), torch.device("cuda"))
+        if kind == "dense":
+            wg, wu = ((_randn(g, E, cfg.d_out, d) * d ** -0.5).half() for _ in range(2))
+            ffn = DenseMoEFFN(wg, wu, wd, K)
+        else:
+            ffn = SpectralMoEFFN(case.layer, Q4Down.pack(wd, 32) if kind == "spectral_q4" else wd)
+        w_down = ffn.q4.unpack().double() if kind == "spectral_q4" else wd.double()
+        downs.append(w_down)
+        blocks.append(MoEBlock(ffn, 1 + 0.1 * _randn(g, d), _randn(g, E, d).half(), w_post=1 + 0.1 * _randn(g, d), alpha=0.5))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y, hr, yr = None, h.double(), None
+    for blk, w_down in zip(blocks, downs):
+        y_in = y
+        y = blk.forward(h, y, status=st)
+        # the plain steps, from the block's own h (its roundings are bounded by the operators' tests)
+        if y_in is not None:
+            u = y_in.double()
+            hr = hr + 0.5 * u / torch.sqrt(u.square().mean(1, keepdim=True) + 1e-6) * blk.w_post.double()
+        assert _rel(h, hr) <= 1e-5
+        hr = h.double()
+        x = (hr / torch.sqrt(hr.square().mean(1, keepdim=True) + 1e-6) * blk.w_norm.double()).half()
+        logits = torch.empty(T, E, device="cuda")
+        B.shared_proj(blk.w_router, x, logits, T, d, E)
+        r = route(logits, K)
+        if kind == "dense":
+            a = x.double()
+            want = torch.zeros(T, d, dtype=torch.float64, device="cuda")
+            for t in range(T):
+                for j in range(K):
+                    e = int(r.topk_ids[t, j])
+                    gate, up = blk.ffn.w_gate[e].double() @ a[t], blk.ffn.w_up[e].double() @ a[t]
+                    want[t] += float(r.gate_w[t, j]) * (w_down[e] @ (gate * torch.sigmoid(gate) * up))
+        else:
+            o = case.layer.forward(x, r.topk_ids, r.gate_w, want_experts=True)
+            gate, up = o["Y_experts_gate"].double(), o["Y_experts_up"].double()
+            hh = gate * torch.sigmoid(gate) * up
+            want = torch.einsum("tk,tkdf,tkf->td", r.gate_w.double(), w_down[r.topk_ids.long()], hh)
+        assert _rel(y, want) <= 4e-3  # x may round the other way in the last bit of fp16, 2e-3 on either side
+    blocks[-1].finish(h, y)
+    assert bool(torch.isfinite(h).all()) and B.read_status(st) == 0

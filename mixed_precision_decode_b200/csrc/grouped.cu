@@ -55,18 +55,27 @@ __device__ __forceinline__ bool row_pair(const GmmParams& P, int i, int64_t& src
 // ---------------------------------------------------------------------------
 // few rows per expert
 // ---------------------------------------------------------------------------
-// Bound by the weights' bytes.  A CTA owns 16 rows of one expert's matrix (of both,
-// when gated) and up to 8 NTL of its input rows; its 8 warps take an eighth of K
+// Bound by the weights' bytes, with too few of them for the kernel below.  A CTA owns
+// 16 rows of one expert's matrix (of both, when gated) and up to 8 of its input rows; its 8 warps take an eighth of K
 // each, so that every SM has enough loads in flight when only a few experts are
 // touched, and add their fp32 partial tiles in warp order.  The products are
 // mma.sync m16n8k16 on operands that go from global memory to registers: a lane
 // loads 16 contiguous bytes of weight row g (and g + 8), eight k's that the two MMAs
 // of a 32-wide step take as k = 2c, 2c+1, 2c+8, 2c+9; the input rows are loaded with
 // the same order of k, so the sum over k is the same and no operand is rearranged.
-constexpr int kGmmTcRows = 8;  // rows per expert, on average, beyond which the tensor-core path is taken
+//
+// Which of the two kernels (us, this one / the next; K x N matrices of E experts, pairs of rows):
+//   gated 2048 x 768, E = 128:   8 pairs 13.7 / 16.9    32 pairs 35.2 / 39.2     64 pairs 60.3 / 54.1
+//   768 x 2048, E = 128:         8 pairs  8.8 /  9.8    32 pairs 25.7 / 22.9     64 pairs 45.6 / 35.1
+//   gated 2048 x 768, E = 8:    16 pairs 11.3 / 16.6    64 pairs 15.0 / 17.2     96 pairs 17.7 / 17.2
+//   768 x 2048, E = 8:          16 pairs  7.5 /  9.6    64 pairs 10.1 /  9.8     96 pairs 11.9 / 10.0
+//   gated 4096 x 14336, E = 8:   2 pairs 75.4 / 78.0     8 pairs  195 /  203     64 pairs  412 /  291
+// The next one's CTA pairs take blocks of 256 weight rows: it is slower while these are fewer than the SMs, and
+// this one reads the weights again for every 8 rows of an expert.
+constexpr int kTcTiles = 148, kTcRows = 8;
 constexpr int kMvWarps = 8;
 constexpr int kMvThreads = 32 * kMvWarps;
-constexpr int kMvRows = 16;
+constexpr int kMvRows = 16, kMvTok = 8;  // weight rows and input rows of a CTA
 constexpr int kMvUnroll = 4;  // 32-wide k steps in flight per warp
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
@@ -123,26 +132,20 @@ __device__ __forceinline__ bool find_slot(const GmmParams& P, int slot, int tok,
     return false;
 }
 
-template <bool BF16, bool GATED, int NTL>
+template <bool BF16, bool GATED>
 __global__ void __launch_bounds__(kMvThreads) k_gmm_mv(const GmmParams P) {
     constexpr int NW = GATED ? 2 : 1;
-    __shared__ float s_part[kMvWarps][NW][kMvRows][8 * NTL + 1];
+    __shared__ float s_part[kMvWarps][NW][kMvRows][kMvTok + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();
     pdl_trigger();
     int e, i0, nt;
-    if (!find_slot(P, (int)blockIdx.y, 8 * NTL, e, i0, nt)) return;
+    if (!find_slot(P, (int)blockIdx.y, kMvTok, e, i0, nt)) return;
     const int n0 = (int)blockIdx.x * kMvRows;
 
-    // this lane's input rows (row g of each group of 8) and weight rows
-    const uint16_t* brow[NTL];
-#pragma unroll
-    for (int j = 0; j < NTL; j++) {
-        const int i = 8 * j + g;
-        int64_t src = 0, dst;
-        const bool ok = i < nt && row_pair(P, i0 + i, src, dst);
-        brow[j] = ok ? P.a + src * P.lda : nullptr;
-    }
+    // this lane's input row and weight rows
+    int64_t src = 0, dst = 0;
+    const uint16_t* brow = g < nt && row_pair(P, i0 + g, src, dst) ? P.a + src * P.lda : nullptr;
     const uint16_t* wrow[NW][2];
 #pragma unroll
     for (int m = 0; m < NW; m++)
@@ -151,21 +154,13 @@ __global__ void __launch_bounds__(kMvThreads) k_gmm_mv(const GmmParams P) {
             const int n = n0 + g + 8 * r;
             wrow[m][r] = n < P.N ? (m ? P.w_up : P.w) + ((int64_t)e * P.N + n) * P.D : nullptr;
         }
-    float acc[NW][NTL][4];
-#pragma unroll
-    for (int m = 0; m < NW; m++)
-#pragma unroll
-        for (int j = 0; j < NTL; j++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) acc[m][j][q] = 0.0f;
-
+    float acc[NW][4] = {};
     const int steps = (P.D + 31) / 32, per = (steps + kMvWarps - 1) / kMvWarps;
     const int s0 = min(steps, warp * per), s1 = min(steps, s0 + per);
-    constexpr int U = NW * NTL > 4 ? 2 : kMvUnroll;
-    for (int s = s0; s < s1; s += U) {
-        uint4 wv[U][NW][2], bv[U][NTL];
+    for (int s = s0; s < s1; s += kMvUnroll) {
+        uint4 wv[kMvUnroll][NW][2], bv[kMvUnroll];
 #pragma unroll
-        for (int u = 0; u < U; u++) {
+        for (int u = 0; u < kMvUnroll; u++) {
             const int k = (s + u) * 32 + 8 * c;  // D is a multiple of 8: a lane's 8 k's are inside or outside together
             const bool in = s + u < s1 && k < P.D;
 #pragma unroll
@@ -173,33 +168,29 @@ __global__ void __launch_bounds__(kMvThreads) k_gmm_mv(const GmmParams P) {
 #pragma unroll
                 for (int r = 0; r < 2; r++)
                     wv[u][m][r] = in && wrow[m][r] ? ld_stream(wrow[m][r] + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < NTL; j++)
-                bv[u][j] = in && brow[j] ? *reinterpret_cast<const uint4*>(brow[j] + k) : make_uint4(0, 0, 0, 0);
+            bv[u] = in && brow ? *reinterpret_cast<const uint4*>(brow + k) : make_uint4(0, 0, 0, 0);
         }
+        // the MMA's accumulator drops what does not fit, toward zero: 128 k's at a time, joined by fp32 additions
+        float part[NW][4] = {};
 #pragma unroll
-        for (int u = 0; u < U; u++)
+        for (int u = 0; u < kMvUnroll; u++)
 #pragma unroll
-            for (int m = 0; m < NW; m++)
+            for (int m = 0; m < NW; m++) {
+                mma16816<BF16>(part[m], wv[u][m][0].x, wv[u][m][1].x, wv[u][m][0].y, wv[u][m][1].y, bv[u].x, bv[u].y);
+                mma16816<BF16>(part[m], wv[u][m][0].z, wv[u][m][1].z, wv[u][m][0].w, wv[u][m][1].w, bv[u].z, bv[u].w);
+            }
 #pragma unroll
-                for (int j = 0; j < NTL; j++) {
-                    mma16816<BF16>(acc[m][j], wv[u][m][0].x, wv[u][m][1].x, wv[u][m][0].y, wv[u][m][1].y, bv[u][j].x,
-                                   bv[u][j].y);
-                    mma16816<BF16>(acc[m][j], wv[u][m][0].z, wv[u][m][1].z, wv[u][m][0].w, wv[u][m][1].w, bv[u][j].z,
-                                   bv[u][j].w);
-                }
+        for (int m = 0; m < NW; m++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) acc[m][q] += part[m][q];
     }
 #pragma unroll
     for (int m = 0; m < NW; m++)
 #pragma unroll
-        for (int j = 0; j < NTL; j++)
-#pragma unroll
-            for (int q = 0; q < 4; q++)
-                s_part[warp][m][g + 8 * (q >> 1)][8 * j + 2 * c + (q & 1)] = acc[m][j][q];
+        for (int q = 0; q < 4; q++) s_part[warp][m][g + 8 * (q >> 1)][2 * c + (q & 1)] = acc[m][q];
     __syncthreads();
     for (int v = threadIdx.x; v < nt * kMvRows; v += kMvThreads) {
         const int i = v / kMvRows, r = v % kMvRows;
-        int64_t src, dst;
         if (n0 + r >= P.N || !row_pair(P, i0 + i, src, dst)) continue;
         float y[NW];
 #pragma unroll
@@ -216,15 +207,8 @@ __global__ void __launch_bounds__(kMvThreads) k_gmm_mv(const GmmParams P) {
 
 template <bool BF16, bool GATED>
 static int launch_gmm_mv(const GmmParams& P, cudaStream_t s) {
-    const int avg = P.P / P.E;
-    const int ntl = avg <= 6 ? 1 : avg <= 12 ? 2 : 4;  // input rows a CTA takes: 8, 16 or 32
-    const int64_t slots = std::min<int64_t>(P.P, P.E) + P.P / (8 * ntl);  // at least the pieces of every group
-    const unsigned tiles = (unsigned)((P.N + kMvRows - 1) / kMvRows);
-    if (slots > 65535) return BITSMOE_EINVAL;
-    const dim3 grid(tiles, (unsigned)slots), block(kMvThreads);
-    if (ntl == 1) return launch_pdl(k_gmm_mv<BF16, GATED, 1>, grid, block, 0, s, P);
-    if (ntl == 2) return launch_pdl(k_gmm_mv<BF16, GATED, 2>, grid, block, 0, s, P);
-    return launch_pdl(k_gmm_mv<BF16, GATED, 4>, grid, block, 0, s, P);
+    const int slots = std::min(P.P, P.E) + P.P / kMvTok;  // at least the pieces of every group; P.P <= kTcRows P.E here
+    return launch_pdl(k_gmm_mv<BF16, GATED>, dim3((P.N + kMvRows - 1) / kMvRows, slots), dim3(kMvThreads), 0, s, P);
 }
 
 // ---------------------------------------------------------------------------
@@ -249,10 +233,21 @@ constexpr int kGtM = 128;                        // weight rows per CTA and matr
 constexpr int kGtK = 64;                         // K per stage: one 128-byte swizzled row
 constexpr int kGtMaxStages = 12;
 constexpr uint32_t kGtAStage = kGtM * kGtK * 2;  // 16 KB
-constexpr int kGtEpiWarps = 4, kGtGatherWarps = 8;
-constexpr int kGtEpiWarp0 = 2, kGtRelayWarp = kGtEpiWarp0 + kGtEpiWarps, kGtGatherWarp0 = kGtRelayWarp + 1;
-constexpr int gt_threads(bool gather) { return 32 * (gather ? kGtGatherWarp0 + kGtGatherWarps : kGtRelayWarp); }
-constexpr size_t kGtSmem = 206 * 1024;           // dynamic shared memory a CTA uses at most (21 KB are static)
+constexpr int kGtRelayWarp = 2;                  // warps 0 and 1 issue loads and MMAs; 3 is idle
+constexpr int kGtEpiWarp0 = 4, kGtGatherWarps = 8;
+__host__ __device__ constexpr int gt_epi_warps(bool seg) { return seg ? 8 : 4; }
+__host__ __device__ constexpr int gt_gather_warp0(bool seg) { return kGtEpiWarp0 + gt_epi_warps(seg); }
+constexpr int gt_threads(bool gather, bool seg) { return 32 * (gt_gather_warp0(seg) + (gather ? kGtGatherWarps : 0)); }
+constexpr size_t kGtSmem = 204 * 1024;           // dynamic shared memory a CTA uses at most (21 KB are static)
+// Segments.  The tensor cores' fp32 accumulator cuts what does not fit, toward zero, at every step of 16 k: an
+// error of about 1.2e-9 K of the results' norm (measured: 4.9e-6 at K = 4096, twice that when gated; 4e-6 of a
+// sum of 768 terms of one sign), nothing beside a rounding to 16 bits but several times an fp32 sum's.  For fp32
+// results it is kept under 1e-6: at most 768 k's (gated: 384) are summed in tensor memory, and fp32 additions to
+// nearest in the epilogue's registers join them.  The epilogue is then 8 warps with 128 sums a thread: 384 threads launch with 168 registers
+// each; the 640 of the gathering kernel with 96, of which the others give up half:
+// 256 x 168 + 384 x 48 = 640 x 96.  (At 2,048 pairs x 768 with fp32 results three segments took 126 us
+// instead of 103.)
+constexpr int gt_segment(bool gated) { return gated ? 6 : 12; }
 
 constexpr int kGtBoxes = 5;
 __host__ __device__ constexpr int gt_box(int i) { return i < 3 ? 16 << i : 32 * i; }  // 16, 32, 64, 96, 128 rows
@@ -267,6 +262,7 @@ struct GmmTcParams {
     int ntiles;       // blocks of 256 weight rows
     int nst;          // K stages
     int stages;       // ring
+    int seg;          // K stages summed in tensor memory
     uint32_t stage_bytes;
     int vec;          // rows of out are whole 16-byte pieces
 };
@@ -311,15 +307,45 @@ __device__ __forceinline__ void gt_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void gt_ld32(uint32_t addr, uint32_t (&v)[32]) {
+template <int REGS, bool MORE>
+__device__ __forceinline__ void gt_regs() {
+    if constexpr (MORE)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+__device__ __forceinline__ void gt_ld16(uint32_t addr, uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
+}
+
+// 32 columns of each accumulator to, or with `more` added to, a thread's sums.
+template <int NW, bool SEG>
+__device__ __forceinline__ void gt_add(uint32_t addr, bool more, float (&y)[NW][32]) {
+    uint32_t v[SEG ? 1 : 2 * NW][16];
+#pragma unroll
+    for (int m = 0; m < 2 * NW; m++) {
+        uint32_t(&x)[16] = v[SEG ? 0 : m];
+        gt_ld16(addr + 128u * (m >> 1) + 16u * (m & 1), x);
+        if (SEG) {
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                float& s = y[m >> 1][16 * (m & 1) + j];
+                s = more ? s + __uint_as_float(x[j]) : __uint_as_float(x[j]);
+            }
+        }
+    }
+    if (!SEG) {
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int m = 0; m < 2 * NW; m++)
+#pragma unroll
+            for (int j = 0; j < 16; j++) y[m >> 1][16 * (m & 1) + j] = __uint_as_float(v[SEG ? 0 : m][j]);
+    }
 }
 
 // One tile of the walk.
@@ -354,16 +380,16 @@ __device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab
     return t;
 }
 
-template <bool GATED, bool GATHER>
-__global__ void __launch_bounds__(gt_threads(GATHER), 1)
+template <bool GATED, bool GATHER, bool SEG>
+__global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
     k_gmm_tc(const GmmTcParams Q, const __grid_constant__ GtMaps M) {
-    constexpr int NW = GATED ? 2 : 1;
+    constexpr int NW = GATED ? 2 : 1, EW = gt_epi_warps(SEG), kGatherWarp0 = gt_gather_warp0(SEG);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t s_full[kGtMaxStages], s_empty[kGtMaxStages], s_rows[kGtMaxStages], s_afull[2], s_aempty[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
-    __shared__ int s_dst[kGtEpiWarps][256];  // per epilogue warp: output row of each input row of a piece, -1 for none
-    __shared__ __align__(16) uint4 s_out[kGtEpiWarps][256];  // per epilogue warp: 32 x 32 results
+    __shared__ int s_dst[EW][1024 / EW];  // per epilogue warp: output row of each of its input rows, -1 for none
+    __shared__ __align__(16) uint4 s_out[EW][1024 / EW];  // per epilogue warp: results to be stored
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -385,7 +411,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
         }
         for (int i = 0; i < 2; i++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(tc_smem(&s_afull[i])));
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc_smem(&s_aempty[i])), "r"(2u * kGtEpiWarps));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc_smem(&s_aempty[i])), "r"(2u * EW));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_fail = 0;
@@ -422,69 +448,125 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
     const uint32_t b_off = NW * kGtAStage;
     volatile int* fail = &s_fail;
 
-    if (warp == 0) {
-        // the weights' tiles, and contiguous input rows; the pair's bytes complete on the first CTA's barrier
-        const uint32_t full0 = gt_mapa(tc_smem(&s_full[0]), 0);
-        int s = 0;
-        uint32_t phase = 1;  // parity of the stage's last release: nothing to wait for in the first round
+    if (warp >= kGtEpiWarp0 && warp < kGatherWarp0) {
+        if constexpr (GATHER && SEG) gt_regs<168, true>();
+        // accumulators to out: a thread owns a weight row, a column of tensor memory is an input row.  With 8 warps two
+        // share 32 weight rows and take the blocks of 32 input rows in turn.
+        constexpr int SHARE = EW / 4, NB = 8 / (NW * SHARE);  // NB: blocks a warp takes at most
+        constexpr int PASS = SEG ? 2 : 1;  // fp32 results go through shared memory in this many passes
+        const int sub = warp & 3, half = (warp - kGtEpiWarp0) >> 2;  // sub: the 32 lanes of tensor memory a warp can read
+        int* dst_of = s_dst[warp - kGtEpiWarp0];
+        uint4* stage_out = s_out[warp - kGtEpiWarp0];
+        const uint32_t aempty0 = gt_mapa(tc_smem(&s_aempty[0]), 0);
+        const bool f32 = SEG || P.out_type == BITSMOE_F32;
+        const int cw = f32 ? 8 : 4, piece = lane % cw;  // 16-byte pieces of 32 results, and this lane's
+        const int64_t pitch = (int64_t)P.N * (f32 ? 4 : 2);
+        int buf = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int item = first; item < total && ok; item += step) {
             const GtTile t = gt_tile(Q, s_tab, item);
-            const int half = t.n_mma / 2, row_w = t.e * P.N + t.n0 + (int)rank * kGtM;
-            const int row_a = t.i0 + (int)rank * half;
-            // one box of at least the half's rows: an issued TMA costs more than the rows behind them
-            const int bi = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : half <= 96 ? 3 : 4;
-            const CUtensorMap* tmA = &M.a[bi];
-            const uint32_t bytes = 2u * (NW * kGtAStage + (GATHER ? 0u : 128u * (uint32_t)gt_box(bi)));
-            for (int k = 0; k < Q.nst; k++) {
-                ok = warp_wait(tc_smem(&s_empty[s]), phase);
+            for (int i = 0; i < NB; i++) {
+                const int j = 32 * (SHARE * i + half) + lane;
+                int64_t src, dst;
+                dst_of[32 * i + lane] = j < t.cnt && row_pair(P, t.i0 + j, src, dst) ? (int)dst : -1;
+            }
+            __syncwarp();
+            const int row = t.n0 + (int)rank * kGtM + 32 * sub, row0 = row + piece * (32 / cw);  // whole pieces inside N
+            const bool live = row + lane < P.N;
+            uint8_t* out0 = static_cast<uint8_t*>(P.out) + (int64_t)row0 * (f32 ? 4 : 2);
+            float y[SEG ? NB : 1][NW][32];
+            for (int k = 0; k < Q.nst; k += Q.seg) {
+                ok = warp_wait(tc_smem(&s_afull[buf]), phase);
                 if (!ok) break;
-                if (gt_elect()) {
-                    const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes, bar = full0 + 8u * (uint32_t)s;
-                    if (rank == 0)
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&s_full[s])),
-                                     "r"(bytes)
-                                     : "memory");
-                    gt_tma2d(st, &M.w, k * kGtK, row_w, bar);
-                    if (GATED) gt_tma2d(st + kGtAStage, &M.u, k * kGtK, row_w, bar);
-                    if (!GATHER) gt_tma2d(st + b_off, tmA, k * kGtK, row_a, bar);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t tl = tmem + 256u * buf + ((uint32_t)(32 * sub) << 16);
+#pragma unroll(SEG ? NB : 1)
+                for (int i = 0; i < NB; i++) {
+                    const int c0 = 32 * (SHARE * i + half), cols = min(32, t.cnt - c0);
+                    if (cols <= 0) break;
+                    float(&yb)[NW][32] = y[SEG ? i : 0];
+                    gt_add<NW, SEG>(tl + (uint32_t)c0, k > 0, yb);
+                    if (SEG && k + Q.seg < Q.nst) continue;
+                    if (GATED) {
+#pragma unroll
+                        for (int j = 0; j < 32; j++) yb[0][j] = silu_f(yb[0][j]) * yb[NW - 1][j];
+                    }
+                    if (Q.vec) {
+                        // through shared memory, [input row][32 weight rows]: then 16 bytes per thread and store
+#pragma unroll
+                        for (int p = 0; p < PASS; p++) {
+                            if (!f32 && p > 0) break;
+                            __syncwarp();
+                            if (f32) {
+                                float* f = reinterpret_cast<float*>(stage_out);
+#pragma unroll
+                                for (int j = 0; j < 32 / PASS; j++) f[32 * j + lane] = yb[0][32 / PASS * p + j];
+                            } else {
+                                uint16_t* h = reinterpret_cast<uint16_t*>(stage_out);
+                                if (P.type == BITSMOE_F16) {
+#pragma unroll
+                                    for (int j = 0; j < 32; j++) h[32 * j + lane] = (uint16_t)to_half_bits(yb[0][j], BITSMOE_F16);
+                                } else {
+#pragma unroll
+                                    for (int j = 0; j < 32; j++) h[32 * j + lane] = (uint16_t)to_half_bits(yb[0][j], BITSMOE_BF16);
+                                }
+                            }
+                            __syncwarp();
+                            const int j0 = 32 / PASS * p, n = f32 ? min(32 / PASS, cols - j0) : cols;
+#pragma unroll 4
+                            for (int j = lane / cw; j < n; j += 32 / cw) {
+                                const int dst = dst_of[32 * i + j0 + j];
+                                const uint4 w = stage_out[j * cw + piece];
+                                if (dst >= 0 && row0 < P.N) *reinterpret_cast<uint4*>(out0 + dst * pitch) = w;
+                            }
+                        }
+                    } else {
+                        const int my_dst = dst_of[32 * i + lane];
+#pragma unroll
+                        for (int j = 0; j < 32; j++) {
+                            const int dst = __shfl_sync(0xffffffffu, my_dst, j);
+                            const float o[1] = {yb[0][j]};
+                            if (dst >= 0 && live) store_elems<1>(P.out, P.out_type, (int64_t)dst * P.N + row + lane, o);
+                        }
+                    }
                 }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
-                if (++s == Q.stages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
+                if (lane == 0) gt_arrive_cluster(aempty0 + 8u * (uint32_t)buf);
+                buf ^= 1;
+                if (buf == 0) phase ^= 1u;
             }
         }
         if (!ok) *fail = 1;
-    } else if (warp == 1) {
-        if (rank == 0) {
-            int s = 0, buf = 0;
-            uint32_t phase = 0, aphase = 1;
+    } else {
+        if constexpr (GATHER && SEG) gt_regs<48, false>();
+        if (warp == 0) {
+            // the weights' tiles, and contiguous input rows; the pair's bytes complete on the first CTA's barrier
+            const uint32_t full0 = gt_mapa(tc_smem(&s_full[0]), 0);
+            int s = 0;
+            uint32_t phase = 1;  // parity of the stage's last release: nothing to wait for in the first round
             bool ok = true;
             for (int item = first; item < total && ok; item += step) {
                 const GtTile t = gt_tile(Q, s_tab, item);
-                const uint32_t idesc = tc_idesc(2 * kGtM, t.n_mma) | (P.type == BITSMOE_BF16 ? (1u << 7) | (1u << 10) : 0u);
-                const uint32_t d = tmem + 256u * buf;
-                ok = warp_wait(tc_smem(&s_aempty[buf]), aphase);
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const int half = t.n_mma / 2, row_w = t.e * P.N + t.n0 + (int)rank * kGtM;
+                const int row_a = t.i0 + (int)rank * half;
+                // one box of at least the half's rows: an issued TMA costs more than the rows behind them
+                const int bi = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : half <= 96 ? 3 : 4;
+                const CUtensorMap* tmA = &M.a[bi];
+                const uint32_t bytes = 2u * (NW * kGtAStage + (GATHER ? 0u : 128u * (uint32_t)gt_box(bi)));
                 for (int k = 0; k < Q.nst; k++) {
-                    ok = warp_wait(tc_smem(&s_full[s]), phase);
+                    ok = warp_wait(tc_smem(&s_empty[s]), phase);
                     if (!ok) break;
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     if (gt_elect()) {
-                        const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes;
-                        // a K step of 16 elements is 32 bytes further in the swizzled row: 2 in the descriptor's address
-                        const uint64_t ad = tc_desc_sw128(st), bd = tc_desc_sw128(st + b_off);
-#pragma unroll
-                        for (int kk = 0; kk < kGtK / 16; kk++)
-#pragma unroll
-                            for (int m = 0; m < NW; m++)
-                                gt_mma(d + 128u * m, ad + (uint64_t)(m * (kGtAStage >> 4) + 2 * kk), bd + 2u * kk, idesc,
-                                       (k > 0 || kk > 0) ? 1u : 0u);
-                        gt_commit_both(tc_smem(&s_empty[s]));
-                        if (k == Q.nst - 1) gt_commit_both(tc_smem(&s_afull[buf]));
+                        const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes, bar = full0 + 8u * (uint32_t)s;
+                        if (rank == 0)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(&s_full[s])),
+                                         "r"(bytes)
+                                         : "memory");
+                        gt_tma2d(st, &M.w, k * kGtK, row_w, bar);
+                        if (GATED) gt_tma2d(st + kGtAStage, &M.u, k * kGtK, row_w, bar);
+                        if (!GATHER) gt_tma2d(st + b_off, tmA, k * kGtK, row_a, bar);
                     }
                     __syncwarp();
                     if (++s == Q.stages) {
@@ -492,149 +574,117 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
                         phase ^= 1u;
                     }
                 }
-                buf ^= 1;
-                if (buf == 0) aphase ^= 1u;
             }
             if (!ok) *fail = 1;
-        }
-    } else if (warp < kGtRelayWarp) {
-        // accumulators to out: a thread owns a weight row, a column of tensor memory is an input row
-        const int sub = warp & 3;  // the 32 lanes of tensor memory a warp can read
-        int* dst_of = s_dst[warp - kGtEpiWarp0];
-        uint4* stage_out = s_out[warp - kGtEpiWarp0];
-        int n = 0;
-        for (int item = first; item < total; item += step, n++) {
-            const GtTile t = gt_tile(Q, s_tab, item);
-            const int buf = n & 1;
-            for (int j = lane; j < t.cnt; j += 32) {
-                int64_t src, dst;
-                dst_of[j] = row_pair(P, t.i0 + j, src, dst) ? (int)dst : -1;
-            }
-            __syncwarp();
-            if (!warp_wait(tc_smem(&s_afull[buf]), (uint32_t)(n >> 1) & 1u)) {
-                *fail = 1;
-                break;
-            }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const int row = t.n0 + (int)rank * kGtM + 32 * sub + lane;
-            const bool live = row < P.N;
-            const uint32_t tl = tmem + 256u * buf + ((uint32_t)(32 * sub) << 16);
-            for (int c0 = 0; c0 < t.cnt; c0 += 32) {
-                uint32_t v[NW][32];
+        } else if (warp == 1) {
+            if (rank == 0) {
+                int s = 0, buf = 0;
+                uint32_t phase = 0, aphase = 1;
+                bool ok = true;
+                for (int item = first; item < total && ok; item += step) {
+                    const GtTile t = gt_tile(Q, s_tab, item);
+                    const uint32_t idesc = tc_idesc(2 * kGtM, t.n_mma) | (P.type == BITSMOE_BF16 ? (1u << 7) | (1u << 10) : 0u);
+                    int left = 0;  // stages left in the segment
+                    for (int k = 0; k < Q.nst; k++) {
+                        const uint32_t d = tmem + 256u * buf;
+                        const bool begin = left == 0;
+                        if (begin) {
+                            left = min(Q.seg, Q.nst - k);
+                            ok = warp_wait(tc_smem(&s_aempty[buf]), aphase);
+                            if (!ok) break;
+                        }
+                        const bool end = --left == 0;
+                        ok = warp_wait(tc_smem(&s_full[s]), phase);
+                        if (!ok) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        if (gt_elect()) {
+                            const uint32_t st = sbase + (uint32_t)s * Q.stage_bytes;
+                            // a K step of 16 elements is 32 bytes further in the swizzled row: 2 in the descriptor's address
+                            const uint64_t ad = tc_desc_sw128(st), bd = tc_desc_sw128(st + b_off);
 #pragma unroll
-                for (int m = 0; m < NW; m++) gt_ld32(tl + 128u * m + (uint32_t)c0, v[m]);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                if (GATED) {
+                            for (int kk = 0; kk < kGtK / 16; kk++)
 #pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        v[0][j] = __float_as_uint(silu_f(__uint_as_float(v[0][j])) * __uint_as_float(v[NW - 1][j]));
-                }
-                if (Q.vec) {
-                    // through shared memory, [input row][32 weight rows]: then 16 bytes per thread and store
-                    const int cols = min(32, t.cnt - c0), cw = P.out_type == BITSMOE_F32 ? 8 : 4;  // 16-byte pieces a row
-                    __syncwarp();
-                    if (P.out_type == BITSMOE_F32) {
-                        float* f = reinterpret_cast<float*>(stage_out);
-#pragma unroll
-                        for (int j = 0; j < 32; j++) f[32 * j + lane] = __uint_as_float(v[0][j]);
-                    } else {
-                        uint16_t* h = reinterpret_cast<uint16_t*>(stage_out);
-                        if (P.type == BITSMOE_F16) {
-#pragma unroll
-                            for (int j = 0; j < 32; j++)
-                                h[32 * j + lane] = (uint16_t)to_half_bits(__uint_as_float(v[0][j]), BITSMOE_F16);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; j++)
-                                h[32 * j + lane] = (uint16_t)to_half_bits(__uint_as_float(v[0][j]), BITSMOE_BF16);
+                                for (int m = 0; m < NW; m++)
+                                    gt_mma(d + 128u * m, ad + (uint64_t)(m * (kGtAStage >> 4) + 2 * kk), bd + 2u * kk, idesc,
+                                           (!begin || kk > 0) ? 1u : 0u);
+                            gt_commit_both(tc_smem(&s_empty[s]));
+                            if (end) gt_commit_both(tc_smem(&s_afull[buf]));
+                        }
+                        __syncwarp();
+                        if (++s == Q.stages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                        if (end) {
+                            buf ^= 1;
+                            if (buf == 0) aphase ^= 1u;
                         }
                     }
+                }
+                if (!ok) *fail = 1;
+            }
+        } else if (GATHER && warp == kGtRelayWarp) {
+            // A stage's gathered rows have arrived: the copies wrote shared memory as ordinary
+            // stores do, the MMAs read it as the asynchronous proxy; then tell the first CTA.
+            // (A gathering thread that fenced would wait for its later copies as well.)
+            const uint32_t full0 = gt_mapa(tc_smem(&s_full[0]), 0);
+            int s = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int item = first; item < total && ok; item += step)
+                for (int k = 0; k < Q.nst; k++) {
+                    ok = warp_wait(tc_smem(&s_rows[s]), phase);
+                    if (!ok) break;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (gt_elect()) gt_arrive_cluster(full0 + 8u * (uint32_t)s);
                     __syncwarp();
-                    const int piece = lane % cw;
-                    const int row0 = t.n0 + (int)rank * kGtM + 32 * sub + piece * (32 / cw);  // whole pieces inside N
-#pragma unroll 4
-                    for (int j = lane / cw; j < cols; j += 32 / cw) {
-                        const int dst = dst_of[c0 + j];
-                        const uint4 w = stage_out[j * cw + piece];
-                        if (dst >= 0 && row0 < P.N)
-                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(P.out) +
-                                                      ((int64_t)dst * P.N + row0) * (16 / (32 / cw))) = w;
+                    if (++s == Q.stages) {
+                        s = 0;
+                        phase ^= 1u;
                     }
-                } else {
-                    const int my_dst = c0 + lane < t.cnt ? dst_of[c0 + lane] : -1;
+                }
+            if (!ok) *fail = 1;
+        } else if (GATHER && warp >= kGatherWarp0) {
+            // this CTA's half of the piece's input rows: 8 threads a row, 16 bytes each, chunk ch of row r at ch ^ (r mod 8)
+            const int gt = tid - 32 * kGatherWarp0, ch = gt & 7, r0 = gt >> 3;
+            constexpr int RS = 4 * kGtGatherWarps, RPT = kGtM / RS;  // rows a thread fetches: r0 + RS i of up to 128
+            const uint32_t b0 = sbase + b_off + 128u * r0 + ((uint32_t)(ch ^ (r0 & 7)) << 4);  // RS is a multiple of 8
+            int s = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int item = first; item < total && ok; item += step) {
+                const GtTile t = gt_tile(Q, s_tab, item);
+                const int half = t.n_mma / 2;
+                const uint16_t* src_row[RPT];  // NULL: zeros
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        const int dst = __shfl_sync(0xffffffffu, my_dst, j);
-                        const float y[1] = {__uint_as_float(v[0][j])};
-                        if (dst >= 0 && live) store_elems<1>(P.out, P.out_type, (int64_t)dst * P.N + row, y);
+                for (int i = 0; i < RPT; i++) {
+                    const int r = r0 + RS * i, j = (int)rank * half + r;
+                    int64_t src = 0, dst;
+                    src_row[i] = r < half && j < t.cnt && row_pair(P, t.i0 + j, src, dst) ? P.a + src * P.lda + 8 * ch : nullptr;
+                }
+                for (int k = 0; k < Q.nst; k++) {
+                    ok = warp_wait(tc_smem(&s_empty[s]), phase);
+                    if (!ok) break;
+                    const uint32_t b = b0 + (uint32_t)s * Q.stage_bytes;
+                    const bool in_k = k * kGtK + 8 * ch < P.D;
+#pragma unroll
+                    for (int i = 0; i < RPT; i++)
+                        if (r0 + RS * i < half) {
+                            const bool in = src_row[i] != nullptr && in_k;
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(b + 128u * RS * i),
+                                         "l"(in ? src_row[i] + k * kGtK : P.a), "r"(in ? 16 : 0)
+                                         : "memory");
+                        }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc_smem(&s_rows[s])) : "memory");
+                    if (++s == Q.stages) {
+                        s = 0;
+                        phase ^= 1u;
                     }
                 }
             }
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) gt_arrive_cluster(gt_mapa(tc_smem(&s_aempty[buf]), 0));
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (!ok) *fail = 1;
         }
-    } else if (GATHER && warp == kGtRelayWarp) {
-        // A stage's gathered rows have arrived: the copies wrote shared memory as ordinary
-        // stores do, the MMAs read it as the asynchronous proxy; then tell the first CTA.
-        // (A gathering thread that fenced would wait for its later copies as well.)
-        const uint32_t full0 = gt_mapa(tc_smem(&s_full[0]), 0);
-        int s = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int item = first; item < total && ok; item += step)
-            for (int k = 0; k < Q.nst; k++) {
-                ok = warp_wait(tc_smem(&s_rows[s]), phase);
-                if (!ok) break;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                if (gt_elect()) gt_arrive_cluster(full0 + 8u * (uint32_t)s);
-                __syncwarp();
-                if (++s == Q.stages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
-        if (!ok) *fail = 1;
-    } else if (GATHER) {
-        // this CTA's half of the piece's input rows: 8 threads a row, 16 bytes each, chunk ch of row r at ch ^ (r mod 8)
-        const int gt = tid - 32 * kGtGatherWarp0, ch = gt & 7, r0 = gt >> 3;
-        constexpr int RS = 4 * kGtGatherWarps, RPT = kGtM / RS;  // rows a thread fetches: r0 + RS i of up to 128
-        const uint32_t b0 = sbase + b_off + 128u * r0 + ((uint32_t)(ch ^ (r0 & 7)) << 4);  // RS is a multiple of 8
-        int s = 0;
-        uint32_t phase = 1;
-        bool ok = true;
-        for (int item = first; item < total && ok; item += step) {
-            const GtTile t = gt_tile(Q, s_tab, item);
-            const int half = t.n_mma / 2;
-            const uint16_t* src_row[RPT];  // NULL: zeros
-#pragma unroll
-            for (int i = 0; i < RPT; i++) {
-                const int r = r0 + RS * i, j = (int)rank * half + r;
-                int64_t src = 0, dst;
-                src_row[i] = r < half && j < t.cnt && row_pair(P, t.i0 + j, src, dst) ? P.a + src * P.lda + 8 * ch : nullptr;
-            }
-            for (int k = 0; k < Q.nst; k++) {
-                ok = warp_wait(tc_smem(&s_empty[s]), phase);
-                if (!ok) break;
-                const uint32_t b = b0 + (uint32_t)s * Q.stage_bytes;
-                const bool in_k = k * kGtK + 8 * ch < P.D;
-#pragma unroll
-                for (int i = 0; i < RPT; i++)
-                    if (r0 + RS * i < half) {
-                        const bool in = src_row[i] != nullptr && in_k;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(b + 128u * RS * i),
-                                     "l"(in ? src_row[i] + k * kGtK : P.a), "r"(in ? 16 : 0)
-                                     : "memory");
-                    }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc_smem(&s_rows[s])) : "memory");
-                if (++s == Q.stages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok) *fail = 1;
     }
     __syncwarp();
     if (*fail && lane == 0 && P.status) atomicOr(P.status, BITSMOE_ST_TIMEOUT);
@@ -646,7 +696,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER), 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <bool GATED, bool GATHER>
+template <bool GATED, bool GATHER, bool SEG>
 static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
     GmmTcParams Q{};
     Q.p = P;
@@ -655,6 +705,8 @@ static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
     Q.tok = std::min(Q.tok, most);
     Q.ntiles = (P.N + 2 * kGtM - 1) / (2 * kGtM);
     Q.nst = (P.D + kGtK - 1) / kGtK;
+    const int segs = SEG ? (Q.nst + gt_segment(GATED) - 1) / gt_segment(GATED) : 1;
+    Q.seg = (Q.nst + segs - 1) / segs;
     Q.stage_bytes = (GATED ? 2 : 1) * kGtAStage + (uint32_t)Q.tok / 2 * 128u;
     const size_t tab = roundup(4ull * (P.E + 1), 16);
     Q.stages = (int)std::min<size_t>(kGtMaxStages, (kGtSmem - 1024 - tab) / Q.stage_bytes);
@@ -670,12 +722,12 @@ static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_gmm_tc<GATED, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGtSmem);
+        e = cudaFuncSetAttribute(k_gmm_tc<GATED, GATHER, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGtSmem);
     if (e != cudaSuccess) return set_cuda_error(e);
     const int64_t tiles = (int64_t)Q.ntiles * (std::min(P.P, P.E) + P.P / Q.tok);  // at least as many as there are
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(sms / 2, tiles)));
-    cfg.blockDim = dim3(gt_threads(GATHER));
+    cfg.blockDim = dim3(gt_threads(GATHER, SEG));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -687,8 +739,14 @@ static int launch_gmm_tc(const GmmParams& P, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, k_gmm_tc<GATED, GATHER>, Q, M);
+    e = cudaLaunchKernelEx(&cfg, k_gmm_tc<GATED, GATHER, SEG>, Q, M);
     return e == cudaSuccess ? BITSMOE_OK : set_cuda_error(e);
+}
+
+template <bool GATED, bool GATHER>
+static int launch_gmm_seg(const GmmParams& P, cudaStream_t s) {
+    return P.out_type == BITSMOE_F32 && P.D > kGtK * gt_segment(GATED) ? launch_gmm_tc<GATED, GATHER, true>(P, s)
+                                                                       : launch_gmm_tc<GATED, GATHER, false>(P, s);
 }
 
 }  // namespace bitsmoe
@@ -728,9 +786,10 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* strea
     P.out_type = d.out_type;
     P.scatter = d.scatter != 0;
     cudaStream_t s = (cudaStream_t)stream;
-    if (d.n_rows > kGmmTcRows * (int64_t)d.n_experts) {
-        if (d.rows) return d.W_up ? launch_gmm_tc<true, true>(P, s) : launch_gmm_tc<false, true>(P, s);
-        return d.W_up ? launch_gmm_tc<true, false>(P, s) : launch_gmm_tc<false, false>(P, s);
+    const int64_t tiles = (int64_t)((P.N + 2 * kGtM - 1) / (2 * kGtM)) * std::min(P.P, P.E);  // were no two pairs of one expert
+    if (tiles >= kTcTiles || P.P > kTcRows * P.E) {
+        if (d.rows) return d.W_up ? launch_gmm_seg<true, true>(P, s) : launch_gmm_seg<false, true>(P, s);
+        return d.W_up ? launch_gmm_seg<true, false>(P, s) : launch_gmm_seg<false, false>(P, s);
     }
     if (d.in_type == BITSMOE_BF16) return d.W_up ? launch_gmm_mv<true, true>(P, s) : launch_gmm_mv<true, false>(P, s);
     return d.W_up ? launch_gmm_mv<false, true>(P, s) : launch_gmm_mv<false, false>(P, s);

@@ -558,6 +558,40 @@ def test_grouped_matmul_bad_indexes(scale):
         _within(out, ref, tol + _rounding(ref, F32) * (tol > 0), scatter)
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("form", ["few", "many", "gated"])
+@pytest.mark.parametrize("K", [760, 776, 4096])
+def test_grouped_matmul_sums_of_one_sign(K, form, gather):
+    """fp32 results of long sums whose terms have one sign, where an accumulator that cuts toward zero drifts with the
+    length.  At most 48 steps of 16 k's go into one such accumulator.  A step aligns 16 products and the partial sum to
+    the largest of them, with two bits or more below fp32's 24, cuts them there and cuts their sum to 24 bits: up to
+    17 / 4 + 1 = 5.25 units (2^-23) of the partial sum, half of that on average, and the partial sums of equally
+    distributed terms are half of the last one on average.  So: 48 x 5.25 = 252 units at most, 48 x 5.25 / 4 = 63 on
+    average, and the few of the other additions.  (A single accumulator's average at K = 4096 would be 336.)
+    (The first form of this bound counted the cut of the sum alone, 48 and 24 units, and failed with 34 on average.)
+    Gated: every gate is 40, whose SiLU is 40 in fp32."""
+    g = _gen(K)
+    E, N, per = 3, 96, 6 if form == "few" else 70
+    P = E * per
+    a = torch.rand((P, K), generator=g, device="cuda").half() + 0.5
+    W = (torch.rand((E, N, K), generator=g, device="cuda") + 0.5).half()
+    gate = None
+    if form == "gated":
+        gate = torch.zeros_like(W)
+        gate[:, :, 0] = 40.0
+        a[:, 0] = 1.0
+    rows = torch.randperm(P, generator=g, device="cuda").to(torch.int32) if gather else None
+    out = torch.zeros((P, N), device="cuda")
+    off = _offsets([per] * E)
+    B.grouped_matmul(a, W if gate is None else gate, off, out, W_up=None if gate is None else W, rows=rows)
+    x = (a if rows is None else a[rows.long()]).double().view(E, per, K)
+    ref = torch.einsum("epk,enk->epn", x, W.double()).reshape(P, N) * (1.0 if gate is None else 40.0)
+    err = (out.double() - ref).abs() / ref
+    extra = 8 + (K + 767) // 768  # the joins, the gate's SiLU and product
+    assert float(err.max()) <= (252 + extra) * U23
+    assert float(err.mean()) <= 63 * U23 + 4 * U24
+
+
 def test_grouped_matmul_non_finite_rows_stay_apart():
     """NaN and infinities in one row of A, or in another expert's rows and matrix, reach no other row."""
     g = _gen(11)
@@ -791,3 +825,14 @@ def test_moe_block_stack(kind, T):
         assert _rel(y, want) <= 4e-3  # x may round the other way in the last bit of fp16, 2e-3 on either side
     blocks[-1].finish(h, y)
     assert bool(torch.isfinite(h).all()) and B.read_status(st) == 0
+
+
+def test_empty_batch():
+    from mixed_precision_decode_b200.layer import DenseMoEFFN, MoEBlock
+    g = _gen(3)
+    E, K, d, d_ff = 4, 2, 64, 32
+    ffn = DenseMoEFFN(_randn(g, E, d_ff, d).half(), _randn(g, E, d_ff, d).half(), _randn(g, E, d, d_ff).half(), K)
+    blk = MoEBlock(ffn, _randn(g, d), _randn(g, E, d).half())
+    h = _randn(g, 0, d)
+    y = blk.forward(h)
+    assert y.shape == (0, d) and blk.finish(h, y).shape == (0, d)

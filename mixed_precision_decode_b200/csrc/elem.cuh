@@ -20,8 +20,35 @@ __device__ __forceinline__ uint32_t to_half_bits(float v, int type) {
     return type == BITSMOE_F16 ? (uint32_t)__half_as_ushort(__float2half_rn(v))
                                : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
-    return to_half_bits(a, type) | (to_half_bits(b, type) << 16);
+// A pair of elements in a word, low half first.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <bool F16>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float2 f = unpack2<F16>(u[j]);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+    }
+}
+template <bool F16>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]), pack2<F16>(v[4], v[5]), pack2<F16>(v[6], v[7]));
 }
 
 // V elements (8: 16-byte aligned; 1: any) from element i of p.
@@ -35,12 +62,10 @@ __device__ __forceinline__ void load_elems(const void* p, int type, int64_t i, f
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         } else {
             const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                v[2 * j] = half_bits(u[j] & 0xffffu, type);
-                v[2 * j + 1] = half_bits(u[j] >> 16, type);
-            }
+            if (type == BITSMOE_F16)
+                unpack8<true>(w, v);
+            else
+                unpack8<false>(w, v);
         }
     } else {
 #pragma unroll
@@ -57,10 +82,10 @@ __device__ __forceinline__ void store_elems(void* p, int type, int64_t i, const 
             float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
             f[0] = make_float4(v[0], v[1], v[2], v[3]);
             f[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else if (type == BITSMOE_F16) {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack8<true>(v);
         } else {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-                make_uint4(pack2(v[0], v[1], type), pack2(v[2], v[3], type), pack2(v[4], v[5], type),
-                           pack2(v[6], v[7], type));
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack8<false>(v);
         }
     } else {
 #pragma unroll

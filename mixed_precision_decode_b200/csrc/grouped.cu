@@ -243,10 +243,10 @@ constexpr size_t kGtSmem = 204 * 1024;           // dynamic shared memory a CTA 
 // error of about 1.2e-9 K of the results' norm (measured: 4.9e-6 at K = 4096, twice that when gated; 4e-6 of a
 // sum of 768 terms of one sign), nothing beside a rounding to 16 bits but several times an fp32 sum's.  For fp32
 // results it is kept under 1e-6: at most 768 k's (gated: 384) are summed in tensor memory, and fp32 additions to
-// nearest in the epilogue's registers join them.  The epilogue is then 8 warps with 128 sums a thread: 384 threads launch with 168 registers
-// each; the 640 of the gathering kernel with 96, of which the others give up half:
-// 256 x 168 + 384 x 48 = 640 x 96.  (At 2,048 pairs x 768 with fp32 results three segments took 126 us
-// instead of 103.)
+// nearest in the epilogue's registers join them.  The epilogue is then 8 warps with 128 sums a thread: 384
+// threads launch with 168 registers each; the 640 of the gathering kernel with 96, of which the others give up
+// half: 256 x 168 + 384 x 48 = 640 x 96.  (At 16,384 pairs of 128 experts, 2048 x 768, fp32 results, three
+// segments took 126 us instead of 103.)
 constexpr int gt_segment(bool gated) { return gated ? 6 : 12; }
 
 constexpr int kGtBoxes = 5;

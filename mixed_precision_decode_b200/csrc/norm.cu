@@ -11,9 +11,16 @@
 //
 // One pass over memory: a row stays in registers between its loads and its stores,
 // so the step is bound by HBM (h and y read once, h' and x written once).  A row
-// belongs to a CTA (one warp when it fits 4 chunks of 8 elements per lane: no CTA
+// belongs to a CTA (to one warp when that holds it in a chunk per lane: no CTA
 // barrier); the two sums are reduced in a fixed order, so results do not depend on
 // timing.  Rows too wide for registers are read once more per sum.
+//
+// 8,192 x 4,096, bf16 h and x, fp32 y, both norms and a gate per channel: 70 us, 4.8 TB/s
+// (the floor is 52).  The rest is each row's chain -- loads, two sums over the CTA, three
+// vectors from L1 -- at 94% of the SM's threads.  Slower were: two rows a CTA (83 us), 256
+// threads a row (72), loads through a ring in shared memory by persistent CTAs (73 to 124,
+// by its depth), the channel vectors held in registers (86 and more): all hold fewer rows
+// or leave L1 too small for the vectors.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -200,13 +207,11 @@ constexpr int kNormWarpRows = 8;  // rows (warps) per CTA when a row belongs to 
 template <int V>
 static int launch_norm(const NormParams& P, cudaStream_t s) {
     const int nch = P.d / V;
-    const int warp_max = 4;             // chunks per lane of a row that stays in one warp
-    if (nch <= 32 * warp_max && P.T > 1) {
+    // A row in one warp while it is one chunk a lane; longer ones are a chain of too many instructions (8,192 rows of
+    // 256: 4.1 us against 8.9 with a CTA each; of 512: 8.7 and 9.0, but 16 rows 2.6 and 1.9; of 1024: 27 and 14).
+    if (nch <= 32 && P.T > 1) {
         const dim3 grid((unsigned)((P.T + kNormWarpRows - 1) / kNormWarpRows)), block(32 * kNormWarpRows);
-        const int nc = (nch + 31) / 32;
-        if (nc <= 1) return launch_pdl(k_norm_residual<V, 1, true>, grid, block, 0, s, P);
-        if (nc <= 2) return launch_pdl(k_norm_residual<V, 2, true>, grid, block, 0, s, P);
-        return launch_pdl(k_norm_residual<V, 4, true>, grid, block, 0, s, P);
+        return launch_pdl(k_norm_residual<V, 1, true>, grid, block, 0, s, P);
     }
     const dim3 grid((unsigned)P.T);
     auto threads = [&](int nc) { return (unsigned)std::max<int64_t>(32, roundup((nch + nc - 1) / nc, 32)); };

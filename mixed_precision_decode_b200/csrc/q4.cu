@@ -281,38 +281,33 @@ __device__ __forceinline__ uint4 q4_ld(const uint8_t* p) {
     return v;
 }
 
-// U consecutive tiles of RB row blocks in one lane's registers: codes, and the scales of
-// rows g and g + 8 (of both groups of a tile when G = 32).  codes[r]: this lane's 16
-// bytes of the first tile of row block r; scales[r]: its rows' scales of that tile's group.
-template <int G, int RB, int U>
+// U consecutive tiles in one lane's registers: codes, and the scales of rows g and g + 8 (of
+// both groups of a tile when G = 32).  codes: this lane's 16 bytes of the first tile; scales:
+// its rows' scales of that tile's group.
+template <int G, int U>
 struct Q4Tiles {
     static constexpr int NS = G < kQ4Cols ? kQ4Cols / G : 1;
-    uint4 w[U][RB];
-    uint16_t s[U][RB][NS][2];
+    uint4 w[U];
+    uint16_t s[U][NS][2];
 
-    __device__ __forceinline__ void load(const uint8_t* const (&codes)[RB], const uint16_t* const (&scales)[RB]) {
+    __device__ __forceinline__ void load(const uint8_t* codes, const uint16_t* scales) {
 #pragma unroll
-        for (int u = 0; u < U; u++)
+        for (int u = 0; u < U; u++) {
+            w[u] = q4_ld(codes + u * kQ4TileBytes);
 #pragma unroll
-            for (int r = 0; r < RB; r++) {
-                w[u][r] = q4_ld(codes[r] + u * kQ4TileBytes);
-#pragma unroll
-                for (int n = 0; n < NS; n++) {
-                    const uint16_t* sc = scales[r] + (G > kQ4Cols ? u / (G / kQ4Cols) : u * NS + n) * kQ4Rows;
-                    s[u][r][n][0] = __ldg(sc);
-                    s[u][r][n][1] = __ldg(sc + 8);
-                }
+            for (int n = 0; n < NS; n++) {
+                const uint16_t* sc = scales + (G > kQ4Cols ? u / (G / kQ4Cols) : u * NS + n) * kQ4Rows;
+                s[u][n][0] = __ldg(sc);
+                s[u][n][1] = __ldg(sc + 8);
             }
+        }
     }
 };
 // Moves tile pointers on by n tiles (a multiple of 2 when a group is two tiles).
-template <int G, int RB>
-__device__ __forceinline__ void q4_advance(const uint8_t* (&codes)[RB], const uint16_t* (&scales)[RB], int n) {
-#pragma unroll
-    for (int r = 0; r < RB; r++) {
-        codes[r] += n * kQ4TileBytes;
-        scales[r] += n * kQ4Cols / G * kQ4Rows;
-    }
+template <int G>
+__device__ __forceinline__ void q4_advance(const uint8_t*& codes, const uint16_t*& scales, int n) {
+    codes += n * kQ4TileBytes;
+    scales += n * kQ4Cols / G * kQ4Rows;
 }
 
 // One tile times the B operands of NB blocks of 8 columns (2 rows of h), added to the row
@@ -377,9 +372,9 @@ constexpr size_t kQ4T1Smem = 200 * 1024;
 
 // U tiles of one row block times h; sums: of the first tile's group.
 template <int G, int U>
-__device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, 1, U>& tiles, const uint32_t* hb, const float* sums, int g,
+__device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, U>& tiles, const uint32_t* hb, const float* sums, int g,
                                             int c, int (&part)[1][4], float (&acc)[1][2]) {
-    constexpr int NS = Q4Tiles<G, 1, U>::NS;
+    constexpr int NS = Q4Tiles<G, U>::NS;
 #pragma unroll
     for (int u = 0; u < U; u++) {
         uint4 bw[1] = {make_uint4(0, 0, 0, 0)};
@@ -387,7 +382,7 @@ __device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, 1, U>& tiles, const
         float start[NS][1];
 #pragma unroll
         for (int n = 0; n < NS; n++) start[n][0] = sums[(u * kQ4Cols / G + n) * 2 + (c & 1)];
-        q4_tile<G, 1, 1>(tiles.w[u][0], tiles.s[u][0], bw, start, u & 1, part, acc);
+        q4_tile<G, 1, 1>(tiles.w[u], tiles.s[u], bw, start, u & 1, part, acc);
     }
 }
 
@@ -431,12 +426,12 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
         uint32_t* hb = s_h + ((size_t)j * ntiles) * 64;
         const float* sums = s_sum + j * ngroups * 2;
         float scale = 1.0f;
-        Q4Tiles<G, 1, U> tiles;
+        Q4Tiles<G, U> tiles;
         const bool batches = t1 - t0 >= U;
         if (e >= 0 && t0 < t1) {
             const uint8_t* base = P.M.blob + ((int64_t)e * nblk + blockIdx.x) * bb;
-            const uint8_t* codes[1] = {base + 16 * lane};
-            const uint16_t* scales[1] = {reinterpret_cast<const uint16_t*>(base + scale_off) + g};
+            const uint8_t* codes = base + 16 * lane;
+            const uint16_t* scales = reinterpret_cast<const uint16_t*>(base + scale_off) + g;
             q4_advance<G>(codes, scales, t0);
             if (batches) tiles.load(codes, scales);
             // chunks of 16 columns, one a lane: the whole range in most layers, else the first 32 stay in registers
@@ -495,8 +490,8 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
             int part[1][4];
             if (e >= 0 && t0 < t1) {
                 const uint8_t* base = P.M.blob + ((int64_t)e * nblk + blockIdx.x + (int64_t)i * gridDim.x) * bb;
-                const uint8_t* codes[1] = {base + 16 * lane};
-                const uint16_t* scales[1] = {reinterpret_cast<const uint16_t*>(base + scale_off) + g};
+                const uint8_t* codes = base + 16 * lane;
+                const uint16_t* scales = reinterpret_cast<const uint16_t*>(base + scale_off) + g;
                 q4_advance<G>(codes, scales, t0);
                 int tb = t0;
                 for (; tb + U <= t1; tb += U) {
@@ -505,7 +500,7 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
                     q4_advance<G>(codes, scales, U);
                 }
                 for (; tb < t1; tb += V) {
-                    Q4Tiles<G, 1, V> one;
+                    Q4Tiles<G, V> one;
                     one.load(codes, scales);
                     q4_t1_batch<G, V>(one, hb + tb * 64, sums + tb * kQ4Cols / G * 2, g, c, part, acc);
                     q4_advance<G>(codes, scales, V);
@@ -918,6 +913,10 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_mt(const Q4Params P) {
         for (int t = t0; t < t1; t += kQ4CT) {
             if (!ring.wait()) {
                 if (lane == 0 && P.status) atomicOr(P.status, BITSMOE_ST_TIMEOUT);
+                for (int i = 1; i < kQ4Stages; i++) {  // the copies still on their way, with the same limit each
+                    ring.pop();
+                    ring.wait();
+                }
                 return;
             }
             q4_stage_any<G, NTL>(ring.slot(), min(kQ4CT, t1 - t), np, piece, acc, lane);
@@ -972,8 +971,10 @@ __global__ void __launch_bounds__(256) k_q4_sum(const Q4Params P) {
 constexpr int kQ4Sms = 148;    // SMs the launches are sized for
 constexpr int kQ4MaxE = 2048;  // the grouping keeps 4 numbers of each in shared memory (32 KB)
 
-// Pairs per piece, by the expected group size.  8 at most: the sums of more do not fit the registers.
-static int q4_tok(int pairs, int E) { return pairs / E <= 3 ? 4 : 8; }
+// Pairs per piece, by the expected group size.  8 at most: the sums of more do not fit the registers.  (Pieces of 4 and
+// of 8, us: 128 experts, 2048 x 768, 1 pair each 23.4 and 25.0, 4 pairs 43.1 and 45.1, 8 pairs 69.2 and 69.2;
+// 8 experts, 4096 x 4096, 8 pairs each 46.4 and 53.7, 16 pairs 76.0 and 73.1.)
+static int q4_tok(int pairs, int E) { return pairs / E <= 8 ? 4 : 8; }
 static int q4_slots(int pairs, int E) { return std::min(pairs, E) + pairs / q4_tok(pairs, E); }
 
 // The single-token kernel: h and the partial sums of a CTA's row blocks fit its shared memory.

@@ -31,7 +31,9 @@ namespace bitsmoe {
 
 constexpr int kRtThreads = 1024;
 constexpr int kRtWarps = kRtThreads / 32;
-constexpr int kRouteOneTokens = 128;  // tokens one CTA routes and groups
+// Tokens one CTA routes and groups.  (One launch and two, us: 128 experts, 64 tokens 8.1 and 7.1, 128 tokens
+// 13.2 and 7.2; 16 experts, 64 tokens 5.2 and 5.5, 128 tokens 7.1 and 5.5; 512 experts, 64 tokens 23.6 and 16.8.)
+constexpr int kRouteOneTokens = 32;
 constexpr int kRouteMaxBlocks = 148;  // CTAs of the two-launch path: one per SM (each sums the others' counts)
 constexpr int kRouteMaxE = 8192;
 constexpr int kRouteMaxK = 1024;

@@ -494,8 +494,11 @@ uint64_t bitsmoe_ffn_down_q4_workspace_bytes(const bitsmoe_ffn_dims* dims, int32
 int bitsmoe_ffn_down_q4_launches(const bitsmoe_ffn_dims* dims, int32_t group, int32_t T);
 
 /* bitsmoe_ffn_down with the down matrices [d_model][d_ff] in 4 bits.  Routing errors and
- * the slot-order sum as there; products keep fp32 precision (a group's sum is scaled in
- * fp32).  At most 2048 experts. */
+ * the slot-order sum as there.  h is a fixed-point number of 32 bits relative to a power
+ * of two above the row's largest |h| (one token: above that of a range of its columns),
+ * an error of at most 2^-31 of that; the products with the codes are exact integers, and a
+ * group's sum is scaled in fp32.  A row of h with a NaN or an infinity gives NaN.  At most
+ * 2048 experts. */
 typedef struct {
     bitsmoe_ffn_dims dims;
     int32_t group, tokens;
@@ -526,7 +529,10 @@ int bitsmoe_ffn_down_q4(const bitsmoe_q4_args *args, void *stream);
  * left as they are.  The sizes of the groups stay on the device: nothing waits for
  * them.  An offset outside [0, n_rows] or below the one before it is clamped, and a
  * row index outside A (or out, with scatter) is left out; both set BITSMOE_ST_BADGROUP.
- * Two sorted rows with the same output row race. */
+ * Two sorted rows with the same output row race; out must not overlap an operand.
+ * fp32 results of long sums: the tensor cores' accumulators cut toward zero, so at most
+ * 768 k's (gated: 384) are summed in one, and fp32 additions join them: about 1e-6 of the
+ * results' norm at most, 4e-6 of a result whose terms all have one sign. */
 typedef struct {
     const void *A;          /* dev, n_a_rows rows of n_in elements, a_stride elements apart (a multiple of 8, >= n_in) */
     const void *W;          /* dev [n_experts][n_out][n_in]; A, W and W_up are 16-byte aligned */
@@ -537,7 +543,7 @@ typedef struct {
     int32_t *status;        /* dev or NULL */
     int64_t a_stride;
     int32_t n_rows;         /* rows the groups may cover: rows of out, entries of `rows` */
-    int32_t n_a_rows, n_out;
+    int32_t n_a_rows, n_out; /* n_experts n_out < 2^31 - 256 */
     int32_t n_in;           /* a multiple of 8 */
     int32_t n_experts;      /* <= BITSMOE_GMM_MAX_EXPERTS */
     int32_t in_type;        /* BITSMOE_F16 or BITSMOE_BF16: A, W and W_up */
@@ -555,7 +561,8 @@ int bitsmoe_grouped_matmul(const bitsmoe_gmm_args *args, void *stream);
  *   h[t][j]   = SiLU(W_gate[e] x[t]) (W_up[e] x[t]),        e = topk_ids[t][j],
  *   out[t]    = sum_j gate_w[t][j] W_down[e] h[t][j]
  * -- the gated grouped product of the gathered tokens, the grouped product of h, and the
- * slot-order sum.  h is rounded to the matrices' type; sums are fp32. */
+ * slot-order sum.  h is rounded to the matrices' type (in fp16 a value beyond 65504
+ * becomes infinite); sums are fp32. */
 typedef struct {
     bitsmoe_ffn_dims dims;     /* d_model and d_ff multiples of 8 */
     int32_t tokens;

@@ -759,7 +759,7 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* strea
     if (d.n_rows < 0 || d.n_a_rows < 0 || d.n_out < 1 || d.n_in < 8 || d.n_in % 8 || d.n_experts < 1 ||
         d.n_experts > BITSMOE_GMM_MAX_EXPERTS || (d.in_type != BITSMOE_F16 && d.in_type != BITSMOE_BF16) ||
         (d.out_type != BITSMOE_F32 && d.out_type != d.in_type) || d.rows_per_a < 1 || d.reserved ||
-        (int64_t)d.n_experts * d.n_out > 0x7fffffff)
+        (int64_t)d.n_experts * d.n_out > 0x7fffffff - 2 * kGtM)  // a tile's last weight row is an int
         return BITSMOE_EINVAL;
     if (!d.rows && (d.scatter || d.rows_per_a != 1 || d.n_a_rows < d.n_rows)) return BITSMOE_EINVAL;
     if (d.n_rows == 0) return BITSMOE_OK;

@@ -1,11 +1,23 @@
 """User-facing objects over the C ABI: a packed projection, a spectral MoE gate/up
-layer, expert FFNs, routing and the block around them.  torch provides device memory and streams; every computation
-is a libbitsmoe kernel."""
+layer, expert FFNs, routing and the block around them.  torch provides device memory
+and streams; every computation is a libbitsmoe kernel."""
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
 from . import bitsmoe as B
+
+
+def _on(stream):
+    """Tensors that a call allocates for itself belong to the stream that its kernels run on: freed on return, their
+    memory then goes to later work of that stream alone."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
 
 
 class PackedProjection:
@@ -169,14 +181,16 @@ class Q4Down:
     def pack(cls, w_down: torch.Tensor, group: int = 64, status: torch.Tensor | None = None, stream=None) -> "Q4Down":
         """Quantise w_down [E][d_model][d_ff] (float32, float16 or bfloat16, on the GPU)."""
         n = B.q4_bytes(*w_down.shape, group)
-        blob = torch.empty(n, dtype=torch.uint8, device=w_down.device)
-        B.q4_pack(w_down.contiguous(), group, blob, status, stream)
+        with _on(stream):
+            blob = torch.empty(n, dtype=torch.uint8, device=w_down.device)
+            B.q4_pack(w_down.contiguous(), group, blob, status, stream)
         return cls(blob, w_down.shape, group)
 
     def unpack(self, stream=None) -> torch.Tensor:
         """The stored values, [E][d_model][d_ff] f32."""
-        w = torch.empty(self.shape, dtype=torch.float32, device=self.blob.device)
-        B.q4_unpack(self.blob, self.group, w, stream)
+        with _on(stream):
+            w = torch.empty(self.shape, dtype=torch.float32, device=self.blob.device)
+            B.q4_unpack(self.blob, self.group, w, stream)
         return w
 
 
@@ -263,12 +277,13 @@ def route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", renormalis
     """Top-k routing of router logits [T][E] (f32, f16 or bf16, on the GPU)."""
     T, E = logits.shape
     i32 = {"dtype": torch.int32, "device": logits.device}
-    r = Routing(torch.empty((T, top_k), **i32), torch.empty((T, top_k), dtype=torch.float32, device=logits.device),
-                torch.empty(E + 1, **i32), torch.empty(T * top_k, **i32))
-    n = B.topk_route_workspace_bytes(T, E, top_k)
-    ws = torch.empty(n, dtype=torch.uint8, device=logits.device) if n else None
-    B.topk_route(logits, r.topk_ids, r.gate_w, r.offsets, r.order, scoring=scoring, renormalise=renormalise, scale=scale,
-                 workspace=ws, status=status, stream=stream)
+    with _on(stream):
+        r = Routing(torch.empty((T, top_k), **i32), torch.empty((T, top_k), dtype=torch.float32, device=logits.device),
+                    torch.empty(E + 1, **i32), torch.empty(T * top_k, **i32))
+        n = B.topk_route_workspace_bytes(T, E, top_k)
+        ws = torch.empty(n, dtype=torch.uint8, device=logits.device) if n else None
+        B.topk_route(logits, r.topk_ids, r.gate_w, r.offsets, r.order, scoring=scoring, renormalise=renormalise,
+                     scale=scale, workspace=ws, status=status, stream=stream)
     return r
 
 
@@ -288,11 +303,12 @@ class DenseMoEFFN:
                 status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x [T][d_model] in the matrices' type -> out [T][d_model] f32."""
         T = x.shape[0]
-        if out is None:
-            out = torch.empty((T, self.dims.d_model), dtype=torch.float32, device=x.device)
-        ws = torch.empty(B.dense_ffn_workspace_bytes(self.dims, T), dtype=torch.uint8, device=x.device)
-        B.dense_ffn_forward(self.dims, self.w_gate, self.w_up, self.w_down, x, routing.topk_ids, routing.gate_w,
-                            routing.offsets, routing.order, out, ws, status, stream)
+        with _on(stream):
+            if out is None:
+                out = torch.empty((T, self.dims.d_model), dtype=torch.float32, device=x.device)
+            ws = torch.empty(B.dense_ffn_workspace_bytes(self.dims, T), dtype=torch.uint8, device=x.device)
+            B.dense_ffn_forward(self.dims, self.w_gate, self.w_up, self.w_down, x, routing.topk_ids, routing.gate_w,
+                                routing.offsets, routing.order, out, ws, status, stream)
         return out
 
 
@@ -303,7 +319,7 @@ class MoEBlock:
         x  = rmsnorm(h) w_norm,  logits = w_router x,  y = FFN(x, top-k routing of the logits)
 
     y is added to h by the next block's forward (or by finish), fused with that block's
-    norm.  w_norm, w_post [d_model] f32, w_router [E][d_model] fp16; ffn a SpectralMoEFFN or
+    norm.  gate belongs to that y, None without one.  w_norm, w_post [d_model] f32, w_router [E][d_model] fp16; ffn a SpectralMoEFFN or
     an fp16 DenseMoEFFN; gate f32 [T or 1][d_model or 1]."""
 
     def __init__(self, ffn: "SpectralMoEFFN | DenseMoEFFN", w_norm: torch.Tensor, w_router: torch.Tensor,
@@ -311,6 +327,7 @@ class MoEBlock:
                  renormalise: bool = True, scale: float = 1.0):
         d = ffn.dims
         assert w_router.dtype == torch.float16 and tuple(w_router.shape) == (d.n_experts, d.d_model)
+        assert not isinstance(ffn, DenseMoEFFN) or ffn.w_gate.dtype == torch.float16
         self.ffn, self.w_norm, self.w_router, self.w_post = ffn, w_norm, w_router.contiguous(), w_post
         self.alpha, self.eps, self.scoring, self.renormalise, self.scale = alpha, eps, scoring, renormalise, scale
 
@@ -320,15 +337,16 @@ class MoEBlock:
         before, added to h in place first.  Returns this block's output, f32."""
         T, d = h.shape
         E = self.ffn.dims.n_experts
-        x = torch.empty((T, d), dtype=torch.float16, device=h.device)
-        B.norm_residual(h, y, self.w_norm, x, w_post=None if y is None else self.w_post, gate=gate, alpha=self.alpha,
-                        eps=self.eps, stream=stream)
-        logits = torch.empty((T, E), dtype=torch.float32, device=h.device)
-        B.shared_proj(self.w_router, x, logits, T, d, E, stream)
-        r = route(logits, self.ffn.dims.top_k, self.scoring, self.renormalise, self.scale, status, stream)
-        if isinstance(self.ffn, DenseMoEFFN):
-            return self.ffn.forward(x, r, status=status, stream=stream)
-        return self.ffn.forward(x, r.topk_ids, r.gate_w, status=status, stream=stream)
+        with _on(stream):
+            x = torch.empty((T, d), dtype=torch.float16, device=h.device)
+            B.norm_residual(h, y, self.w_norm, x, w_post=None if y is None else self.w_post, gate=gate, alpha=self.alpha,
+                            eps=self.eps, stream=stream)
+            logits = torch.empty((T, E), dtype=torch.float32, device=h.device)
+            B.shared_proj(self.w_router, x, logits, T, d, E, stream)
+            r = route(logits, self.ffn.dims.top_k, self.scoring, self.renormalise, self.scale, status, stream)
+            if isinstance(self.ffn, DenseMoEFFN):
+                return self.ffn.forward(x, r, status=status, stream=stream)
+            return self.ffn.forward(x, r.topk_ids, r.gate_w, status=status, stream=stream)
 
     def finish(self, h: torch.Tensor, y: torch.Tensor, gate: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Adds the last block's output to h in place."""

@@ -51,6 +51,33 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]), pack2<F16>(v[4], v[5]), pack2<F16>(v[6], v[7]));
 }
 
+__device__ __forceinline__ void unpack4(uint2 w, int type, float (&v)[4]) {
+    const float2 a = type == BITSMOE_F16 ? unpack2<true>(w.x) : unpack2<false>(w.x);
+    const float2 b = type == BITSMOE_F16 ? unpack2<true>(w.y) : unpack2<false>(w.y);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+
+// 4 elements, F32 or 16-bit of `type` (16 and 8 bytes, aligned).
+template <bool F32>
+__device__ __forceinline__ void load4(const void* p, int type, int64_t i, float (&v)[4]) {
+    if constexpr (F32) {
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    } else {
+        unpack4(*reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i), type, v);
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void store4(void* p, int type, int64_t i, const float (&v)[4]) {
+    if constexpr (F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        const uint2 w = type == BITSMOE_F16 ? make_uint2(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]))
+                                            : make_uint2(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]));
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = w;
+    }
+}
+
 // V elements (8: 16-byte aligned; 1: any) from element i of p.
 template <int V>
 __device__ __forceinline__ void load_elems(const void* p, int type, int64_t i, float (&v)[V]) {

@@ -9,25 +9,31 @@
 // pre-norm block, with the optional second norm.  x is formed from the fp32 h', not
 // from the stored one: one rounding fewer where h is held in 16 bits.
 //
-// One pass over memory: a row stays in registers between its loads and its stores,
-// so the step is bound by HBM (h and y read once, h' and x written once).  A row
-// belongs to a CTA (to one warp when that holds it in a chunk per lane: no CTA
-// barrier); the two sums are reduced in a fixed order, so results do not depend on
-// timing.  Rows too wide for registers are read once more per sum.
+// One pass over memory: a row stays in registers between its loads and its stores, so
+// the step is bound by HBM (h and y read once, h' and x written once).  A row belongs to
+// a CTA (up to 512 columns to a warp: no CTA barrier); the two sums are reduced in a
+// fixed order, so results do not depend on timing.  Rows too wide for registers are read
+// once more per sum.
 //
-// 8,192 x 4,096, bf16 h and x, fp32 y, both norms and a gate per channel: 70 us, 4.8 TB/s
-// (the floor is 52).  The rest is each row's chain -- loads, two sums over the CTA, three
-// vectors from L1 -- at 94% of the SM's threads.  Slower were: two rows a CTA (83 us), 256
-// threads a row (72), loads through a ring in shared memory by persistent CTAs (73 to 124,
-// by its depth), the channel vectors held in registers (86 and more): all hold fewer rows
-// or leave L1 too small for the vectors.
+// What decides the time is how many rows an SM has under way, and how long each takes
+// from its loads to its stores.  So: every load of a phase in straight-line code, with the
+// conversions behind them (under a branch per chunk 8,192 rows of 4,096 took 66 us
+// instead of 61.5, 4,096 rows of 8,192 107 instead of 53); h kept in 16 bits until it is
+// needed, which leaves registers for a fifth row; element widths fixed when the kernel is
+// built.  8,192 x 4,096, bf16 h and x, fp32 y, both norms and a gate per channel: 57.5 us,
+// 5.8 TB/s, 90% of a plain copy's rate.  Slower were two rows a CTA (83 us), loads through
+// a ring in shared memory by persistent CTAs (73 to 124, by its depth) and the channel
+// vectors held in registers (86 and more): they hold fewer rows, or leave the L1 cache
+// too small for the vectors.
 #include <algorithm>
 
 #include "elem.cuh"
 
 namespace bitsmoe {
 
-constexpr int kNormThreads = 512;  // threads per row, at most, while it stays in registers
+// Threads per row, at most, while it stays in registers, and the CTAs that an SM is to hold then.
+constexpr int norm_threads(int v, int nc) { return v == 4 && nc > 2 ? 256 : 512; }
+constexpr int norm_ctas(int v, int nc, bool h32) { return v != 4 || nc > 8 ? 1 : nc <= 2 ? 4 : nc == 4 ? 5 : h32 ? 2 : 3; }
 
 struct NormParams {
     const void* h;
@@ -55,9 +61,58 @@ __device__ __forceinline__ float row_sum(float v, float* s_part) {
     return warp_sum(v);
 }
 
-// NC chunks of V elements per thread; NC = 0: the row is read again for every sum.
-template <int V, int NC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? kNormThreads : 1024) k_norm_residual(const NormParams P) {
+// Loads and stores of V elements: 4, of a type whose width the kernel is built for, or 1 of any type.
+template <int V, bool F32>
+__device__ __forceinline__ void norm_load(const void* p, int type, int64_t i, float (&v)[V]) {
+    if constexpr (V == 4)
+        load4<F32>(p, type, i, v);
+    else
+        load_elems<V>(p, type, i, v);
+}
+template <int V, bool F32>
+__device__ __forceinline__ void norm_store(void* p, int type, int64_t i, const float (&v)[V]) {
+    if constexpr (V == 4)
+        store4<F32>(p, type, i, v);
+    else
+        store_elems<V>(p, type, i, v);
+}
+
+// V elements as they are in memory: h waits so for the sum over y.
+template <int V, bool F32>
+struct NormRaw {
+    float v[V];
+    __device__ __forceinline__ void load(const void* p, int type, int64_t i) { norm_load<V, F32>(p, type, i, v); }
+    __device__ __forceinline__ void get(int, float (&o)[V]) const {
+#pragma unroll
+        for (int j = 0; j < V; j++) o[j] = v[j];
+    }
+};
+template <>
+struct NormRaw<4, false> {
+    uint2 w;
+    __device__ __forceinline__ void load(const void* p, int, int64_t i) {
+        w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    }
+    __device__ __forceinline__ void get(int type, float (&o)[4]) const { unpack4(w, type, o); }
+};
+
+// v[j] times the channel vector w's chunk at at[j].
+template <int V, int NC>
+__device__ __forceinline__ void norm_scale(float (&v)[NC][V], const float* w, const int64_t (&at)[NC]) {
+    float f[NC][V];
+#pragma unroll
+    for (int j = 0; j < NC; j++) norm_load<V, true>(w, BITSMOE_F32, at[j], f[j]);
+#pragma unroll
+    for (int j = 0; j < NC; j++)
+#pragma unroll
+        for (int i = 0; i < V; i++) v[j][i] *= f[j][i];
+}
+
+// NC chunks of V elements per thread; NC = 0: the row is read again for every sum.  H32, Y32, X32 (V = 4): h, y and x
+// are fp32.
+template <int V, int NC, bool WARP, bool H32, bool Y32, bool X32>
+__global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? norm_threads(V, NC) : 1024, WARP || NC == 0 ? 1 : norm_ctas(V, NC, H32))
+    k_norm_residual(const NormParams P) {
     __shared__ float s_part[2][32];
     const int lane_in_row = WARP ? (int)threadIdx.x & 31 : (int)threadIdx.x;
     const int nthr = WARP ? 32 : (int)blockDim.x;
@@ -70,78 +125,67 @@ __global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? kNormThreads : 1024) k_n
     const int64_t h0 = t * P.h_ld, y0 = t * P.y_ld, ho0 = t * P.ho_ld, x0 = t * P.x_ld, g0 = t * P.gate_t;
 
     if constexpr (NC > 0) {
-        float hv[NC][V], yv[NC][V];
+        // Every load of a phase stands in straight-line code, conversions after them, so that they are in flight
+        // together: threads past the row's end read its last chunk and count nothing.
+        int64_t at[NC];
+        bool in[NC];
 #pragma unroll
         for (int j = 0; j < NC; j++) {
             const int c = lane_in_row + j * nthr;
-            if (c < nch) {
-                load_elems<V>(P.h, P.h_type, h0 + (int64_t)c * V, hv[j]);
-                if (P.y) load_elems<V>(P.y, P.y_type, y0 + (int64_t)c * V, yv[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; i++) hv[j][i] = yv[j][i] = 0.0f;
-            }
+            in[j] = c < nch;
+            at[j] = (int64_t)min(c, nch - 1) * V;
         }
+        NormRaw<V, H32> h[NC];
+        NormRaw<V, Y32> y[NC];
+        float hv[NC][V];  // y, then h'
+#pragma unroll
+        for (int j = 0; j < NC; j++) h[j].load(P.h, P.h_type, h0 + at[j]);
         if (P.y) {
+#pragma unroll
+            for (int j = 0; j < NC; j++) y[j].load(P.y, P.y_type, y0 + at[j]);
+#pragma unroll
+            for (int j = 0; j < NC; j++) y[j].get(P.y_type, hv[j]);
             float r = P.alpha;
+            if (P.gate && P.gate_i == 0) r *= P.gate[g0];
             if (P.w_post) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NC; j++)
 #pragma unroll
-                    for (int i = 0; i < V; i++) ss = fmaf(yv[j][i], yv[j][i], ss);
-                const float ry = rsqrtf(fmaf(row_sum<WARP>(ss, s_part[0]), inv_d, P.eps));
-#pragma unroll
-                for (int j = 0; j < NC; j++) {
-                    const int c = lane_in_row + j * nthr;
-                    if (c < nch) {
-                        float w[V];
-                        load_elems<V>(P.w_post, BITSMOE_F32, (int64_t)c * V, w);
-#pragma unroll
-                        for (int i = 0; i < V; i++) yv[j][i] *= ry * w[i];
-                    }
-                }
+                    for (int i = 0; i < V; i++) ss = in[j] ? fmaf(hv[j][i], hv[j][i], ss) : ss;
+                r *= rsqrtf(fmaf(row_sum<WARP>(ss, s_part[0]), inv_d, P.eps));
+                norm_scale<V, NC>(hv, P.w_post, at);
             }
-            if (P.gate && P.gate_i == 0) r *= P.gate[g0];
+            if (P.gate && P.gate_i) norm_scale<V, NC>(hv, P.gate + g0, at);
 #pragma unroll
             for (int j = 0; j < NC; j++) {
-                const int c = lane_in_row + j * nthr;
-                if (c < nch) {
-                    if (P.gate && P.gate_i) {
-                        float g[V];
-                        load_elems<V>(P.gate, BITSMOE_F32, g0 + (int64_t)c * V, g);
+                float v[V];
+                h[j].get(P.h_type, v);
 #pragma unroll
-                        for (int i = 0; i < V; i++) yv[j][i] *= g[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < V; i++) hv[j][i] = fmaf(r, yv[j][i], hv[j][i]);
-                }
+                for (int i = 0; i < V; i++) hv[j][i] = fmaf(r, hv[j][i], v[i]);
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NC; j++) h[j].get(P.h_type, hv[j]);
         }
         if (P.h_out) {
 #pragma unroll
-            for (int j = 0; j < NC; j++) {
-                const int c = lane_in_row + j * nthr;
-                if (c < nch) store_elems<V>(P.h_out, P.h_type, ho0 + (int64_t)c * V, hv[j]);
-            }
+            for (int j = 0; j < NC; j++)
+                if (in[j]) norm_store<V, H32>(P.h_out, P.h_type, ho0 + at[j], hv[j]);
         }
         if (!P.x) return;
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < NC; j++)
 #pragma unroll
-            for (int i = 0; i < V; i++) ss = fmaf(hv[j][i], hv[j][i], ss);
+            for (int i = 0; i < V; i++) ss = in[j] ? fmaf(hv[j][i], hv[j][i], ss) : ss;
         const float rx = rsqrtf(fmaf(row_sum<WARP>(ss, s_part[1]), inv_d, P.eps));
+        norm_scale<V, NC>(hv, P.w_pre, at);
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = lane_in_row + j * nthr;
-            if (c < nch) {
-                float w[V];
-                load_elems<V>(P.w_pre, BITSMOE_F32, (int64_t)c * V, w);
 #pragma unroll
-                for (int i = 0; i < V; i++) hv[j][i] *= rx * w[i];
-                store_elems<V>(P.x, P.x_type, x0 + (int64_t)c * V, hv[j]);
-            }
+            for (int i = 0; i < V; i++) hv[j][i] *= rx;
+            if (in[j]) norm_store<V, X32>(P.x, P.x_type, x0 + at[j], hv[j]);
         }
     } else {
         float ry = 1.0f;
@@ -149,7 +193,7 @@ __global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? kNormThreads : 1024) k_n
             float ss = 0.0f;
             for (int c = lane_in_row; c < nch; c += nthr) {
                 float v[V];
-                load_elems<V>(P.y, P.y_type, y0 + (int64_t)c * V, v);
+                norm_load<V, Y32>(P.y, P.y_type, y0 + (int64_t)c * V, v);
 #pragma unroll
                 for (int i = 0; i < V; i++) ss = fmaf(v[i], v[i], ss);
             }
@@ -158,17 +202,17 @@ __global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? kNormThreads : 1024) k_n
         float r = P.alpha;
         if (P.gate && P.gate_i == 0) r *= P.gate[g0];
         auto chunk = [&](int c, float(&hv)[V]) {
-            load_elems<V>(P.h, P.h_type, h0 + (int64_t)c * V, hv);
+            norm_load<V, H32>(P.h, P.h_type, h0 + (int64_t)c * V, hv);
             if (!P.y) return;
             float v[V], w[V];
-            load_elems<V>(P.y, P.y_type, y0 + (int64_t)c * V, v);
+            norm_load<V, Y32>(P.y, P.y_type, y0 + (int64_t)c * V, v);
             if (P.w_post) {
-                load_elems<V>(P.w_post, BITSMOE_F32, (int64_t)c * V, w);
+                norm_load<V, true>(P.w_post, BITSMOE_F32, (int64_t)c * V, w);
 #pragma unroll
                 for (int i = 0; i < V; i++) v[i] *= ry * w[i];
             }
             if (P.gate && P.gate_i) {
-                load_elems<V>(P.gate, BITSMOE_F32, g0 + (int64_t)c * V, w);
+                norm_load<V, true>(P.gate, BITSMOE_F32, g0 + (int64_t)c * V, w);
 #pragma unroll
                 for (int i = 0; i < V; i++) v[i] *= w[i];
             }
@@ -190,13 +234,13 @@ __global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? kNormThreads : 1024) k_n
         for (int c = lane_in_row; c < nch; c += nthr) {
             float v[V];
             chunk(c, v);
-            if (P.h_out) store_elems<V>(P.h_out, P.h_type, ho0 + (int64_t)c * V, v);
+            if (P.h_out) norm_store<V, H32>(P.h_out, P.h_type, ho0 + (int64_t)c * V, v);
             if (P.x) {
                 float w[V];
-                load_elems<V>(P.w_pre, BITSMOE_F32, (int64_t)c * V, w);
+                norm_load<V, true>(P.w_pre, BITSMOE_F32, (int64_t)c * V, w);
 #pragma unroll
                 for (int i = 0; i < V; i++) v[i] *= rx * w[i];
-                store_elems<V>(P.x, P.x_type, x0 + (int64_t)c * V, v);
+                norm_store<V, X32>(P.x, P.x_type, x0 + (int64_t)c * V, v);
             }
         }
     }
@@ -204,22 +248,47 @@ __global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? kNormThreads : 1024) k_n
 
 constexpr int kNormWarpRows = 8;  // rows (warps) per CTA when a row belongs to a warp
 
-template <int V>
+template <int V, bool H32, bool Y32, bool X32>
 static int launch_norm(const NormParams& P, cudaStream_t s) {
     const int nch = P.d / V;
-    // A row in one warp while it is one chunk a lane; longer ones are a chain of too many instructions (8,192 rows of
-    // 256: 4.1 us against 8.9 with a CTA each; of 512: 8.7 and 9.0, but 16 rows 2.6 and 1.9; of 1024: 27 and 14).
-    if (nch <= 32 && P.T > 1) {
-        const dim3 grid((unsigned)((P.T + kNormWarpRows - 1) / kNormWarpRows)), block(32 * kNormWarpRows);
-        return launch_pdl(k_norm_residual<V, 1, true>, grid, block, 0, s, P);
+    // A row in one warp up to 512 columns (8,192 rows, one warp each and a CTA each, us: 256 columns 4.1 and 8.9,
+    // 512 columns 8.9 and 9.7; of 768 and more a CTA is as fast).
+    if (nch <= 32 * (V == 4 ? 4 : 1)) {
+        const dim3 rows((unsigned)((P.T + kNormWarpRows - 1) / kNormWarpRows)), block(32 * kNormWarpRows);
+        if constexpr (V == 1) return launch_pdl(k_norm_residual<V, 1, true, H32, Y32, X32>, rows, block, 0, s, P);
+        if constexpr (V == 4) {
+            if (nch <= 64) return launch_pdl(k_norm_residual<V, 2, true, H32, Y32, X32>, rows, block, 0, s, P);
+            return launch_pdl(k_norm_residual<V, 4, true, H32, Y32, X32>, rows, block, 0, s, P);
+        }
     }
     const dim3 grid((unsigned)P.T);
     auto threads = [&](int nc) { return (unsigned)std::max<int64_t>(32, roundup((nch + nc - 1) / nc, 32)); };
-    constexpr int N0 = V == 8 ? 1 : 4;  // chunks per thread: N0, 2 N0 or 4 N0
-    if (nch <= N0 * kNormThreads) return launch_pdl(k_norm_residual<V, N0, false>, grid, threads(N0), 0, s, P);
-    if (nch <= 2 * N0 * kNormThreads) return launch_pdl(k_norm_residual<V, 2 * N0, false>, grid, threads(2 * N0), 0, s, P);
-    if (nch <= 4 * N0 * kNormThreads) return launch_pdl(k_norm_residual<V, 4 * N0, false>, grid, threads(4 * N0), 0, s, P);
-    return launch_pdl(k_norm_residual<V, 0, false>, grid, 1024, 0, s, P);
+    if constexpr (V == 4) {
+        // 512 threads of 8 elements, or 256 of 16 with an SM's 5 rows in place of 4: with h in 16 bits the second is
+        // faster for many rows (8,192 x 4,096: 57.5 against 61.5 us; 1,024 rows 10.1 and 10.1; 1 row 2.8 and 2.6).
+        if constexpr (!H32)
+            if (P.T >= 2048 && P.d >= 1536 && nch <= 4 * norm_threads(V, 4))
+                return launch_pdl(k_norm_residual<V, 4, false, H32, Y32, X32>, grid, threads(4), 0, s, P);
+        if (nch <= 2 * norm_threads(V, 2))
+            return launch_pdl(k_norm_residual<V, 2, false, H32, Y32, X32>, grid, threads(2), 0, s, P);
+    } else if (nch <= 4 * norm_threads(V, 4)) {
+        return launch_pdl(k_norm_residual<V, 4, false, H32, Y32, X32>, grid, threads(4), 0, s, P);
+    }
+    if (nch <= 8 * norm_threads(V, 8))
+        return launch_pdl(k_norm_residual<V, 8, false, H32, Y32, X32>, grid, threads(8), 0, s, P);
+    if (nch <= 16 * norm_threads(V, 16))
+        return launch_pdl(k_norm_residual<V, 16, false, H32, Y32, X32>, grid, threads(16), 0, s, P);
+    return launch_pdl(k_norm_residual<V, 0, false, H32, Y32, X32>, grid, 1024, 0, s, P);
+}
+
+static int launch_norm4(const NormParams& P, cudaStream_t s) {
+    const bool h32 = P.h_type == BITSMOE_F32, y32 = P.y_type == BITSMOE_F32, x32 = P.x_type == BITSMOE_F32;
+    if (h32) {
+        if (y32) return x32 ? launch_norm<4, true, true, true>(P, s) : launch_norm<4, true, true, false>(P, s);
+        return x32 ? launch_norm<4, true, false, true>(P, s) : launch_norm<4, true, false, false>(P, s);
+    }
+    if (y32) return x32 ? launch_norm<4, false, true, true>(P, s) : launch_norm<4, false, true, false>(P, s);
+    return x32 ? launch_norm<4, false, false, true>(P, s) : launch_norm<4, false, false, false>(P, s);
 }
 
 }  // namespace bitsmoe
@@ -268,9 +337,9 @@ BITSMOE_API int bitsmoe_norm_residual(const bitsmoe_norm_args* args, void* strea
     auto vec = [](const void* p, int type, int64_t ld) {
         return !p || ((uintptr_t)p % 16 == 0 && (ld * elem_bytes(type)) % 16 == 0);
     };
-    const bool v8 = a.d % 8 == 0 && vec(a.h, a.h_type, a.h_stride) && vec(a.y, a.y_type, a.y_stride) &&
+    const bool vec4 = a.d % 8 == 0 && vec(a.h, a.h_type, a.h_stride) && vec(a.y, a.y_type, a.y_stride) &&
                     vec(a.h_out, a.h_type, a.h_out_stride) && vec(a.x, a.x_type, a.x_stride) &&
                     vec(a.w_post, BITSMOE_F32, 0) && vec(a.w_pre, BITSMOE_F32, 0) &&
                     (!a.gate_per_channel || vec(a.gate, BITSMOE_F32, a.gate_stride));
-    return v8 ? launch_norm<8>(P, (cudaStream_t)stream) : launch_norm<1>(P, (cudaStream_t)stream);
+    return vec4 ? launch_norm4(P, (cudaStream_t)stream) : launch_norm<1, false, false, false>(P, (cudaStream_t)stream);
 }

@@ -147,6 +147,23 @@ def test_norm_residual_special_rows(d):
     assert bool(torch.isfinite(x[0]).all()) and bool(torch.isfinite(x[3]).all())
 
 
+@pytest.mark.parametrize("T", [1, 2050])
+@pytest.mark.parametrize("d", [1, 8, 64, 300, 520, 1000, 1001, 2000, 4104, 6000, 9000])
+def test_norm_residual_infinity_in_the_last_place(d, T):
+    """mean(h^2) is infinite, 1 / sqrt of it 0: the row's other elements become 0, the infinite one NaN (infinity
+    times 0), and no other row notices; the same through the norm on y."""
+    g = _gen(5)
+    h, w = _randn(g, T, d).half(), torch.ones(d, device="cuda")
+    h[-1, -1] = float("inf")
+    y = torch.zeros(T, d, device="cuda")
+    x = torch.empty(T, d, device="cuda")
+    B.norm_residual(h.clone(), y, w, x, w_post=w)
+    assert bool((x[-1, :-1] == 0).all()) and bool(torch.isnan(x[-1, -1])) and bool(torch.isfinite(x[:-1]).all())
+    h_out = torch.empty_like(h)
+    B.norm_residual(y.half(), h, w, x, w_post=w, h_out=h_out)
+    assert bool((h_out[-1, :-1] == 0).all()) and bool(torch.isnan(h_out[-1, -1])) and bool(torch.isfinite(x[:-1]).all())
+
+
 # ---------------------------------------------------------------------------
 # routing
 # ---------------------------------------------------------------------------

@@ -367,6 +367,8 @@ __device__ __forceinline__ float q4_join(const float (&acc)[2], int lane) {
 // Before the programmatic-launch wait the CTA asks L2 for its rows of the experts that
 // the ids name at that moment (a prefetch alone: nothing read there is used, and the
 // loads after the wait go by the ids as they are then).
+// 8 experts, 2048 x 768, G = 64: 7.0 us, one chain from the ids over h's digits and 12 tiles
+// a warp to the joining of the warps; the 6.7 MB alone would take 1.
 constexpr int kQ4T1Warps = 16;
 constexpr size_t kQ4T1Smem = 200 * 1024;
 
@@ -701,6 +703,8 @@ __global__ void __launch_bounds__(THREADS) k_q4_prep(const Q4Params P) {
 // its own in shared memory, filled by bulk copies of up to 8 tiles, a stage ahead and
 // across the borders of units (without the products this reads at HBM's rate).  Results go
 // from registers to memory, a row of y per pair and range; no CTA barrier is met.
+// 64 tokens, 128 experts, 2048 x 768, top 8: about 33 us of the step's 45 (108 MB); 56% of
+// the issue slots are used, most by unpacking and scaling, the MMAs take 11 us.
 constexpr int kQ4Warps = 8;
 constexpr int kQ4Threads = 32 * kQ4Warps;
 constexpr int kQ4CT = 8;                                        // tiles per stage, at most

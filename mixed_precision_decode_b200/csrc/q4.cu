@@ -269,8 +269,9 @@ struct Q4Params {
 };
 constexpr int kQ4Rec = 12;   // ints of a piece's record: expert, pairs in it, 2 unused, 8 pair indexes
 constexpr int kQ4Slot0 = 4;
-// Cost of a unit of a piece with np pairs: unpacking the codes, and 2 pairs a block of columns.
-__host__ __device__ constexpr int q4_cost(int np) { return 3 + 2 * (np <= 2 ? 1 : np <= 4 ? 2 : 4); }
+// Cost of a unit of a piece with np pairs: unpacking the codes, and 1, 2 or 4 blocks of 2 pairs each.  (As 5 : 7 : 11
+// 128 tokens of 128 experts took 65.1 us instead of 64.5, 32 tokens of 8 experts 4096 x 14336 138 instead of 134.)
+__host__ __device__ constexpr int q4_cost(int np) { return np <= 2 ? 3 : np <= 4 ? 4 : 7; }
 
 // 16 weight bytes of a lane, read once.
 __device__ __forceinline__ uint4 q4_ld(const uint8_t* p) {
@@ -700,14 +701,16 @@ __global__ void __launch_bounds__(THREADS) k_q4_prep(const Q4Params P) {
 // piece, one range of columns and one block of 16 rows, in that order, and every CTA takes
 // a contiguous run of them of equal cost for its 8 warps: its units share a piece and a
 // range, whose B operands stay in L1.  A warp streams its units' tiles through a ring of
-// its own in shared memory, filled by bulk copies of up to 8 tiles, a stage ahead and
+// its own in shared memory, filled by bulk copies of up to 12 tiles, a stage ahead and
 // across the borders of units (without the products this reads at HBM's rate).  Results go
 // from registers to memory, a row of y per pair and range; no CTA barrier is met.
-// 64 tokens, 128 experts, 2048 x 768, top 8: about 33 us of the step's 45 (108 MB); 56% of
+// 64 tokens, 128 experts, 2048 x 768, top 8: about 32 us of the step's 42 (108 MB); 56% of
 // the issue slots are used, most by unpacking and scaling, the MMAs take 11 us.
 constexpr int kQ4Warps = 8;
 constexpr int kQ4Threads = 32 * kQ4Warps;
-constexpr int kQ4CT = 8;                                        // tiles per stage, at most
+// Tiles per stage, at most: two CTAs' rings of two stages fill an SM's shared memory.  (8: 43.2 instead of 42.2 us at 64
+// tokens of 128 experts, 2048 x 768, where 12 are a whole row block and one copy; 120 instead of 112 at 256 tokens.)
+constexpr int kQ4CT = 12;
 constexpr int kQ4StageBytes = kQ4CT * (kQ4TileBytes + 2 * 32);  // their codes, and up to 2 groups' scales each
 constexpr int kQ4Stages = 2;
 

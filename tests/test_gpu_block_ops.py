@@ -888,3 +888,44 @@ def test_moe_block_on_a_given_stream():
     side = torch.cuda.Stream()
     for stream in (side, side.cuda_stream):
         assert torch.equal(run(stream, True), want)
+
+
+def test_two_graphs_share_workspaces():
+    """Two captured graphs of different batches on the same workspaces, replayed in turn: no call leaves anything in a
+    workspace that the next one reads."""
+    E, K, d, d_ff = 20, 3, 384, 256
+    g = _gen(31)
+    blob, _ = _q4_blob(_randn(g, E, d, d_ff), 64)
+    wg, wu, wd = _randn(g, E, d_ff, d).half() * 0.1, _randn(g, E, d_ff, d).half() * 0.1, _randn(g, E, d, d_ff).half() * 0.1
+    dims = B.ffn_dims(d, d_ff, E, K)
+    Ts = (150, 37)
+    n = max(max(B.topk_route_workspace_bytes(T, E, K), B.ffn_down_q4_workspace_bytes(dims, 64, T),
+                B.dense_ffn_workspace_bytes(dims, T)) for T in Ts)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")  # one for all three operators
+    sets = []
+    for T in Ts:
+        i32 = {"dtype": torch.int32, "device": "cuda"}
+        s = {"logits": _randn(g, T, E), "yg": _randn(g, T, K, d_ff), "yu": _randn(g, T, K, d_ff), "x": _randn(g, T, d).half(),
+             "ids": torch.empty(T, K, **i32), "gw": torch.empty(T, K, device="cuda"), "off": torch.empty(E + 1, **i32),
+             "order": torch.empty(T * K, **i32), "q4": torch.empty(T, d, device="cuda"),
+             "dense": torch.empty(T, d, device="cuda")}
+
+        def run(s=s, T=T):
+            B.topk_route(s["logits"], s["ids"], s["gw"], s["off"], s["order"], workspace=ws)
+            B.ffn_down_q4(dims, blob, 64, s["yg"], s["yu"], s["ids"], s["gw"], T, s["q4"], ws, n)
+            B.dense_ffn_forward(dims, wg, wu, wd, s["x"], s["ids"], s["gw"], s["off"], s["order"], s["dense"], ws)
+
+        run()
+        torch.cuda.synchronize()
+        s["want"] = {k: s[k].clone() for k in ("ids", "gw", "off", "order", "q4", "dense")}
+        s["graph"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(s["graph"]):
+            run()
+        sets.append(s)
+    for k in (0, 1, 0, 0, 1):
+        for key in ("q4", "dense", "ids"):
+            sets[k][key].zero_()
+        sets[k]["graph"].replay()
+        torch.cuda.synchronize()
+        for key, want in sets[k]["want"].items():
+            assert torch.equal(sets[k][key], want), key

@@ -56,8 +56,8 @@ __device__ __forceinline__ bool row_pair(const GmmParams& P, int i, int64_t& src
 // few rows per expert
 // ---------------------------------------------------------------------------
 // Bound by the weights' bytes, with too few of them for the kernel below (one token, 8 of
-// 128 experts, 2048 -> 768 gated: 13.7 us, 3.7 TB/s).  A CTA owns
-// 16 rows of one expert's matrix (of both, when gated) and up to 8 of its input rows; its 8 warps take an eighth of K
+// 128 experts, 2048 -> 768 gated: 11.6 us, 4.3 TB/s).  A CTA owns 16 rows of one expert's
+// matrix (of both, when gated) and up to 8 of its input rows; its 4 warps take a quarter of K
 // each, so that every SM has enough loads in flight when only a few experts are
 // touched, and add their fp32 partial tiles in warp order.  The products are
 // mma.sync m16n8k16 on operands that go from global memory to registers: a lane
@@ -65,16 +65,20 @@ __device__ __forceinline__ bool row_pair(const GmmParams& P, int i, int64_t& src
 // of a 32-wide step take as k = 2c, 2c+1, 2c+8, 2c+9; the input rows are loaded with
 // the same order of k, so the sum over k is the same and no operand is rearranged.
 //
+// 4 warps, and registers for a warp's loads of 4 steps at once: 8 warps took 15.4 us
+// in that case, and 10.4 instead of 7.4 for the 768 -> 2048 products of one token.
+//
 // Which of the two kernels (us, this one / the next; K x N matrices of E experts, pairs of rows):
-//   gated 2048 x 768, E = 128:   8 pairs 13.7 / 16.9    32 pairs 35.2 / 39.2     64 pairs 60.3 / 54.1
-//   768 x 2048, E = 128:         8 pairs  8.8 /  9.8    32 pairs 25.7 / 22.9     64 pairs 45.6 / 35.1
-//   gated 2048 x 768, E = 8:    16 pairs 11.3 / 16.6    64 pairs 15.0 / 17.2     96 pairs 17.7 / 17.2
-//   768 x 2048, E = 8:          16 pairs  7.5 /  9.6    64 pairs 10.1 /  9.8     96 pairs 11.9 / 10.0
-//   gated 4096 x 14336, E = 8:   2 pairs 75.4 / 78.0     8 pairs  195 /  203     64 pairs  412 /  291
-// The next one's CTA pairs take blocks of 256 weight rows: it is slower while these are fewer than the SMs, and
-// this one reads the weights again for every 8 rows of an expert.
-constexpr int kTcTiles = 148, kTcRows = 8;
-constexpr int kMvWarps = 8;
+//   gated 2048 x 768, E = 128:   32 pairs 33.4 / 38.1    128 pairs 81.9 / 81.3   256 pairs  106 /  105
+//   768 x 2048, E = 128:         64 pairs 33.0 / 33.6    128 pairs 56.3 / 48.5
+//   1024 x 4096, E = 64:         32 pairs 36.0 / 37.3     64 pairs 59.3 / 54.0
+//   gated 2048 x 768, E = 8:     32 pairs 11.3 / 16.2     64 pairs 12.4 / 16.4   192 pairs 22.0 / 16.8
+//   768 x 2048, E = 8:           32 pairs  6.1 /  9.1     64 pairs  9.1 /  9.1    96 pairs 10.2 /  9.1
+//   gated 4096 x 14336, E = 8:    4 pairs  120 /  129     32 pairs  305 /  295    64 pairs  415 /  296
+// The next one's CTA pairs take blocks of 256 weight rows: it is slower while these are few for the SMs, and this one
+// reads the weights again for every 8 rows of an expert.
+constexpr int kTcTiles = 384, kTcRows = 8;
+constexpr int kMvWarps = 4;
 constexpr int kMvThreads = 32 * kMvWarps;
 constexpr int kMvRows = 16, kMvTok = 8;  // weight rows and input rows of a CTA
 constexpr int kMvUnroll = 4;  // 32-wide k steps in flight per warp
@@ -134,7 +138,7 @@ __device__ __forceinline__ bool find_slot(const GmmParams& P, int slot, int tok,
 }
 
 template <bool BF16, bool GATED>
-__global__ void __launch_bounds__(kMvThreads) k_gmm_mv(const GmmParams P) {
+__global__ void __launch_bounds__(kMvThreads, GATED ? 4 : 8) k_gmm_mv(const GmmParams P) {
     constexpr int NW = GATED ? 2 : 1;
     __shared__ float s_part[kMvWarps][NW][kMvRows][kMvTok + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -232,7 +236,7 @@ static int launch_gmm_mv(const GmmParams& P, cudaStream_t s) {
 // The number of tiles is known on the device alone: every CTA derives it from offsets.
 //
 // Bound by the weights' bytes up to a few hundred rows per expert, then by the tensor
-// pipe.  128 experts, 2048 -> 768 gated, gathered: 64 pairs 54 us (308 MB, 5.7 TB/s), 16,384
+// pipe.  128 experts, 2048 -> 768 gated, gathered: 128 pairs 81 us (510 MB, 6.3 TB/s), 16,384
 // pairs 153 us (870 MB, 5.7 TB/s, the tensor pipe 40% busy); 768 -> 2048 with fp32 results,
 // 16,384 pairs 104 us; 8 experts, 4096 -> 14336, 2,050 pairs 232 us (1.04 PFLOP/s, the pipe
 // 69% busy) before the power limit lowers the clocks.  Tiles of one expert stand together:
@@ -795,7 +799,7 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* strea
     P.scatter = d.scatter != 0;
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t tiles = (int64_t)((P.N + 2 * kGtM - 1) / (2 * kGtM)) * std::min(P.P, P.E);  // were no two pairs of one expert
-    if (tiles >= kTcTiles || P.P > kTcRows * P.E) {
+    if ((tiles >= kTcTiles && P.P >= P.E) || P.P > kTcRows * P.E) {
         if (d.rows) return d.W_up ? launch_gmm_seg<true, true>(P, s) : launch_gmm_seg<false, true>(P, s);
         return d.W_up ? launch_gmm_seg<true, false>(P, s) : launch_gmm_seg<false, false>(P, s);
     }

@@ -75,9 +75,13 @@ __device__ __forceinline__ bool row_pair(const GmmParams& P, int i, int64_t& src
 //   gated 2048 x 768, E = 8:     32 pairs 11.3 / 16.2     64 pairs 12.4 / 16.4   192 pairs 22.0 / 16.8
 //   768 x 2048, E = 8:           32 pairs  6.1 /  9.1     64 pairs  9.1 /  9.1    96 pairs 10.2 /  9.1
 //   gated 4096 x 14336, E = 8:    4 pairs  120 /  129     32 pairs  305 /  295    64 pairs  415 /  296
-// The next one's CTA pairs take blocks of 256 weight rows: it is slower while these are few for the SMs, and this one
-// reads the weights again for every 8 rows of an expert.
-constexpr int kTcTiles = 384, kTcRows = 8;
+//   2048 x 256, E = 8:          256 pairs  9.6 / 15.7   1024 pairs 18.0 / 18.8
+//   4096 x 64, E = 2:            32 pairs  6.1 / 24.2    512 pairs  7.1 / 30.6
+//   gated 4096 x 256, E = 2:     32 pairs  7.8 / 24.0    512 pairs 27.3 / 27.1
+// The next one's CTA pairs take blocks of 256 weight rows over all of K: it is slower while these are few for the SMs,
+// and this one reads the weights again for every 8 rows of an expert.  So the next one takes over where its tiles are
+// many and the experts have a row each on average, or more than 8 rows; but not products with few results.
+constexpr int kTcTiles = 384, kTcRows = 8, kMvResults = 1 << 17;
 constexpr int kMvWarps = 4;
 constexpr int kMvThreads = 32 * kMvWarps;
 constexpr int kMvRows = 16, kMvTok = 8;  // weight rows and input rows of a CTA
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(kMvThreads, GATED ? 4 : 8) k_gmm_mv(const GmmP
 
 template <bool BF16, bool GATED>
 static int launch_gmm_mv(const GmmParams& P, cudaStream_t s) {
-    const int slots = std::min(P.P, P.E) + P.P / kMvTok;  // at least the pieces of every group; P.P <= kTcRows P.E here
+    const int slots = std::min(P.P, P.E) + P.P / kMvTok;  // at least the pieces of every group; at most 2^15 here
     return launch_pdl(k_gmm_mv<BF16, GATED>, dim3((P.N + kMvRows - 1) / kMvRows, slots), dim3(kMvThreads), 0, s, P);
 }
 
@@ -799,7 +803,8 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* strea
     P.scatter = d.scatter != 0;
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t tiles = (int64_t)((P.N + 2 * kGtM - 1) / (2 * kGtM)) * std::min(P.P, P.E);  // were no two pairs of one expert
-    if ((tiles >= kTcTiles && P.P >= P.E) || P.P > kTcRows * P.E) {
+    const bool few = (int64_t)P.N * P.P * (P.w_up ? 2 : 1) <= kMvResults;
+    if (!few && ((tiles >= kTcTiles && P.P >= P.E) || P.P > kTcRows * P.E)) {
         if (d.rows) return d.W_up ? launch_gmm_seg<true, true>(P, s) : launch_gmm_seg<false, true>(P, s);
         return d.W_up ? launch_gmm_seg<true, false>(P, s) : launch_gmm_seg<false, false>(P, s);
     }

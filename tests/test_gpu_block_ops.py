@@ -521,6 +521,7 @@ GMM_SIZES = [
     ([1], 16, 8), ([1, 0, 2], 5, 24), ([0, 7, 1, 0, 9], 130, 64), ([33, 1, 64, 0], 257, 136), ([3] * 40, 96, 256),
     ([8, 8, 8, 8, 8, 8, 8, 8], 768, 2048), ([300], 64, 72), ([129, 511, 2], 300, 520), ([257, 1, 0, 96, 40], 512, 1024),
     ([0, 0, 0, 5], 384, 4096), ([1000, 24], 128, 768), ([17] * 130, 264, 320),
+    ([700], 257, 72), ([400, 3, 0, 200], 333, 8), ([2] * 200, 700, 40), ([1] * 129 + [0], 1030, 136),
 ]
 
 
@@ -536,16 +537,18 @@ def test_grouped_matmul_strided_and_spare_rows():
     """Rows of A further apart than K; places behind the last group and rows without a pair stay as they were."""
     for form in ("sorted", "gated_gather", "scatter"):
         _check_gmm([5, 0, 40, 300], 136, 72, F16, F16, form, lda=16, spare=37)
+        _check_gmm([5, 0, 40, 700], 264, 72, F16, F16, form, lda=16, spare=37)
+        _check_gmm([5, 0, 40, 700], 268, 72, BF16, F32, form, lda=8, spare=37)
         _check_gmm([2, 1], 40, 64, BF16, F32, form, lda=8, spare=3)
         _check_gmm([0, 0], 40, 64, BF16, F32, form, spare=3)
 
 
-@pytest.mark.parametrize("scale", [1, 40])
-def test_grouped_matmul_bad_indexes(scale):
+@pytest.mark.parametrize("scale, N", [(1, 48), (40, 48), (40, 480)])
+def test_grouped_matmul_bad_indexes(scale, N):
     """Offsets outside the rows are clamped, row indexes outside A or out are left out; both are reported and
-    every other row is right.  scale 40: the path for many rows."""
+    every other row is right.  40 x 480: the tensor-core kernel."""
     g = _gen(9)
-    n, N, K = 12 * scale, 48, 64
+    n, K = 12 * scale, 64
     a, W = _randn(g, n, K).half(), _randn(g, 3, N, K).half()
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
 
@@ -593,7 +596,7 @@ def test_grouped_matmul_sums_of_one_sign(K, form, gather):
     (The first form of this bound counted the cut of the sum alone, 48 and 24 units, and failed with 34 on average.)
     Gated: every gate is 40, whose SiLU is 40 in fp32."""
     g = _gen(K)
-    E, N, per = 3, 96, 6 if form == "few" else 70
+    E, N, per = 3, 96 if form == "few" else 640, 6 if form == "few" else 70
     P = E * per
     a = torch.rand((P, K), generator=g, device="cuda").half() + 0.5
     W = (torch.rand((E, N, K), generator=g, device="cuda") + 0.5).half()
@@ -617,12 +620,12 @@ def test_grouped_matmul_sums_of_one_sign(K, form, gather):
 def test_grouped_matmul_non_finite_rows_stay_apart():
     """NaN and infinities in one row of A, or in another expert's rows and matrix, reach no other row."""
     g = _gen(11)
-    for sizes in ([3, 4, 2], [150, 90, 200]):
+    for sizes, N in (([3, 4, 2], 40), ([150, 90, 200], 40), ([150, 90, 200], 400)):
         P = sum(sizes)
-        a, W = _randn(g, P, 72).half(), _randn(g, 3, 40, 72).half()
+        a, W = _randn(g, P, 72).half(), _randn(g, 3, N, 72).half()
         a[1], a[sizes[0]] = float("nan"), float("inf")
         W[2] = float("nan")
-        out = torch.zeros(P, 40, device="cuda")
+        out = torch.zeros(P, N, device="cuda")
         B.grouped_matmul(a, W, _offsets(sizes), out)
         fin = torch.isfinite(out).all(1).cpu()
         want = torch.ones(P, dtype=torch.bool)
@@ -640,7 +643,7 @@ def _rel(got, ref):
     return float(((got - ref).abs().amax(-1) / ref.abs().amax(-1).clamp_min(1e-30)).max())
 
 
-@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("T", [1, 40, 400])
 def test_operators_on_another_stream_and_in_a_graph(T):
     """Each operator on a side stream and in a replayed graph whose inputs change between replays equals its
     plain call bit for bit (no operator's result depends on timing)."""

@@ -364,6 +364,26 @@ __device__ __forceinline__ void gt_add(uint32_t addr, bool more, float (&y)[NW][
     }
 }
 
+// Column `row` of ROWS rows of out from shared memory, [ROWS][32]; dst: the rows' places, -1 for none.
+template <typename T, int ROWS>
+__device__ __forceinline__ void gt_store_rows(const T* src, const int* dst, void* out, int n_out, int row) {
+    if (row >= n_out) return;
+    T* col = static_cast<T*>(out) + row;
+    const int lane = threadIdx.x & 31;
+    for (int j = 0; j < ROWS; j += 8) {
+        T v[8];
+        int d[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            v[k] = src[32 * (j + k) + lane];
+            d[k] = dst[j + k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            if (d[k] >= 0) col[(int64_t)d[k] * n_out] = v[k];
+    }
+}
+
 // One tile of the walk.
 struct GtTile {
     int e, n0;   // expert, first weight row of the pair's block
@@ -489,7 +509,6 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
             }
             __syncwarp();
             const int row = t.n0 + (int)rank * kGtM + 32 * sub, row0 = row + piece * (32 / cw);  // whole pieces inside N
-            const bool live = row + lane < P.N;
             uint8_t* out0 = static_cast<uint8_t*>(P.out) + (int64_t)row0 * (f32 ? 4 : 2);
             float y[SEG ? NB : 1][NW][32];
             for (int k = 0; k < Q.nst; k += Q.seg) {
@@ -508,42 +527,41 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
 #pragma unroll
                         for (int j = 0; j < 32; j++) yb[0][j] = silu_f(yb[0][j]) * yb[NW - 1][j];
                     }
-                    if (Q.vec) {
-                        // through shared memory, [input row][32 weight rows]: then 16 bytes per thread and store
+                    // through shared memory, [input row][32 weight rows]: then 16 bytes per thread and store, or, where rows
+                    // of out are not whole 16-byte pieces, a weight row per thread, 8 stores behind their 8 loads (one by
+                    // one, each under its branch, 4,737 rows x 206 took 28 us, and 208 columns 12)
 #pragma unroll
-                        for (int p = 0; p < PASS; p++) {
-                            if (!f32 && p > 0) break;
-                            __syncwarp();
-                            if (f32) {
-                                float* f = reinterpret_cast<float*>(stage_out);
+                    for (int p = 0; p < PASS; p++) {
+                        if (!f32 && p > 0) break;
+                        __syncwarp();
+                        if (f32) {
+                            float* f = reinterpret_cast<float*>(stage_out);
 #pragma unroll
-                                for (int j = 0; j < 32 / PASS; j++) f[32 * j + lane] = yb[0][32 / PASS * p + j];
+                            for (int j = 0; j < 32 / PASS; j++) f[32 * j + lane] = yb[0][32 / PASS * p + j];
+                        } else {
+                            uint16_t* h = reinterpret_cast<uint16_t*>(stage_out);
+                            if (P.type == BITSMOE_F16) {
+#pragma unroll
+                                for (int j = 0; j < 32; j++) h[32 * j + lane] = (uint16_t)to_half_bits(yb[0][j], BITSMOE_F16);
                             } else {
-                                uint16_t* h = reinterpret_cast<uint16_t*>(stage_out);
-                                if (P.type == BITSMOE_F16) {
 #pragma unroll
-                                    for (int j = 0; j < 32; j++) h[32 * j + lane] = (uint16_t)to_half_bits(yb[0][j], BITSMOE_F16);
-                                } else {
-#pragma unroll
-                                    for (int j = 0; j < 32; j++) h[32 * j + lane] = (uint16_t)to_half_bits(yb[0][j], BITSMOE_BF16);
-                                }
+                                for (int j = 0; j < 32; j++) h[32 * j + lane] = (uint16_t)to_half_bits(yb[0][j], BITSMOE_BF16);
                             }
-                            __syncwarp();
-                            const int j0 = 32 / PASS * p, n = f32 ? min(32 / PASS, cols - j0) : cols;
+                        }
+                        __syncwarp();
+                        const int j0 = 32 / PASS * p, n = f32 ? min(32 / PASS, cols - j0) : cols;
+                        const int* dsts = dst_of + 32 * i + j0;  // -1 past the last row
+                        if (Q.vec) {
 #pragma unroll 4
                             for (int j = lane / cw; j < n; j += 32 / cw) {
-                                const int dst = dst_of[32 * i + j0 + j];
+                                const int dst = dsts[j];
                                 const uint4 w = stage_out[j * cw + piece];
                                 if (dst >= 0 && row0 < P.N) *reinterpret_cast<uint4*>(out0 + dst * pitch) = w;
                             }
-                        }
-                    } else {
-                        const int my_dst = dst_of[32 * i + lane];
-#pragma unroll
-                        for (int j = 0; j < 32; j++) {
-                            const int dst = __shfl_sync(0xffffffffu, my_dst, j);
-                            const float o[1] = {yb[0][j]};
-                            if (dst >= 0 && live) store_elems<1>(P.out, P.out_type, (int64_t)dst * P.N + row + lane, o);
+                        } else if (f32) {
+                            gt_store_rows<float, 32 / PASS>(reinterpret_cast<const float*>(stage_out), dsts, P.out, P.N, row + lane);
+                        } else {
+                            gt_store_rows<uint16_t, 32>(reinterpret_cast<const uint16_t*>(stage_out), dsts, P.out, P.N, row + lane);
                         }
                     }
                 }

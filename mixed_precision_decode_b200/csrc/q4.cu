@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
     float* s_g = reinterpret_cast<float*>(s_e + P.K);
     const int64_t bb = q4_block_bytes(P.M.cols_p, G), scale_off = (int64_t)P.M.cols_p * 8;
     for (int v = threadIdx.x; v < P.K * nrb; v += 32 * kQ4T1Warps) {
-        const int e = P.ids[v % P.K];
+        const int e = __ldcg(P.ids + v % P.K);  // leaves no line in L1, which the loads after the wait go through
         if (e >= 0 && e < P.E)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                              P.M.blob + ((int64_t)e * nblk + blockIdx.x + (int64_t)(v / P.K) * gridDim.x) * bb),

@@ -932,3 +932,38 @@ def test_two_graphs_share_workspaces():
         torch.cuda.synchronize()
         for key, want in sets[k]["want"].items():
             assert torch.equal(sets[k][key], want), key
+
+
+def test_routing_right_before_the_single_token_step():
+    """The single-token 4-bit step looks at the ids before the routing that writes them has ended: what it computes goes
+    by the ids written, in a chain of 40 routings and steps whose choices all differ."""
+    E, K, d, d_ff, n = 64, 4, 256, 128, 40
+    g = _gen(91)
+    blob, _ = _q4_blob(_randn(g, E, d, d_ff), 64)
+    dims = B.ffn_dims(d, d_ff, E, K)
+    yg = _randn(g, 1, K, d_ff)
+    logits = _randn(g, n, E)
+    ids, gw = torch.empty(1, K, dtype=torch.int32, device="cuda"), torch.empty(1, K, device="cuda")
+    out, want = torch.empty(n, 1, d, device="cuda"), torch.empty(n, 1, d, device="cuda")
+
+    def chain():
+        for i in range(n):
+            B.topk_route(logits[i:i + 1], ids, gw)
+            B.ffn_down_q4(dims, blob, 64, yg, None, ids, gw, 1, out[i], None, 0)
+
+    for i in range(n):
+        B.topk_route(logits[i:i + 1], ids, gw)
+        torch.cuda.synchronize()
+        B.ffn_down_q4(dims, blob, 64, yg, None, ids, gw, 1, want[i], None, 0)
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    chain()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)

@@ -26,6 +26,7 @@
 // vectors held in registers (86 and more): they hold fewer rows, or leave the L1 cache
 // too small for the vectors.
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.cuh"
 
@@ -246,6 +247,133 @@ __global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? norm_threads(V, NC) : 10
     }
 }
 
+// Rows that start anywhere: groups of 4 elements on their natural boundary all the same, the first of which may begin
+// q = 1 to 3 elements before the row and the last end behind it; those two go element by element, and nothing outside
+// the row is read or written.  A CTA per row.
+// (Against one element per load, us: 4,000 rows x 1,999 in bf16 22.4 and 46.5, 868 x 3,251 11.9 and 18.5, 583 x 1,281 4.2
+// and 5.1; but 1,000 x 300 3.7 and 3.5, 1 x 3,251 3.7 and 3.5, 8,192 x 20 12.2 and 2.5.)
+constexpr int kShiftChunks = 4, kShiftThreads = 256, kShiftMinCols = 1024, kShiftMinRows = 128;
+
+template <bool H32, bool Y32, bool X32>
+__global__ void __launch_bounds__(kShiftThreads, 4) k_norm_shift(const NormParams P) {
+    constexpr int NC = kShiftChunks;
+    __shared__ float s_part[2][32];
+    const int64_t t = blockIdx.x;
+    const int d = P.d, q = (int)((t * P.h_ld) & 3);  // the same for every operand: their strides agree modulo 4
+    const float inv_d = 1.0f / (float)d;
+    const int64_t h0 = t * P.h_ld, y0 = t * P.y_ld, ho0 = t * P.ho_ld, x0 = t * P.x_ld, g0 = t * P.gate_t;
+    int s[NC], at[NC];  // first element of each group; where it is loaded from: a whole group in any case
+    bool full[NC];
+#pragma unroll
+    for (int j = 0; j < NC; j++) {
+        s[j] = 4 * ((int)threadIdx.x + j * (int)blockDim.x) - q;
+        full[j] = s[j] >= 0 && s[j] + 4 <= d;
+        at[j] = full[j] ? s[j] : (4 - q) & 3;
+    }
+    pdl_wait();
+    pdl_trigger();
+    auto inside = [&](int j, int i) { return s[j] + i >= 0 && s[j] + i < d; };
+    NormRaw<4, H32> h[NC];
+    NormRaw<4, Y32> y[NC];
+    float hv[NC][4];
+#pragma unroll
+    for (int j = 0; j < NC; j++) h[j].load(P.h, P.h_type, h0 + at[j]);
+    if (P.y) {
+#pragma unroll
+        for (int j = 0; j < NC; j++) y[j].load(P.y, P.y_type, y0 + at[j]);
+    }
+    // the elements of partial groups, and zeros outside the row
+    auto take = [&](const void* p, int type, int64_t row, int j, float(&v)[4]) {
+        if (full[j]) return;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float one[1] = {0.0f};
+            if (inside(j, i)) load_elems<1>(p, type, row + s[j] + i, one);
+            v[i] = one[0];
+        }
+    };
+    auto scale = [&](const float* w) {
+        float f[NC][4];
+#pragma unroll
+        for (int j = 0; j < NC; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) f[j][i] = w[min(max(s[j] + i, 0), d - 1)];
+#pragma unroll
+        for (int j = 0; j < NC; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) hv[j][i] *= f[j][i];
+    };
+    if (P.y) {
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            y[j].get(P.y_type, hv[j]);
+            take(P.y, P.y_type, y0, j, hv[j]);
+        }
+        float r = P.alpha;
+        if (P.gate && P.gate_i == 0) r *= P.gate[g0];
+        if (P.w_post) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NC; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) ss = fmaf(hv[j][i], hv[j][i], ss);
+            r *= rsqrtf(fmaf(row_sum<false>(ss, s_part[0]), inv_d, P.eps));
+            scale(P.w_post);
+        }
+        if (P.gate && P.gate_i) scale(P.gate + g0);
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            float v[4];
+            h[j].get(P.h_type, v);
+            take(P.h, P.h_type, h0, j, v);
+#pragma unroll
+            for (int i = 0; i < 4; i++) hv[j][i] = full[j] || inside(j, i) ? fmaf(r, hv[j][i], v[i]) : 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            h[j].get(P.h_type, hv[j]);
+            take(P.h, P.h_type, h0, j, hv[j]);
+        }
+    }
+    if (P.h_out) {
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            if (full[j]) {
+                store4<H32>(P.h_out, P.h_type, ho0 + s[j], hv[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float one[1] = {hv[j][i]};
+                    if (inside(j, i)) store_elems<1>(P.h_out, P.h_type, ho0 + s[j] + i, one);
+                }
+            }
+        }
+    }
+    if (!P.x) return;
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NC; j++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) ss = fmaf(hv[j][i], hv[j][i], ss);
+    const float rx = rsqrtf(fmaf(row_sum<false>(ss, s_part[1]), inv_d, P.eps));
+    scale(P.w_pre);
+#pragma unroll
+    for (int j = 0; j < NC; j++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) hv[j][i] *= rx;
+        if (full[j]) {
+            store4<X32>(P.x, P.x_type, x0 + s[j], hv[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float one[1] = {hv[j][i]};
+                if (inside(j, i)) store_elems<1>(P.x, P.x_type, x0 + s[j] + i, one);
+            }
+        }
+    }
+}
+
 constexpr int kNormWarpRows = 8;  // rows (warps) per CTA when a row belongs to a warp
 
 template <int V, bool H32, bool Y32, bool X32>
@@ -281,14 +409,30 @@ static int launch_norm(const NormParams& P, cudaStream_t s) {
     return launch_pdl(k_norm_residual<V, 0, false, H32, Y32, X32>, grid, 1024, 0, s, P);
 }
 
+template <bool H32, bool Y32, bool X32>
+static int launch_norm_shift(const NormParams& P, cudaStream_t s) {
+    const int groups = (P.d + 6) / 4;  // with the partial ones
+    const unsigned threads = (unsigned)roundup((groups + kShiftChunks - 1) / kShiftChunks, 32);
+    return launch_pdl(k_norm_shift<H32, Y32, X32>, dim3((unsigned)P.T), dim3(threads), 0, s, P);
+}
+
+// One of the kernels built for each set of element widths.
+template <bool SHIFT>
 static int launch_norm4(const NormParams& P, cudaStream_t s) {
     const bool h32 = P.h_type == BITSMOE_F32, y32 = P.y_type == BITSMOE_F32, x32 = P.x_type == BITSMOE_F32;
+    auto run = [&](auto h, auto y, auto x) {
+        constexpr bool H = decltype(h)::value, Y = decltype(y)::value, X = decltype(x)::value;
+        if constexpr (SHIFT) return launch_norm_shift<H, Y, X>(P, s);
+        else return launch_norm<4, H, Y, X>(P, s);
+    };
+    const std::true_type f32;
+    const std::false_type f16;
     if (h32) {
-        if (y32) return x32 ? launch_norm<4, true, true, true>(P, s) : launch_norm<4, true, true, false>(P, s);
-        return x32 ? launch_norm<4, true, false, true>(P, s) : launch_norm<4, true, false, false>(P, s);
+        if (y32) return x32 ? run(f32, f32, f32) : run(f32, f32, f16);
+        return x32 ? run(f32, f16, f32) : run(f32, f16, f16);
     }
-    if (y32) return x32 ? launch_norm<4, false, true, true>(P, s) : launch_norm<4, false, true, false>(P, s);
-    return x32 ? launch_norm<4, false, false, true>(P, s) : launch_norm<4, false, false, false>(P, s);
+    if (y32) return x32 ? run(f16, f32, f32) : run(f16, f32, f16);
+    return x32 ? run(f16, f16, f32) : run(f16, f16, f16);
 }
 
 }  // namespace bitsmoe
@@ -341,5 +485,9 @@ BITSMOE_API int bitsmoe_norm_residual(const bitsmoe_norm_args* args, void* strea
                     vec(a.h_out, a.h_type, a.h_out_stride) && vec(a.x, a.x_type, a.x_stride) &&
                     vec(a.w_post, BITSMOE_F32, 0) && vec(a.w_pre, BITSMOE_F32, 0) &&
                     (!a.gate_per_channel || vec(a.gate, BITSMOE_F32, a.gate_stride));
-    return vec4 ? launch_norm4(P, (cudaStream_t)stream) : launch_norm<1, false, false, false>(P, (cudaStream_t)stream);
+    if (vec4) return launch_norm4<false>(P, (cudaStream_t)stream);
+    auto same = [&](const void* p, int64_t ld) { return !p || ((uintptr_t)p % 16 == 0 && ((ld - a.h_stride) & 3) == 0); };
+    const bool shift = a.rows >= kShiftMinRows && a.d >= kShiftMinCols && a.d <= 4 * kShiftChunks * kShiftThreads - 6 && same(a.h, a.h_stride) &&
+                       same(a.y, a.y_stride) && same(a.h_out, a.h_out_stride) && same(a.x, a.x_stride);
+    return shift ? launch_norm4<true>(P, (cudaStream_t)stream) : launch_norm<1, false, false, false>(P, (cudaStream_t)stream);
 }

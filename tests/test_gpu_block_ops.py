@@ -72,6 +72,15 @@ NORM_CASES = [
     (3, 7, F16, BF16, F32, True, "token"),
     (5, 8, BF16, F32, BF16, False, "channel"),
     (333, 1001, F16, F32, F16, False, "token"),
+    (131, 1999, BF16, BF16, BF16, True, "both"),
+    (128, 4090, F16, F16, F32, True, "token"),
+    (129, 1025, F32, F32, F32, False, "channel"),
+    (150, 3251, F32, BF16, F16, True, "channel"),
+    (9, 13, F32, F16, F16, True, "channel"),
+    (6, 4090, F16, F16, F32, True, "token"),
+    (6, 4091, F32, BF16, F32, False, "channel"),
+    (1, 3251, F32, F32, BF16, True, "channel"),
+    (50, 130, F32, F32, F32, True, None),
     (17, 256, BF16, F16, F16, True, "both"),
     (9, 520, F32, F32, BF16, True, "one"),
     (65, 1024, F16, F16, F16, True, "channel"),
@@ -147,8 +156,42 @@ def test_norm_residual_special_rows(d):
     assert bool(torch.isfinite(x[0]).all()) and bool(torch.isfinite(x[3]).all())
 
 
+@pytest.mark.parametrize("T, d", [(9, 8), (9, 61), (9, 1001), (130, 61), (130, 1025), (130, 1026), (130, 1027), (130, 2050),
+                                  (130, 4089), (130, 4090)])
+@pytest.mark.parametrize("types", [(F16, F16, F16), (F32, BF16, F16), (BF16, F32, F32)])
+def test_norm_residual_between_gaps(T, d, types):
+    """Rows that start at any element, with gaps that agree modulo 4 between them: the results are those of dense
+    rows, and what lies in the gaps, NaN, is neither read nor written."""
+    ht, yt, xt = types
+    g = _gen(d)
+    nan = float("nan")
+
+    def rows(t, ld, value=None):
+        buf = torch.full((T, ld), nan, dtype=t, device="cuda")
+        v = buf[:, :d]
+        if value is not None:
+            v.copy_(value)
+        return buf, v
+
+    h, y = _randn(g, T, d).to(ht), _randn(g, T, d).to(yt)
+    w, wp, gate = 1 + 0.1 * _randn(g, d), 1 + 0.1 * _randn(g, d), _randn(g, T, d)
+    for w_post in (None, wp):
+        hb, hv = rows(ht, d + 4, h)
+        yb, yv = rows(yt, d, y)
+        ob, ov = rows(ht, d + 8)
+        xb, xv = rows(xt, d + 12)
+        B.norm_residual(hv, yv, w, xv, w_post=w_post, gate=gate, alpha=0.5, h_out=ov)
+        rh, rx, th, tx = _norm_ref(h, y, w, w_post, gate, 0.5, 1e-6)
+        _within(ov, rh, th + _rounding(rh, ht), "h'")
+        _within(xv, rx, tx + _rounding(rx, xt), "x")
+        B.norm_residual(hv, yv, w, xv, w_post=w_post, gate=gate, alpha=0.5)  # in place
+        assert torch.equal(hv, ov)
+        for b in (hb, ob, xb):
+            assert bool(torch.isnan(b[:, d:]).all())
+
+
 @pytest.mark.parametrize("T", [1, 2050])
-@pytest.mark.parametrize("d", [1, 8, 64, 300, 520, 1000, 1001, 2000, 4104, 6000, 9000])
+@pytest.mark.parametrize("d", [1, 8, 64, 300, 520, 1000, 1001, 1026, 2000, 3999, 4090, 4104, 6000, 9000])
 def test_norm_residual_infinity_in_the_last_place(d, T):
     """mean(h^2) is infinite, 1 / sqrt of it 0: the row's other elements become 0, the infinite one NaN (infinity
     times 0), and no other row notices; the same through the norm on y."""

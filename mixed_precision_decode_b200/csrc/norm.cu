@@ -487,7 +487,8 @@ BITSMOE_API int bitsmoe_norm_residual(const bitsmoe_norm_args* args, void* strea
                     (!a.gate_per_channel || vec(a.gate, BITSMOE_F32, a.gate_stride));
     if (vec4) return launch_norm4<false>(P, (cudaStream_t)stream);
     auto same = [&](const void* p, int64_t ld) { return !p || ((uintptr_t)p % 16 == 0 && ((ld - a.h_stride) & 3) == 0); };
-    const bool shift = a.rows >= kShiftMinRows && a.d >= kShiftMinCols && a.d <= 4 * kShiftChunks * kShiftThreads - 6 && same(a.h, a.h_stride) &&
-                       same(a.y, a.y_stride) && same(a.h_out, a.h_out_stride) && same(a.x, a.x_stride);
+    const bool shift = a.rows >= kShiftMinRows && a.d >= kShiftMinCols && a.d <= 4 * kShiftChunks * kShiftThreads - 6 &&
+                       same(a.h, a.h_stride) && same(a.y, a.y_stride) && same(a.h_out, a.h_out_stride) &&
+                       same(a.x, a.x_stride);
     return shift ? launch_norm4<true>(P, (cudaStream_t)stream) : launch_norm<1, false, false, false>(P, (cudaStream_t)stream);
 }

@@ -4,6 +4,7 @@ and streams; every computation is a libbitsmoe kernel."""
 from __future__ import annotations
 
 import contextlib
+import warnings
 
 import torch
 
@@ -315,12 +316,14 @@ class DenseMoEFFN:
 class MoEBlock:
     """A pre-norm MoE block around an expert FFN:
 
-        h <- h + alpha * gate * (the previous block's output, normalised with w_post if given)
-        x  = rmsnorm(h) w_norm,  logits = w_router x,  y = FFN(x, top-k routing of the logits)
+        x = rmsnorm(h) w_norm,  logits = w_router x,  y = FFN(x, top-k routing of the logits),
+        h <- h + alpha * gate * (y, or rmsnorm(y) w_post with w_post given)
 
-    y is added to h by the next block's forward (or by finish), fused with that block's
-    norm.  gate belongs to that y, None without one.  w_norm, w_post [d_model] f32, w_router [E][d_model] fp16; ffn a SpectralMoEFFN or
-    an fp16 DenseMoEFFN; gate f32 [T or 1][d_model or 1]."""
+    The last step is taken by the next block's forward, fused with that block's norm, or by
+    finish.  w_post and alpha belong to the block that made y: the next block is told which
+    one that is (made_by).  w_norm, w_post [d_model] f32, w_router [E][d_model] fp16; ffn a
+    SpectralMoEFFN or an fp16 DenseMoEFFN; gate, of that y, f32 [T or 1][d_model or 1], None
+    without a y.  eps is that of the norms in this block's calls."""
 
     def __init__(self, ffn: "SpectralMoEFFN | DenseMoEFFN", w_norm: torch.Tensor, w_router: torch.Tensor,
                  w_post: torch.Tensor | None = None, alpha: float = 1.0, eps: float = 1e-6, scoring: str = "softmax",
@@ -331,16 +334,31 @@ class MoEBlock:
         self.ffn, self.w_norm, self.w_router, self.w_post = ffn, w_norm, w_router.contiguous(), w_post
         self.alpha, self.eps, self.scoring, self.renormalise, self.scale = alpha, eps, scoring, renormalise, scale
 
+    def _post_of(self, made_by) -> tuple:
+        """(w_post, alpha) of the output that a block, or such a pair, stands for."""
+        if isinstance(made_by, MoEBlock):
+            return made_by.w_post, made_by.alpha
+        if made_by is not None:
+            w_post, alpha = made_by
+            return w_post, alpha
+        if self.w_post is not None or self.alpha != 1.0:
+            warnings.warn("MoEBlock.forward: y without made_by is added with this block's own w_post and alpha",
+                          stacklevel=3)
+        return self.w_post, self.alpha
+
     def forward(self, h: torch.Tensor, y: torch.Tensor | None = None, gate: torch.Tensor | None = None,
-                status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                status: torch.Tensor | None = None, stream=None,
+                made_by: "MoEBlock | tuple | None" = None) -> torch.Tensor:
         """h [T][d_model] (the residual stream, f32, f16 or bf16), y: the output of the block
-        before, added to h in place first.  Returns this block's output, f32."""
+        before, added to h in place first.  made_by: the MoEBlock that made y, or the pair
+        (w_post or None, alpha) of another kind of block; left out, y is taken as of a block
+        with this one's w_post and alpha.  Returns this block's output, f32."""
         T, d = h.shape
         E = self.ffn.dims.n_experts
+        w_post, alpha = (None, 1.0) if y is None else self._post_of(made_by)
         with _on(stream):
             x = torch.empty((T, d), dtype=torch.float16, device=h.device)
-            B.norm_residual(h, y, self.w_norm, x, w_post=None if y is None else self.w_post, gate=gate, alpha=self.alpha,
-                            eps=self.eps, stream=stream)
+            B.norm_residual(h, y, self.w_norm, x, w_post=w_post, gate=gate, alpha=alpha, eps=self.eps, stream=stream)
             logits = torch.empty((T, E), dtype=torch.float32, device=h.device)
             B.shared_proj(self.w_router, x, logits, T, d, E, stream)
             r = route(logits, self.ffn.dims.top_k, self.scoring, self.renormalise, self.scale, status, stream)
@@ -349,6 +367,6 @@ class MoEBlock:
             return self.ffn.forward(x, r.topk_ids, r.gate_w, status=status, stream=stream)
 
     def finish(self, h: torch.Tensor, y: torch.Tensor, gate: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        """Adds the last block's output to h in place."""
+        """Adds y, this block's own output and the last of a stack, to h in place."""
         B.norm_residual(h, y, w_post=self.w_post, gate=gate, alpha=self.alpha, eps=self.eps, stream=stream)
         return h

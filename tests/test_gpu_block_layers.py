@@ -1,0 +1,73 @@
+"""The layer objects around the routed experts as a stack uses them, on the GPU: whose parameters add an output, streams
+and workspaces, and the calls next to one another.  Tolerances count roundings, as in test_gpu_block_ops.py."""
+import pytest
+import torch
+
+from mixed_precision_decode_b200 import bitsmoe as B
+
+pytestmark = pytest.mark.gpu
+
+U24 = 2.0 ** -24
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def _dense(g, E, K, d, d_ff):
+    from mixed_precision_decode_b200.layer import DenseMoEFFN
+    return DenseMoEFFN((_randn(g, E, d_ff, d) * d ** -0.5).half(), (_randn(g, E, d_ff, d) * d ** -0.5).half(),
+                       (_randn(g, E, d, d_ff) * d_ff ** -0.5).half(), K)
+
+
+def _spectral(kind, seed):
+    """A SpectralMoEFFN of the small test layer, with fp16 or 4-bit down matrices."""
+    from cases import SMALL, get_case
+    from mixed_precision_decode_b200 import synth
+    from mixed_precision_decode_b200.layer import Q4Down, SpectralMoEFFN
+    cfg = SMALL["tiny"]
+    wd = synth.make_down(cfg, synth.make_generator(seed, torch.device("cuda")), torch.device("cuda"))
+    return SpectralMoEFFN(get_case("tiny").layer, Q4Down.pack(wd, 32) if kind == "q4" else wd)
+
+
+@pytest.mark.parametrize("T", [1, 9, 140])
+@pytest.mark.parametrize("kind", ["dense", "fp16", "q4"])
+def test_stack_adds_each_output_with_its_makers_parameters(kind, T):
+    """Every block has its own w_post and alpha, two have no w_post: h after each forward and after finish is the h
+    before it plus alpha gate rmsnorm(y) w_post of the block that made y.  A row's sum of squares is taken in at most 60
+    sequential additions: its inverse root is off by 32 units of 2^-24, the factors by one each."""
+    from mixed_precision_decode_b200.layer import MoEBlock
+    g = _gen(T + len(kind))
+    ffns = [_dense(g, 6, 2, 136, 200) if kind == "dense" else _spectral(kind, 40 + b) for b in range(4)]
+    d, E = ffns[0].dims.d_model, ffns[0].dims.n_experts
+    blocks = [MoEBlock(f, 1 + 0.1 * _randn(g, d), _randn(g, E, d).half(), w_post=1 + 0.3 * _randn(g, d) if b % 3 else None,
+                       alpha=0.5 + 0.25 * b) for b, f in enumerate(ffns)]
+    gates = [torch.sigmoid(_randn(g, T, 1)) for _ in blocks]
+    h = _randn(g, T, d)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def check(before, y, made_by, gate):
+        u = y.double()
+        if made_by.w_post is not None:
+            u = u / torch.sqrt(u.square().mean(1, keepdim=True) + made_by.eps) * made_by.w_post.double()
+        u = made_by.alpha * gate.double() * u
+        tol = 64 * U24 * (before.abs() + u.abs()) + 2.0 ** -149
+        assert bool(((h.double() - before - u).abs() <= tol).all())
+
+    y = before = gate = None
+    for b, own in zip(blocks, gates):
+        h0, y0 = h.double(), y
+        y = b.forward(h, y, gate=gate, status=st, made_by=before)
+        if y0 is not None:
+            check(h0, y0, before, gate)
+        before, gate = b, own
+    h0 = h.double()
+    assert blocks[-1].finish(h, y, gate=gate) is h
+    check(h0, y, blocks[-1], gate)
+    assert B.read_status(st) == 0

@@ -11,11 +11,15 @@ import torch
 from . import bitsmoe as B
 
 
-def _on(stream):
-    """Tensors that a call allocates for itself belong to the stream that its kernels run on: freed on return, their
-    memory then goes to later work of that stream alone."""
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, like: torch.Tensor):
+    """Makes the given stream current (None: as it is).  Tensors that a call allocates, fills or copies for itself then
+    belong to the stream that its kernels run on: ordered with them, and, freed on return, their memory goes to later
+    work of that stream alone."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if isinstance(stream, torch.cuda.Stream):
         return torch.cuda.stream(stream)
     return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
@@ -41,14 +45,15 @@ class PackedProjection:
         E, r, d_out = comps.shape
         d_in = phi_t.shape[1]
         dev = comps.device
-        plan = B.pack_plan(d_in, d_out, E, r, top_k, widths.cpu())
-        w_dev = widths.to(dev, torch.uint8).contiguous()
-        if scales is None:
-            scales = torch.empty((E, r), dtype=torch.int16, device=dev)
-            B.compute_scales(plan, comps, w_dev, scales, status, stream)
-        blob = torch.empty(plan.blob_bytes, dtype=torch.uint8, device=dev)
-        B.pack(plan, comps.contiguous(), w_dev, scales.contiguous(), amps.contiguous(), blob, status, stream)
-        return cls(plan, blob, phi_t.contiguous())
+        with _on(stream, comps):
+            plan = B.pack_plan(d_in, d_out, E, r, top_k, widths.cpu())
+            w_dev = widths.to(dev, torch.uint8).contiguous()
+            if scales is None:
+                scales = torch.empty((E, r), dtype=torch.int16, device=dev)
+                B.compute_scales(plan, comps, w_dev, scales, status, stream)
+            blob = torch.empty(plan.blob_bytes, dtype=torch.uint8, device=dev)
+            B.pack(plan, comps.contiguous(), w_dev, scales.contiguous(), amps.contiguous(), blob, status, stream)
+            return cls(plan, blob, phi_t.contiguous())
 
     def expert_bytes_touched(self, experts) -> int:
         """Packed bytes (planes + per-component metadata, padding included) of the given experts."""
@@ -69,21 +74,22 @@ def decompose_and_pack(W: torch.Tensor, rank: int, widths_in_order, counts, top_
     projection and the decomposition (phi_t, sigma, amps, comps, widths)."""
     E, d_out, d_in = W.shape
     dev = W.device
-    n = B.ssd_workspace_bytes(E, d_out, d_in, rank)
-    if n == 0:
-        raise B.BitsMoEError(B.ECUDA, "ssd_workspace_bytes")
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    phi_t = torch.empty((rank, d_in), dtype=torch.float16, device=dev)
-    phi_t32 = torch.empty((rank, d_in), dtype=torch.float32, device=dev)
-    sigma = torch.empty(rank, dtype=torch.float32, device=dev)
-    amps = torch.empty((E, rank), dtype=torch.float32, device=dev)
-    comps = torch.empty((E, rank, d_out), dtype=torch.float32, device=dev)
-    B.ssd_decompose(W.contiguous(), rank, phi_t, amps, comps, ws, n, sigma=sigma, phi_t32=phi_t32, status=status,
-                    stream=stream)
-    del ws
-    widths = torch.from_numpy(B.assign_widths(amps.cpu().numpy(), widths_in_order, counts))
-    pk = PackedProjection.from_factors(phi_t, amps, comps, widths, top_k, status=status, stream=stream)
-    return pk, {"phi_t": phi_t, "phi_t32": phi_t32, "sigma": sigma, "amps": amps, "comps": comps, "widths": widths}
+    with _on(stream, W):
+        n = B.ssd_workspace_bytes(E, d_out, d_in, rank)
+        if n == 0:
+            raise B.BitsMoEError(B.ECUDA, "ssd_workspace_bytes")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        phi_t = torch.empty((rank, d_in), dtype=torch.float16, device=dev)
+        phi_t32 = torch.empty((rank, d_in), dtype=torch.float32, device=dev)
+        sigma = torch.empty(rank, dtype=torch.float32, device=dev)
+        amps = torch.empty((E, rank), dtype=torch.float32, device=dev)
+        comps = torch.empty((E, rank, d_out), dtype=torch.float32, device=dev)
+        B.ssd_decompose(W.contiguous(), rank, phi_t, amps, comps, ws, n, sigma=sigma, phi_t32=phi_t32, status=status,
+                        stream=stream)
+        del ws
+        widths = torch.from_numpy(B.assign_widths(amps.cpu().numpy(), widths_in_order, counts))
+        pk = PackedProjection.from_factors(phi_t, amps, comps, widths, top_k, status=status, stream=stream)
+        return pk, {"phi_t": phi_t, "phi_t32": phi_t32, "sigma": sigma, "amps": amps, "comps": comps, "widths": widths}
 
 
 def fqcm_widths(dec: dict, x_calib: torch.Tensor, ids_calib: torch.Tensor, gw_calib: torch.Tensor,
@@ -98,12 +104,14 @@ def fqcm_widths(dec: dict, x_calib: torch.Tensor, ids_calib: torch.Tensor, gw_ca
     r, d_in = phi_t.shape
     E, _, d_out = dec["comps"].shape
     T = x_calib.shape[0]
-    Z = torch.empty((T, r), dtype=torch.float32, device=phi_t.device)
-    B.shared_proj(phi_t, x_calib.contiguous(), Z, T, d_in, r, stream)
-    beta = B.fqcm_beta(Z.cpu().numpy(), ids_calib.cpu().numpy(), gw_calib.cpu().numpy(), E)
-    eps = B.fqcm_eps(dec["comps"].cpu().numpy())
+    with _on(stream, phi_t):
+        Z = torch.empty((T, r), dtype=torch.float32, device=phi_t.device)
+        B.shared_proj(phi_t, x_calib.contiguous(), Z, T, d_in, r, stream)
+        beta = B.fqcm_beta(Z.cpu().numpy(), ids_calib.cpu().numpy(), gw_calib.cpu().numpy(), E)
+        eps = B.fqcm_eps(dec["comps"].cpu().numpy())
+        amps = dec["amps"].cpu().numpy()
     budget = int(avg_bits * E * r * d_out)
-    widths, loss = B.allocate_widths(dec["amps"].cpu().numpy(), beta, eps, d_out, budget)
+    widths, loss = B.allocate_widths(amps, beta, eps, d_out, budget)
     return torch.from_numpy(widths), loss, {"beta": beta, "eps": eps}
 
 
@@ -152,21 +160,22 @@ class SpectralMoELayer:
         L2 while this call evaluates its experts (single-token path)."""
         T = x.shape[0]
         dev = x.device
-        if out is None:
-            out = {}
-            for name, p in (("gate", self.gate), ("up", self.up)):
-                out[f"Y_sum_{name}"] = torch.empty((T, p.d_out), dtype=torch.float32, device=dev)
-                if want_experts:
-                    out[f"Y_experts_{name}"] = torch.empty((T, p.top_k, p.d_out), dtype=torch.float32, device=dev)
-                if want_z:
-                    out[f"Z_{name}"] = torch.empty((T, p.rank), dtype=torch.float32, device=dev)
-        ios = self._proj_ios(out)
-        ws = self.workspace(T)
-        if next_layer is None:
-            B.layer_forward(ios[0], ios[1], x, topk_ids, gate_w, T, ws, ws.numel(), status, stream)
-        else:
-            B.layer_forward_chained(ios[0], ios[1], x, topk_ids, gate_w, T, ws, ws.numel(), next_layer.gate.phi_t,
-                                    next_layer.up.phi_t, status, stream)
+        with _on(stream, x):
+            if out is None:
+                out = {}
+                for name, p in (("gate", self.gate), ("up", self.up)):
+                    out[f"Y_sum_{name}"] = torch.empty((T, p.d_out), dtype=torch.float32, device=dev)
+                    if want_experts:
+                        out[f"Y_experts_{name}"] = torch.empty((T, p.top_k, p.d_out), dtype=torch.float32, device=dev)
+                    if want_z:
+                        out[f"Z_{name}"] = torch.empty((T, p.rank), dtype=torch.float32, device=dev)
+            ios = self._proj_ios(out)
+            ws = self.workspace(T)
+            if next_layer is None:
+                B.layer_forward(ios[0], ios[1], x, topk_ids, gate_w, T, ws, ws.numel(), status, stream)
+            else:
+                B.layer_forward_chained(ios[0], ios[1], x, topk_ids, gate_w, T, ws, ws.numel(), next_layer.gate.phi_t,
+                                        next_layer.up.phi_t, status, stream)
         return out
 
 
@@ -182,14 +191,14 @@ class Q4Down:
     def pack(cls, w_down: torch.Tensor, group: int = 64, status: torch.Tensor | None = None, stream=None) -> "Q4Down":
         """Quantise w_down [E][d_model][d_ff] (float32, float16 or bfloat16, on the GPU)."""
         n = B.q4_bytes(*w_down.shape, group)
-        with _on(stream):
+        with _on(stream, w_down):
             blob = torch.empty(n, dtype=torch.uint8, device=w_down.device)
             B.q4_pack(w_down.contiguous(), group, blob, status, stream)
         return cls(blob, w_down.shape, group)
 
     def unpack(self, stream=None) -> torch.Tensor:
         """The stored values, [E][d_model][d_ff] f32."""
-        with _on(stream):
+        with _on(stream, self.blob):
             w = torch.empty(self.shape, dtype=torch.float32, device=self.blob.device)
             B.q4_unpack(self.blob, self.group, w, stream)
         return w
@@ -249,19 +258,19 @@ class SpectralMoEFFN:
         """x [T][d_in] fp16, topk_ids [T][top_k] int32, gate_w [T][top_k] f32 -> out [T][d_model] f32.
         gate_up: the gate/up output buffers (gate_up_buffers) to reuse between calls."""
         T = x.shape[0]
-        if out is None:
-            out = torch.empty((T, self.dims.d_model), dtype=torch.float32, device=x.device)
-        if gate_up is None:
-            gate_up = self.gate_up_buffers(T, x.device)
-        if self.q4 is not None:
-            self.layer.forward(x, topk_ids, gate_w, out=gate_up, status=status, stream=stream)
+        with _on(stream, x):
+            if out is None:
+                out = torch.empty((T, self.dims.d_model), dtype=torch.float32, device=x.device)
+            if gate_up is None:
+                gate_up = self.gate_up_buffers(T, x.device)
             ws = self.workspace(T)
-            B.ffn_down_q4(self.dims, self.q4.blob, self.q4.group, gate_up["Y_experts_gate"], gate_up["Y_experts_up"],
-                          topk_ids, gate_w, T, out, ws, ws.numel(), status, stream)
-            return out
-        ios = self.layer._proj_ios(gate_up)
-        ws = self.workspace(T)
-        B.ffn_forward(ios[0], ios[1], self.w_down, x, topk_ids, gate_w, T, out, ws, ws.numel(), status, stream)
+            if self.q4 is not None:
+                self.layer.forward(x, topk_ids, gate_w, out=gate_up, status=status, stream=stream)
+                B.ffn_down_q4(self.dims, self.q4.blob, self.q4.group, gate_up["Y_experts_gate"], gate_up["Y_experts_up"],
+                              topk_ids, gate_w, T, out, ws, ws.numel(), status, stream)
+            else:
+                ios = self.layer._proj_ios(gate_up)
+                B.ffn_forward(ios[0], ios[1], self.w_down, x, topk_ids, gate_w, T, out, ws, ws.numel(), status, stream)
         return out
 
 
@@ -278,7 +287,7 @@ def route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", renormalis
     """Top-k routing of router logits [T][E] (f32, f16 or bf16, on the GPU)."""
     T, E = logits.shape
     i32 = {"dtype": torch.int32, "device": logits.device}
-    with _on(stream):
+    with _on(stream, logits):
         r = Routing(torch.empty((T, top_k), **i32), torch.empty((T, top_k), dtype=torch.float32, device=logits.device),
                     torch.empty(E + 1, **i32), torch.empty(T * top_k, **i32))
         n = B.topk_route_workspace_bytes(T, E, top_k)
@@ -304,7 +313,7 @@ class DenseMoEFFN:
                 status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x [T][d_model] in the matrices' type -> out [T][d_model] f32."""
         T = x.shape[0]
-        with _on(stream):
+        with _on(stream, x):
             if out is None:
                 out = torch.empty((T, self.dims.d_model), dtype=torch.float32, device=x.device)
             ws = torch.empty(B.dense_ffn_workspace_bytes(self.dims, T), dtype=torch.uint8, device=x.device)
@@ -356,7 +365,7 @@ class MoEBlock:
         T, d = h.shape
         E = self.ffn.dims.n_experts
         w_post, alpha = (None, 1.0) if y is None else self._post_of(made_by)
-        with _on(stream):
+        with _on(stream, h):
             x = torch.empty((T, d), dtype=torch.float16, device=h.device)
             B.norm_residual(h, y, self.w_norm, x, w_post=w_post, gate=gate, alpha=alpha, eps=self.eps, stream=stream)
             logits = torch.empty((T, E), dtype=torch.float32, device=h.device)

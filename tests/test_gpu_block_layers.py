@@ -71,3 +71,46 @@ def test_stack_adds_each_output_with_its_makers_parameters(kind, T):
     assert blocks[-1].finish(h, y, gate=gate) is h
     check(h0, y, blocks[-1], gate)
     assert B.read_status(st) == 0
+
+
+@pytest.mark.parametrize("T", [1, 9, 140])
+@pytest.mark.parametrize("kind", ["fp16", "q4", "layer"])
+def test_spectral_calls_on_a_given_stream(kind, T):
+    """stream=, as a torch stream and as a raw handle, on a new object each time (its first call makes the workspace),
+    while the current stream allocates and overwrites memory: the results are those of the current stream's calls.  One
+    token's partial rows are added by atomics, in any order: there within the outputs' 2e-3 bound."""
+    from cases import get_case
+    from mixed_precision_decode_b200.layer import SpectralMoELayer
+    g = _gen(5 * T)
+    ffn = _spectral("q4" if kind == "q4" else "fp16", 91)
+    d, E, K = ffn.dims.d_model, ffn.dims.n_experts, ffn.dims.top_k
+    x, gw = _randn(g, T, d).half(), torch.rand((T, K), generator=g, device="cuda")
+    ids = torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :K].to(torch.int32).contiguous()
+    layer = get_case("tiny").layer
+
+    def run(stream, noise):
+        new = SpectralMoELayer(layer.gate, layer.up)
+        if kind != "layer":
+            new = type(ffn)(new, ffn.q4 or ffn.w_down)
+        torch.cuda.synchronize()
+        sizes = (T * d, 2 * T * d, T * K * ffn.dims.d_ff, new.workspace(T).numel() // 4)
+        new._ws.clear()
+        torch.cuda.synchronize()
+        got = []
+        for _ in range(4):
+            got.append(new.forward(x, ids, gw, stream=stream))
+            if noise:
+                for n in sizes:
+                    for _ in range(4):
+                        torch.full((max(n, 64),), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        return torch.stack([y if kind != "layer" else torch.cat((y["Y_sum_gate"], y["Y_sum_up"]), 1) for y in got])
+
+    want = run(None, False)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = run(stream, True)
+        if T > 1:
+            assert torch.equal(got, want)
+        else:
+            assert bool(((got - want).abs() <= 2e-3 * want.abs().amax(-1, keepdim=True)).all())

@@ -15,14 +15,15 @@ _HERE = contextlib.nullcontext()
 
 
 def _on(stream, like: torch.Tensor):
-    """Makes the given stream current (None: as it is).  Tensors that a call allocates, fills or copies for itself then
-    belong to the stream that its kernels run on: ordered with them, and, freed on return, their memory goes to later
-    work of that stream alone."""
-    if stream is None:
-        return _HERE
+    """Makes like's GPU and the given stream (torch's current one there, when None) current.  Tensors that a call
+    allocates, fills or copies for itself then belong to the stream that its kernels run on: ordered with them, and,
+    freed on return, their memory goes to later work of that stream alone."""
     if isinstance(stream, torch.cuda.Stream):
         return torch.cuda.stream(stream)
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
+    dev = like.get_device()
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev))
+    return _HERE if dev < 0 or dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 class PackedProjection:

@@ -283,9 +283,10 @@ int bitsmoe_ffn_down_launches(const bitsmoe_ffn_dims *dims, int32_t T);
  * A slot whose id is outside [0, E) contributes nothing and sets
  * BITSMOE_ST_BADEXPERT.  fp32 arithmetic; each token's sum runs in slot order, so
  * results do not depend on timing.  The single-token kernel is launched with
- * programmatic dependent launch: it requests its weight rows into L2 before it
- * waits for the kernel ahead of it in the stream (the layer call that wrote
- * Y_gate / Y_up), and reads nothing else before that wait.
+ * programmatic dependent launch: before it waits for the kernel ahead of it in the
+ * stream (the layer call that wrote Y_gate / Y_up) it looks at topk_ids, requests the
+ * weight rows they name into L2 and loads the first of them; after the wait it reads
+ * topk_ids again and goes by what they are then.
  * Errors: EINVAL (dims, NULL or misaligned pointers), ESIZE (workspace), ECUDA. */
 int bitsmoe_ffn_down(const bitsmoe_ffn_dims *dims, const uint16_t *w_down, const float *Y_gate, const float *Y_up,
                      const int32_t *topk_ids, const float *gate_w, int32_t T, float *out, void *workspace,
@@ -394,7 +395,9 @@ int bitsmoe_allocate_widths(const float *amps_host, const double *beta_host, con
  * products grouped by expert for dense experts and long prompts.  The BitsMoE pages
  * stop at the gate and up projections and have no counterpart to them.  Kernels are
  * launched with programmatic dependent launch: each waits for the kernels before it in
- * the stream before it reads or writes anything. */
+ * the stream before it writes anything or reads what goes into its results.  The 4-bit
+ * step for one token looks at topk_ids before that, to ask L2 for the weights of the
+ * experts they name; it reads them again after it. */
 
 /* ---- element types ---- */
 #define BITSMOE_F32 0

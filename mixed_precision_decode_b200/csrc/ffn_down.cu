@@ -154,9 +154,10 @@ __global__ void __launch_bounds__(kDnThreads) k_down_t1(const DownT1Params P) {
     // contiguous range per slot) are requested into L2, and each warp loads its first
     // batch of rows into registers.  The ids may still be being written by an earlier
     // kernel, so they only choose what to read here: after the wait they are read
-    // again, and a batch whose expert changed is loaded again.
+    // again, and a batch whose expert changed is loaded again.  This early look goes past
+    // L1: a line left there could be what the loads after the wait find.
     if (tid < P.K && nrows > 0) {
-        const int e = P.ids[tid];
+        const int e = __ldcg(P.ids + tid);
         if (e >= 0 && e < P.E)
             prefetch_l2(P.w + ((size_t)e * P.d_model + row0) * P.d_ff, 2ull * nrows * P.d_ff);
     }
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kDnThreads) k_down_t1(const DownT1Params P) {
     int e_pre = -1;
     if (first_fits && warp < nbatch) {
         const int j = warp / nrb;
-        e_pre = P.ids[j];
+        e_pre = __ldcg(P.ids + j);
         if (e_pre < 0 || e_pre >= P.E) e_pre = -1;
         load_rows(wv, P, e_pre, row0 + (warp - j * nrb) * kDnRowBatch, nrows - (warp - j * nrb) * kDnRowBatch, 0,
                   nch, lane);

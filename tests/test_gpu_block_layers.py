@@ -114,3 +114,48 @@ def test_spectral_calls_on_a_given_stream(kind, T):
             assert torch.equal(got, want)
         else:
             assert bool(((got - want).abs() <= 2e-3 * want.abs().amax(-1, keepdim=True)).all())
+
+
+@pytest.mark.parametrize("kind", ["fp16", "q4"])
+def test_single_token_step_right_behind_its_routing(kind):
+    """The single-token steps look at the ids before the routing that writes them has ended: what they compute goes by
+    the ids written, in a chain of 40 routings and steps whose choices all differ, run at once and as a replayed graph."""
+    E, K, d, d_ff, n = 64, 4, 256, 128, 40
+    g = _gen(92)
+    w = _randn(g, E, d, d_ff).half()
+    dims = B.ffn_dims(d, d_ff, E, K)
+    blob = torch.empty(B.q4_bytes(E, d, d_ff, 64), dtype=torch.uint8, device="cuda")
+    B.q4_pack(w, 64, blob)
+    yg, yu = _randn(g, 1, K, d_ff), _randn(g, 1, K, d_ff)
+    logits = _randn(g, n, E)
+    ids, gw = torch.empty(1, K, dtype=torch.int32, device="cuda"), torch.empty(1, K, device="cuda")
+    out, want = torch.empty(n, 1, d, device="cuda"), torch.empty(n, 1, d, device="cuda")
+    assert B.ffn_down_workspace_bytes(dims, 1) == 0 and B.ffn_down_q4_workspace_bytes(dims, 64, 1) == 0
+
+    def step(to):
+        if kind == "fp16":
+            B.ffn_down(dims, w, yg, yu, ids, gw, 1, to)
+        else:
+            B.ffn_down_q4(dims, blob, 64, yg, yu, ids, gw, 1, to)
+
+    def chain():
+        for i in range(n):
+            B.topk_route(logits[i:i + 1], ids, gw)
+            step(out[i])
+
+    for i in range(n):
+        B.topk_route(logits[i:i + 1], ids, gw)
+        torch.cuda.synchronize()
+        step(want[i])
+        torch.cuda.synchronize()
+    chain()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)

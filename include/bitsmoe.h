@@ -530,8 +530,9 @@ int bitsmoe_ffn_down_q4(const bitsmoe_q4_args *args, void *stream);
  * offsets and rows as bitsmoe_topk_route writes them: with rows = order and rows_per_a
  * = top_k every routed pair reads its token's row.  Rows of out that no group names are
  * left as they are.  The sizes of the groups stay on the device: nothing waits for
- * them.  An offset outside [0, n_rows] or below the one before it is clamped, and a
- * row index outside A (or out, with scatter) is left out; both set BITSMOE_ST_BADGROUP.
+ * them.  An offset outside [0, n_rows] is clamped, one below an earlier offset counts as
+ * that one (groups never share a row), and a row index outside A (or out, with scatter)
+ * is left out; all of them set BITSMOE_ST_BADGROUP.
  * Two sorted rows with the same output row race; out must not overlap an operand.
  * fp32 results of long sums: the tensor cores' accumulators cut toward zero, so at most
  * 768 k's (gated: 384) are summed in one, and fp32 additions join them: about 1e-6 of the

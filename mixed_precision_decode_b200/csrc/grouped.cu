@@ -28,10 +28,15 @@ struct GmmParams {
     int P, N, D, E, n_a, div, type, out_type, scatter;
 };
 
-// The group of expert e, inside [0, P] whatever the offsets hold.
-__device__ __forceinline__ void group_range(const GmmParams& P, int e, int& i0, int& i1) {
+// The group of expert e, whatever the offsets hold: an offset counts as the largest up to it, inside [0, P], so that
+// groups never share a row (two experts would write it) and stand in order.  down: some offset is below the one before
+// it, and the largest has to be looked for; else an offset's own value is it.
+__device__ __forceinline__ void group_range(const GmmParams& P, int e, bool down, int& i0, int& i1) {
     const int a = P.offsets[e], b = P.offsets[e + 1];
-    i0 = min(max(a, 0), P.P);
+    int most = max(a, 0);
+    if (down)
+        for (int i = 0; i < e; i++) most = max(most, P.offsets[i]);
+    i0 = min(most, P.P);
     i1 = min(max(b, i0), P.P);
     if ((i0 != a || i1 != b) && P.status) atomicOr(P.status, BITSMOE_ST_BADGROUP);
 }
@@ -115,10 +120,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ bool find_slot(const GmmParams& P, int slot, int tok, int& e_out, int& i0_out, int& n_out) {
     const int lane = threadIdx.x & 31;
     int base = 0;
+    bool down = false;
     for (int e0 = 0; e0 < P.E; e0 += 32) {
         const int e = e0 + lane;
         int i0 = 0, i1 = 0;
-        if (e < P.E) group_range(P, e, i0, i1);
+        down = __any_sync(0xffffffffu, down || (e < P.E && P.offsets[e + 1] < P.offsets[e]));
+        if (e < P.E) group_range(P, e, down, i0, i1);
         const int n = (i1 - i0 + tok - 1) / tok;
         int inc = n;
 #pragma unroll
@@ -392,8 +399,8 @@ struct GtTile {
 };
 __device__ __forceinline__ int gt_pieces(int cnt, int tok) { return (cnt + tok - 1) / tok; }
 
-// Tile `item`; s_tab[e]: tiles of the experts before e.
-__device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab, int item) {
+// Tile `item`; s_tab[e]: tiles of the experts before e; down: as group_range has it.
+__device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab, bool down, int item) {
     int lo = 0, hi = Q.p.E;  // s_tab[lo] <= item < s_tab[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -405,7 +412,7 @@ __device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab
     GtTile t;
     t.e = lo;
     int i0, i1;
-    group_range(Q.p, lo, i0, i1);
+    group_range(Q.p, lo, down, i0, i1);
     const int np = gt_pieces(i1 - i0, Q.tok), within = item - s_tab[lo];
     // pieces of equal size, whole steps of 32
     const int size = (int)roundup((uint64_t)((i1 - i0 + np - 1) / np), 32);
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t s_full[kGtMaxStages], s_empty[kGtMaxStages], s_rows[kGtMaxStages], s_afull[2], s_aempty[2];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_fail;
+    __shared__ int s_fail, s_down;
     __shared__ int s_dst[EW][1024 / EW];  // per epilogue warp: output row of each of its input rows, -1 for none
     __shared__ __align__(16) uint4 s_out[EW][1024 / EW];  // per epilogue warp: results to be stored
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -455,9 +462,13 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
     pdl_wait();
     pdl_trigger();
     // tiles of every expert, then their running sum
+    int descents = 0;
+    for (int e = tid; e < P.E; e += blockDim.x) descents |= P.offsets[e + 1] < P.offsets[e];
+    const bool down = __syncthreads_or(descents);
+    if (tid == 0) s_down = down;
     for (int e = tid; e < P.E; e += blockDim.x) {
         int i0, i1;
-        group_range(P, e, i0, i1);
+        group_range(P, e, down, i0, i1);
         s_tab[e + 1] = gt_pieces(i1 - i0, Q.tok) * Q.ntiles;
     }
     if (tid == 0) s_tab[0] = 0;
@@ -501,7 +512,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
         uint32_t phase = 0;
         bool ok = true;
         for (int item = first; item < total && ok; item += step) {
-            const GtTile t = gt_tile(Q, s_tab, item);
+            const GtTile t = gt_tile(Q, s_tab, s_down, item);
             for (int i = 0; i < NB; i++) {
                 const int j = 32 * (SHARE * i + half) + lane;
                 int64_t src, dst;
@@ -582,7 +593,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
             uint32_t phase = 1;  // parity of the stage's last release: nothing to wait for in the first round
             bool ok = true;
             for (int item = first; item < total && ok; item += step) {
-                const GtTile t = gt_tile(Q, s_tab, item);
+                const GtTile t = gt_tile(Q, s_tab, s_down, item);
                 const int half = t.n_mma / 2, row_w = t.e * P.N + t.n0 + (int)rank * kGtM;
                 const int row_a = t.i0 + (int)rank * half;
                 // one box of at least the half's rows: an issued TMA costs more than the rows behind them
@@ -616,7 +627,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
                 uint32_t phase = 0, aphase = 1;
                 bool ok = true;
                 for (int item = first; item < total && ok; item += step) {
-                    const GtTile t = gt_tile(Q, s_tab, item);
+                    const GtTile t = gt_tile(Q, s_tab, s_down, item);
                     const uint32_t idesc = tc_idesc(2 * kGtM, t.n_mma) | (P.type == BITSMOE_BF16 ? (1u << 7) | (1u << 10) : 0u);
                     int left = 0;  // stages left in the segment
                     for (int k = 0; k < Q.nst; k++) {
@@ -687,7 +698,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
             uint32_t phase = 1;
             bool ok = true;
             for (int item = first; item < total && ok; item += step) {
-                const GtTile t = gt_tile(Q, s_tab, item);
+                const GtTile t = gt_tile(Q, s_tab, s_down, item);
                 const int half = t.n_mma / 2;
                 const uint16_t* src_row[RPT];  // NULL: zeros
 #pragma unroll

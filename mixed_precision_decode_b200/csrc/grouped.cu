@@ -28,17 +28,19 @@ struct GmmParams {
     int P, N, D, E, n_a, div, type, out_type, scatter;
 };
 
-// The group of expert e, whatever the offsets hold: an offset counts as the largest up to it, inside [0, P], so that
-// groups never share a row (two experts would write it) and stand in order.  down: some offset is below the one before
-// it, and the largest has to be looked for; else an offset's own value is it.
-__device__ __forceinline__ void group_range(const GmmParams& P, int e, bool down, int& i0, int& i1) {
+// The group of expert e in ascending offsets, inside [0, P].  True when its end is below its start: the groups from it
+// on are then those of group_from.
+__device__ __forceinline__ bool group_range(const GmmParams& P, int e, int& i0, int& i1) {
     const int a = P.offsets[e], b = P.offsets[e + 1];
-    int most = max(a, 0);
-    if (down)
-        for (int i = 0; i < e; i++) most = max(most, P.offsets[i]);
-    i0 = min(most, P.P);
+    i0 = min(max(a, 0), P.P);
     i1 = min(max(b, i0), P.P);
     if ((i0 != a || i1 != b) && P.status) atomicOr(P.status, BITSMOE_ST_BADGROUP);
+    return b < a;
+}
+// Whatever the offsets hold, an offset counts as the largest up to it, so that no row belongs to two experts (both
+// would write it): the group that starts at i0, the end of the one before, ends at i0 or at offset e + 1.
+__device__ __forceinline__ int group_from(const GmmParams& P, int e, int i0) {
+    return min(max(P.offsets[e + 1], i0), P.P);
 }
 
 // Input and output row of sorted row i; false (and the status bit) for a bad index.
@@ -120,12 +122,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ bool find_slot(const GmmParams& P, int slot, int tok, int& e_out, int& i0_out, int& n_out) {
     const int lane = threadIdx.x & 31;
     int base = 0;
-    bool down = false;
+    bool fell = false;
     for (int e0 = 0; e0 < P.E; e0 += 32) {
         const int e = e0 + lane;
         int i0 = 0, i1 = 0;
-        down = __any_sync(0xffffffffu, down || (e < P.E && P.offsets[e + 1] < P.offsets[e]));
-        if (e < P.E) group_range(P, e, down, i0, i1);
+        bool falls = false;
+        if (e < P.E) falls = group_range(P, e, i0, i1);
+        fell = __any_sync(0xffffffffu, falls);
+        if (fell) break;
         const int n = (i1 - i0 + tok - 1) / tok;
         int inc = n;
 #pragma unroll
@@ -144,6 +148,21 @@ __device__ __forceinline__ bool find_slot(const GmmParams& P, int slot, int tok,
             return true;
         }
         base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (!fell) return false;
+    int i0 = min(max(P.offsets[0], 0), P.P);
+    base = 0;
+#pragma unroll 1
+    for (int e = 0; e < P.E; e++) {  // offsets that fall: one expert after the other
+        const int i1 = group_from(P, e, i0), n = (i1 - i0 + tok - 1) / tok;
+        if (slot < base + n) {
+            e_out = e;
+            i0_out = i0 + (slot - base) * tok;
+            n_out = min(tok, i1 - i0_out);
+            return true;
+        }
+        base += n;
+        i0 = i1;
     }
     return false;
 }
@@ -399,8 +418,8 @@ struct GtTile {
 };
 __device__ __forceinline__ int gt_pieces(int cnt, int tok) { return (cnt + tok - 1) / tok; }
 
-// Tile `item`; s_tab[e]: tiles of the experts before e; down: as group_range has it.
-__device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab, bool down, int item) {
+// Tile `item`; s_tab[e]: tiles of the experts before e.
+__device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab, int item) {
     int lo = 0, hi = Q.p.E;  // s_tab[lo] <= item < s_tab[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -412,7 +431,7 @@ __device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab
     GtTile t;
     t.e = lo;
     int i0, i1;
-    group_range(Q.p, lo, down, i0, i1);
+    group_range(Q.p, lo, i0, i1);
     const int np = gt_pieces(i1 - i0, Q.tok), within = item - s_tab[lo];
     // pieces of equal size, whole steps of 32
     const int size = (int)roundup((uint64_t)((i1 - i0 + np - 1) / np), 32);
@@ -423,6 +442,35 @@ __device__ __forceinline__ GtTile gt_tile(const GmmTcParams& Q, const int* s_tab
     return t;
 }
 
+// All of it by fp32 products one by one, a result per thread: for offsets that fall somewhere, which are an error of
+// the caller's that need not be fast.  (With tiles that look for their groups in such offsets, every call took 1% more:
+// 16,384 pairs, 768 -> 2048, 122.9 us instead of 121.4.)
+template <bool GATED>
+__device__ __forceinline__ void gmm_plain(const GmmParams& P) {
+    int i0 = min(max(P.offsets[0], 0), P.P);
+#pragma unroll 1
+    for (int e = 0; e < P.E; e++) {
+        const int i1 = group_from(P, e, i0);
+        const int64_t n = (int64_t)(i1 - i0) * P.N;
+#pragma unroll 1
+        for (int64_t v = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; v < n; v += (int64_t)gridDim.x * blockDim.x) {
+            int64_t src, dst;
+            if (!row_pair(P, i0 + (int)(v / P.N), src, dst)) continue;
+            const int64_t row = ((int64_t)e * P.N + v % P.N) * P.D;
+            float y = 0.0f, u = 0.0f;
+#pragma unroll 1
+            for (int k = 0; k < P.D; k++) {
+                const float a = half_bits(P.a[src * P.lda + k], P.type);
+                y = fmaf(half_bits(P.w[row + k], P.type), a, y);
+                if (GATED) u = fmaf(half_bits(P.w_up[row + k], P.type), a, u);
+            }
+            const float o[1] = {GATED ? silu_f(y) * u : y};
+            store_elems<1>(P.out, P.out_type, dst * P.N + v % P.N, o);
+        }
+        i0 = i1;
+    }
+}
+
 template <bool GATED, bool GATHER, bool SEG>
 __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
     k_gmm_tc(const GmmTcParams Q, const __grid_constant__ GtMaps M) {
@@ -430,7 +478,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t s_full[kGtMaxStages], s_empty[kGtMaxStages], s_rows[kGtMaxStages], s_afull[2], s_aempty[2];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_fail, s_down;
+    __shared__ int s_fail;
     __shared__ int s_dst[EW][1024 / EW];  // per epilogue warp: output row of each of its input rows, -1 for none
     __shared__ __align__(16) uint4 s_out[EW][1024 / EW];  // per epilogue warp: results to be stored
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -462,17 +510,15 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
     pdl_wait();
     pdl_trigger();
     // tiles of every expert, then their running sum
-    int descents = 0;
-    for (int e = tid; e < P.E; e += blockDim.x) descents |= P.offsets[e + 1] < P.offsets[e];
-    const bool down = __syncthreads_or(descents);
-    if (tid == 0) s_down = down;
+    int falls = 0;
     for (int e = tid; e < P.E; e += blockDim.x) {
         int i0, i1;
-        group_range(P, e, down, i0, i1);
+        falls |= group_range(P, e, i0, i1);
         s_tab[e + 1] = gt_pieces(i1 - i0, Q.tok) * Q.ntiles;
     }
     if (tid == 0) s_tab[0] = 0;
-    __syncthreads();
+    falls = __syncthreads_or(falls);
+    if (falls) gmm_plain<GATED>(P);  // and no tiles; here, where every thread still has the registers of the launch
     if (warp == 0) {
         int base = 0;
         for (int e0 = 0; e0 < P.E; e0 += 32) {
@@ -491,7 +537,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
     gt_cluster_sync();  // both CTAs' barriers and tensor memory are ready
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
-    const int total = s_tab[P.E], first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+    const int total = falls ? 0 : s_tab[P.E], first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
     const uint32_t b_off = NW * kGtAStage;
     volatile int* fail = &s_fail;
 
@@ -512,7 +558,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
         uint32_t phase = 0;
         bool ok = true;
         for (int item = first; item < total && ok; item += step) {
-            const GtTile t = gt_tile(Q, s_tab, s_down, item);
+            const GtTile t = gt_tile(Q, s_tab, item);
             for (int i = 0; i < NB; i++) {
                 const int j = 32 * (SHARE * i + half) + lane;
                 int64_t src, dst;
@@ -593,7 +639,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
             uint32_t phase = 1;  // parity of the stage's last release: nothing to wait for in the first round
             bool ok = true;
             for (int item = first; item < total && ok; item += step) {
-                const GtTile t = gt_tile(Q, s_tab, s_down, item);
+                const GtTile t = gt_tile(Q, s_tab, item);
                 const int half = t.n_mma / 2, row_w = t.e * P.N + t.n0 + (int)rank * kGtM;
                 const int row_a = t.i0 + (int)rank * half;
                 // one box of at least the half's rows: an issued TMA costs more than the rows behind them
@@ -627,7 +673,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
                 uint32_t phase = 0, aphase = 1;
                 bool ok = true;
                 for (int item = first; item < total && ok; item += step) {
-                    const GtTile t = gt_tile(Q, s_tab, s_down, item);
+                    const GtTile t = gt_tile(Q, s_tab, item);
                     const uint32_t idesc = tc_idesc(2 * kGtM, t.n_mma) | (P.type == BITSMOE_BF16 ? (1u << 7) | (1u << 10) : 0u);
                     int left = 0;  // stages left in the segment
                     for (int k = 0; k < Q.nst; k++) {
@@ -698,7 +744,7 @@ __global__ void __launch_bounds__(gt_threads(GATHER, SEG), 1)
             uint32_t phase = 1;
             bool ok = true;
             for (int item = first; item < total && ok; item += step) {
-                const GtTile t = gt_tile(Q, s_tab, s_down, item);
+                const GtTile t = gt_tile(Q, s_tab, item);
                 const int half = t.n_mma / 2;
                 const uint16_t* src_row[RPT];  // NULL: zeros
 #pragma unroll

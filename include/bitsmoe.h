@@ -440,7 +440,8 @@ uint64_t bitsmoe_topk_route_workspace_bytes(int32_t T, int32_t n_experts, int32_
  * (token, slot) pairs grouped by expert.
  * A logit of -inf closes an expert to the token; a slot without an open expert gets id
  * -1, weight 0 and no group.  A row with a NaN or +inf logit gets -1 and 0 in every
- * slot and sets BITSMOE_ST_NONFINITE.  n_experts <= 8192, top_k <= min(n_experts, 1024).
+ * slot and sets BITSMOE_ST_NONFINITE.  n_experts <= 8192, top_k <= min(n_experts, 1024),
+ * tokens top_k <= 2^30.
  * tokens = 0 writes zero offsets. */
 typedef struct {
     const void *logits;  /* dev, rows of n_experts elements of logits_type, logits_stride elements apart */
@@ -546,7 +547,7 @@ typedef struct {
     void *out;              /* dev [n_rows][n_out] */
     int32_t *status;        /* dev or NULL */
     int64_t a_stride;
-    int32_t n_rows;         /* rows the groups may cover: rows of out, entries of `rows` */
+    int32_t n_rows;         /* rows the groups may cover: rows of out, entries of `rows`; <= 2^30 */
     int32_t n_a_rows, n_out; /* n_experts n_out < 2^31 - 256 */
     int32_t n_in;           /* a multiple of 8 */
     int32_t n_experts;      /* <= BITSMOE_GMM_MAX_EXPERTS */
@@ -569,7 +570,7 @@ int bitsmoe_grouped_matmul(const bitsmoe_gmm_args *args, void *stream);
  * becomes infinite); sums are fp32. */
 typedef struct {
     bitsmoe_ffn_dims dims;     /* d_model and d_ff multiples of 8 */
-    int32_t tokens;
+    int32_t tokens;            /* tokens top_k <= 2^30 */
     int32_t type;              /* BITSMOE_F16 or BITSMOE_BF16: x and the matrices */
     const void *x;             /* dev [tokens] rows of d_model elements, x_stride apart (a multiple of 8, >= d_model) */
     const void *W_gate, *W_up; /* dev [E][d_ff][d_model] */

@@ -16,6 +16,8 @@ namespace bitsmoe {
 int launch_combine(const int32_t* ids, const float* gw, float* Ye, float* Ysum, int T, int K, int E, int d_out,
                    cudaStream_t s);
 
+constexpr int kGmmMaxRows = 1 << 30;  // a row's index and a tile of rows behind it are ints
+
 struct GmmParams {
     const uint16_t* a;
     const uint16_t* w;
@@ -847,7 +849,7 @@ using namespace bitsmoe;
 BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* stream) {
     if (!args) return BITSMOE_EINVAL;
     const bitsmoe_gmm_args& d = *args;
-    if (d.n_rows < 0 || d.n_a_rows < 0 || d.n_out < 1 || d.n_in < 8 || d.n_in % 8 || d.n_experts < 1 ||
+    if (d.n_rows < 0 || d.n_rows > kGmmMaxRows || d.n_a_rows < 0 || d.n_out < 1 || d.n_in < 8 || d.n_in % 8 || d.n_experts < 1 ||
         d.n_experts > BITSMOE_GMM_MAX_EXPERTS || (d.in_type != BITSMOE_F16 && d.in_type != BITSMOE_BF16) ||
         (d.out_type != BITSMOE_F32 && d.out_type != d.in_type) || d.rows_per_a < 1 || d.reserved ||
         (int64_t)d.n_experts * d.n_out > 0x7fffffff - 2 * kGtM)  // a tile's last weight row is an int
@@ -892,7 +894,7 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* strea
 // ---------------------------------------------------------------------------
 static bool dense_dims_ok(const bitsmoe_ffn_dims* d, int32_t T) {
     return d && T >= 0 && d->d_model >= 8 && d->d_model % 8 == 0 && d->d_ff >= 8 && d->d_ff % 8 == 0 && d->n_experts >= 1 &&
-           d->n_experts <= BITSMOE_GMM_MAX_EXPERTS && d->top_k >= 1 && (int64_t)T * d->top_k <= 0x7fffffff;
+           d->n_experts <= BITSMOE_GMM_MAX_EXPERTS && d->top_k >= 1 && (int64_t)T * d->top_k <= kGmmMaxRows;
 }
 
 BITSMOE_API uint64_t bitsmoe_dense_ffn_workspace_bytes(const bitsmoe_ffn_dims* dims, int32_t T) {

@@ -39,6 +39,7 @@ constexpr int kRouteOneTokens = 32;
 constexpr int kRouteMaxBlocks = 148;  // CTAs of the two-launch path: one per SM (each sums the others' counts)
 constexpr int kRouteMaxE = 8192;
 constexpr int kRouteMaxK = 1024;
+constexpr int kRouteMaxPairs = 1 << 30;  // T K: pairs are walked by ints in steps of kRtThreads
 constexpr int kRouteBitInts = 8192;   // ints of shared memory for the bits (32 KB), if 32 tokens' fit them
 
 struct RouteParams {
@@ -461,7 +462,7 @@ static int launch_route_kernel(const RouteParams& P, unsigned grid, size_t smem,
 using namespace bitsmoe;
 
 BITSMOE_API uint64_t bitsmoe_topk_route_workspace_bytes(int32_t T, int32_t n_experts, int32_t top_k) {
-    if (T < 1 || n_experts < 1 || n_experts > kRouteMaxE || top_k < 1) return 0;
+    if (T < 1 || n_experts < 1 || n_experts > kRouteMaxE || top_k < 1 || (int64_t)T * top_k > kRouteMaxPairs) return 0;
     const int nb = route_blocks(T);
     return nb == 1 ? 0 : 4ull * nb * n_experts;
 }
@@ -472,7 +473,7 @@ BITSMOE_API int bitsmoe_topk_route(const bitsmoe_route_args* args, void* stream)
     const int T = a.tokens, n_experts = a.n_experts, top_k = a.top_k;
     if (T < 0 || n_experts < 1 || n_experts > kRouteMaxE || top_k < 1 || top_k > n_experts || top_k > kRouteMaxK ||
         !elem_ok(a.logits_type) || (a.scoring != BITSMOE_SCORE_SOFTMAX && a.scoring != BITSMOE_SCORE_SIGMOID) ||
-        (int64_t)T * top_k > 0x7fffffff || a.reserved)
+        (int64_t)T * top_k > kRouteMaxPairs || a.reserved)
         return BITSMOE_EINVAL;
     if (T == 0 && !a.offsets) return BITSMOE_OK;
     if (T > 0 && (!a.logits || !a.topk_ids || !a.gate_w || a.logits_stride < 0)) return BITSMOE_EINVAL;

@@ -425,20 +425,37 @@ def _dense(what: str, name: str, t: torch.Tensor, dtype, shape: tuple, dev: int)
     return t.data_ptr()
 
 
-def _where(what: str, t: torch.Tensor) -> int:
-    dev = t.get_device()
-    if dev < 0:
-        _refuse(what, "the tensors are not on one GPU")
-    return dev
-
-
-def _extra(what: str, t, dev: int) -> int:
-    """Pointer of an optional workspace or status tensor on GPU dev; 0 for None."""
+def _status(what: str, t, dev: int) -> int:
+    """Pointer of an optional status word on GPU dev; 0 for None."""
     if t is None:
         return 0
+    if t.dtype is not torch.int32 or t.numel() < 1:
+        _refuse(what, "status is not an int32 tensor")
     if t.get_device() != dev:
         _refuse(what, "the tensors are not on one GPU")
     return t.data_ptr()
+
+
+def _bytes(what: str, name: str, t, dev: int, need: int = 0) -> int:
+    """Pointer of an optional buffer of at least `need` bytes on GPU dev; 0 for None."""
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        _refuse(what, f"{name} is not contiguous")
+    if t.nbytes < need:
+        raise BitsMoEError(ESIZE, f"{what}: {name} of {t.nbytes} bytes, {need} needed")
+    if t.get_device() != dev:
+        _refuse(what, "the tensors are not on one GPU")
+    return t.data_ptr()
+
+
+def _blob(what: str, t, need: int, dev: int) -> int:
+    """Pointer of packed matrices (uint8, `need` bytes; 0: bad dimensions) on GPU dev."""
+    if need == 0:
+        _refuse(what, "the dimensions or the group (32, 64 or 128) are out of range")
+    if t.dtype is not torch.uint8:
+        _refuse(what, f"blob is {t.dtype}, not uint8")
+    return _bytes(what, "blob", t, dev, need)
 
 
 def _launch(what: str, call, dev: int, stream, *args):
@@ -522,12 +539,12 @@ def topk_route(logits, topk_ids, gate_w, offsets=None, order=None, *, scoring: s
     gw = _dense(what, "gate_w", gate_w, torch.float32, kshape, dev)
     off = 0 if offsets is None else _dense(what, "offsets", offsets, torch.int32, (E + 1,), dev)
     od = 0 if order is None else _dense(what, "order", order, torch.int32, (T * K,), dev)
-    ws = _extra(what, workspace, dev)
+    ws = _bytes(what, "workspace", workspace, dev)
     if dev < 0:
         _refuse(what, "the tensors are not on one GPU")
     _launch(what, lib().bitsmoe_topk_route, dev, stream,
-            _ROUTE.pack(lp, ids, gw, off, od, ws, _extra(what, status, dev), workspace.nbytes if ws else 0, ls, T, E, K, lt,
-                        mode, renormalise, scale, 0))
+            _ROUTE.pack(lp, ids, gw, off, od, ws, _status(what, status, dev), workspace.nbytes if ws else 0, ls, T, E, K,
+                        lt, mode, renormalise, scale, 0))
 
 
 def q4_bytes(n_experts: int, rows: int, cols: int, group: int) -> int:
@@ -543,11 +560,12 @@ def q4_pack(W, group: int, blob, status=None, stream=None):
     n = q4_bytes(E, rows, cols, group)
     if n == 0:
         _refuse(what, f"group {group} is not 32, 64 or 128, or W is empty")
-    if blob.dtype != torch.uint8 or not blob.is_contiguous() or blob.numel() < n:
-        raise BitsMoEError(ESIZE, f"{what}: blob is not {n} contiguous bytes")
-    dev = _where(what, W)
+    dev = W.get_device()
+    _blob(what, blob, n, dev)
+    if dev < 0:
+        _refuse(what, "the tensors are not on one GPU")
     _launch(what, lib().bitsmoe_q4_pack, dev, stream, W.data_ptr(), _TYPE[W.dtype], E, rows, cols, group,
-            _extra(what, blob, dev), _extra(what, status, dev))
+            blob.data_ptr(), _status(what, status, dev))
 
 
 def q4_unpack(blob, group: int, W, stream=None):
@@ -556,12 +574,12 @@ def q4_unpack(blob, group: int, W, stream=None):
     if W.dim() != 3:
         _refuse(what, "W is not [E][rows][cols]")
     E, rows, cols = W.shape
-    n = q4_bytes(E, rows, cols, group)
-    if n == 0 or blob.numel() < n:
-        raise BitsMoEError(ESIZE if n else EINVAL, f"{what}: blob of {blob.numel()} bytes, {n} needed")
-    dev = _where(what, W)
+    dev = W.get_device()
+    bp = _blob(what, blob, q4_bytes(E, rows, cols, group), dev)
     wp = _dense(what, "W", W, torch.float32, (E, rows, cols), dev)
-    _launch(what, lib().bitsmoe_q4_unpack, dev, stream, _extra(what, blob, dev), E, rows, cols, group, wp)
+    if dev < 0:
+        _refuse(what, "the tensors are not on one GPU")
+    _launch(what, lib().bitsmoe_q4_unpack, dev, stream, bp, E, rows, cols, group, wp)
 
 
 def ffn_down_q4_workspace_bytes(dims: FfnDims, group: int, T: int) -> int:
@@ -587,14 +605,13 @@ def ffn_down_q4(dims: FfnDims, blob, group: int, Y_gate, Y_up, topk_ids, gate_w,
     ids = _dense(what, "topk_ids", topk_ids, torch.int32, (T, K), dev)
     gw = _dense(what, "gate_w", gate_w, torch.float32, (T, K), dev)
     op = _dense(what, "out", out, torch.float32, (T, d_model), dev)
-    n = lib().bitsmoe_q4_bytes(E, d_model, d_ff, group)
-    if n == 0 or blob.nbytes < n:
-        raise BitsMoEError(ESIZE if n else EINVAL, f"{what}: blob of {blob.nbytes} bytes, {n} needed")
+    bp = _blob(what, blob, lib().bitsmoe_q4_bytes(E, d_model, d_ff, group), dev)
+    ws = _bytes(what, "workspace", workspace, dev, workspace_bytes)
     if dev < 0:
         _refuse(what, "the tensors are not on one GPU")
     _launch(what, lib().bitsmoe_ffn_down_q4, dev, stream,
-            _Q4.pack(d_model, d_ff, E, K, group, T, blob.data_ptr(), yg, yu, ids, gw, op, _extra(what, workspace, dev),
-                     _extra(what, status, dev), workspace_bytes))
+            _Q4.pack(d_model, d_ff, E, K, group, T, bp, yg, yu, ids, gw, op, ws, _status(what, status, dev),
+                     workspace_bytes))
 
 
 def grouped_matmul(A, W, offsets, out, *, W_up=None, rows=None, rows_per_a: int = 1, scatter: bool = False, status=None,
@@ -624,7 +641,7 @@ def grouped_matmul(A, W, offsets, out, *, W_up=None, rows=None, rows_per_a: int 
     if dev < 0:
         _refuse(what, "the tensors are not on one GPU")
     _launch(what, lib().bitsmoe_grouped_matmul, dev, stream,
-            _GMM.pack(ap, wp, up, off, rp, op, _extra(what, status, dev), lda, n, ashape[0], N, K, E, it, ot, rows_per_a,
+            _GMM.pack(ap, wp, up, off, rp, op, _status(what, status, dev), lda, n, ashape[0], N, K, E, it, ot, rows_per_a,
                       scatter, 0))
 
 
@@ -649,11 +666,11 @@ def dense_ffn_forward(dims: FfnDims, w_gate, w_up, w_down, x, topk_ids, gate_w, 
     off = _dense(what, "offsets", offsets, torch.int32, (E + 1,), dev)
     od = _dense(what, "order", order, torch.int32, (T * K,), dev)
     op = _dense(what, "out", out, torch.float32, (T, d_model), dev)
-    ws = _extra(what, workspace, dev)
+    ws = _bytes(what, "workspace", workspace, dev)
     if dev < 0:
         _refuse(what, "the tensors are not on one GPU")
     _launch(what, lib().bitsmoe_dense_ffn_forward, dev, stream,
-            _DENSE.pack(d_model, d_ff, E, K, T, kind, xp, wg, wu, wd, ids, gw, off, od, op, ws, _extra(what, status, dev),
+            _DENSE.pack(d_model, d_ff, E, K, T, kind, xp, wg, wu, wd, ids, gw, off, od, op, ws, _status(what, status, dev),
                         workspace.nbytes if ws else 0, xs if T > 1 else d_model))
 
 

@@ -26,6 +26,15 @@ def _on(stream, like: torch.Tensor):
     return _HERE if dev < 0 or dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
+def _workspace(kept: dict, T: int, n: int, device) -> torch.Tensor:
+    """n bytes for a call of T tokens; one token's are zeros at first and stay in `kept`."""
+    if T != 1:
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    if T not in kept:
+        kept[T] = torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+    return kept[T]
+
+
 class PackedProjection:
     """One projection (gate or up) of a spectral MoE layer, packed on the GPU.
 
@@ -117,7 +126,10 @@ def fqcm_widths(dec: dict, x_calib: torch.Tensor, ids_calib: torch.Tensor, gw_ca
 
 
 class SpectralMoELayer:
-    """Gate and up projections of one MoE layer in shared-spectral form."""
+    """Gate and up projections of one MoE layer in shared-spectral form.
+
+    Calls for one token keep state in the object between them: they must not overlap on
+    the GPU, whatever their streams, nor may replays of graphs captured from them."""
 
     def __init__(self, gate: PackedProjection, up: PackedProjection):
         assert gate.d_in == up.d_in and gate.top_k == up.top_k and gate.n_experts == up.n_experts
@@ -126,15 +138,10 @@ class SpectralMoELayer:
         self._ios = {}
 
     def workspace(self, T: int) -> torch.Tensor:
-        """The layer's workspace for T tokens, allocated on first use.  The plans
-        are immutable, so its size for a given T never changes."""
-        ws = self._ws.get(T)
-        if ws is None:
-            n = B.layer_workspace_bytes(self.gate.plan, self.up.plan, T)
-            # zero-filled once: its head keeps the fused path's counters between calls
-            ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.gate.blob.device)
-            self._ws[T] = ws
-        return ws
+        """A workspace for a call of T tokens.  One token's is the layer's own, made and
+        zero-filled on first use: its head keeps the fused path's counters between calls.
+        Any other T uses nothing that an earlier call left and gets a new one."""
+        return _workspace(self._ws, T, B.layer_workspace_bytes(self.gate.plan, self.up.plan, T), self.gate.blob.device)
 
     def _proj_ios(self, out: dict) -> tuple:
         """The two projections' I/O descriptors for these output buffers, reused
@@ -212,7 +219,8 @@ class SpectralMoEFFN:
     dense fp16 down matrices, the layer call and bitsmoe_ffn_down_q4 with 4-bit ones.
 
     w_down [E][d_model][d_ff] fp16 on the GPU, or a Q4Down of that shape; d_model = the
-    layer's d_in and d_ff = the gate/up d_out."""
+    layer's d_in and d_ff = the gate/up d_out.  Calls for one token must not overlap on the
+    GPU (see SpectralMoELayer)."""
 
     def __init__(self, layer: SpectralMoELayer, w_down: "torch.Tensor | Q4Down"):
         g = layer.gate
@@ -227,17 +235,13 @@ class SpectralMoEFFN:
         self._ws = {}
 
     def workspace(self, T: int) -> torch.Tensor:
-        """The call's workspace for T tokens (the layer's, then the down step's),
-        zero-filled once on first use: its head keeps the fused path's counters."""
-        ws = self._ws.get(T)
-        if ws is None:
-            if self.q4 is None:
-                n = B.ffn_workspace_bytes(self.layer.gate.plan, self.layer.up.plan, T)
-            else:  # the down step's alone: the layer keeps its own
-                n = B.ffn_down_q4_workspace_bytes(self.dims, self.q4.group, T)
-            ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.layer.gate.blob.device)
-            self._ws[T] = ws
-        return ws
+        """A workspace for a call of T tokens: with fp16 down matrices the layer's, then
+        the down step's, one token's kept as SpectralMoELayer.workspace has it; with 4-bit
+        ones the down step's alone, which keeps nothing between calls."""
+        dev = self.layer.gate.blob.device
+        if self.q4 is not None:
+            return torch.empty(B.ffn_down_q4_workspace_bytes(self.dims, self.q4.group, T), dtype=torch.uint8, device=dev)
+        return _workspace(self._ws, T, B.ffn_workspace_bytes(self.layer.gate.plan, self.layer.up.plan, T), dev)
 
     def launches(self, T: int) -> int:
         """Kernels one forward launches for T tokens (the layer's, then the down step's)."""

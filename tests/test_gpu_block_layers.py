@@ -159,3 +159,30 @@ def test_single_token_step_right_behind_its_routing(kind):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [2, 33, 150])
+@pytest.mark.parametrize("kind", ["fp16", "q4", "layer"])
+def test_overlapping_calls_of_one_object(kind, T):
+    """Two streams call one object at the same T, again and again, with other inputs: each gets what it gets alone."""
+    ffn = _spectral("q4" if kind == "q4" else "fp16", 92)
+    obj = ffn.layer if kind == "layer" else ffn
+    d, E, K = ffn.dims.d_model, ffn.dims.n_experts, ffn.dims.top_k
+    sets = []
+    for i in range(2):
+        g = _gen(7 * T + i)
+        x, gw = _randn(g, T, d).half(), torch.rand((T, K), generator=g, device="cuda")
+        ids = torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :K].to(torch.int32).contiguous()
+        sets.append((x, ids, gw))
+    leaf = (lambda y: y["Y_sum_gate"]) if kind == "layer" else (lambda y: y)
+    want = [leaf(obj.forward(*s)).clone() for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(sets):
+            got[i].append(leaf(obj.forward(*s, stream=streams[i])))
+    torch.cuda.synchronize()
+    for w, ys in zip(want, got):
+        for y in ys:
+            assert torch.equal(y, w)

@@ -846,9 +846,7 @@ static int launch_gmm_seg(const GmmParams& P, cudaStream_t s) {
 
 using namespace bitsmoe;
 
-BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* stream) {
-    if (!args) return BITSMOE_EINVAL;
-    const bitsmoe_gmm_args& d = *args;
+static int gmm_refusal(const bitsmoe_gmm_args& d) {
     if (d.n_rows < 0 || d.n_rows > kGmmMaxRows || d.n_a_rows < 0 || d.n_out < 1 || d.n_in < 8 || d.n_in % 8 || d.n_experts < 1 ||
         d.n_experts > BITSMOE_GMM_MAX_EXPERTS || (d.in_type != BITSMOE_F16 && d.in_type != BITSMOE_BF16) ||
         (d.out_type != BITSMOE_F32 && d.out_type != d.in_type) || d.rows_per_a < 1 || d.reserved ||
@@ -860,6 +858,10 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* strea
     if ((uintptr_t)d.A % 16 || (uintptr_t)d.W % 16 || (uintptr_t)d.W_up % 16 || (uintptr_t)d.offsets % 4 ||
         (uintptr_t)d.rows % 4 || (uintptr_t)d.out % elem_bytes(d.out_type))
         return BITSMOE_EINVAL;
+    return BITSMOE_OK;
+}
+
+static int launch_gmm(const bitsmoe_gmm_args& d, void* stream) {
     GmmParams P{};
     P.a = (const uint16_t*)d.A;
     P.w = (const uint16_t*)d.W;
@@ -887,6 +889,12 @@ BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* strea
     }
     if (d.in_type == BITSMOE_BF16) return d.W_up ? launch_gmm_mv<true, true>(P, s) : launch_gmm_mv<true, false>(P, s);
     return d.W_up ? launch_gmm_mv<false, true>(P, s) : launch_gmm_mv<false, false>(P, s);
+}
+
+BITSMOE_API int bitsmoe_grouped_matmul(const bitsmoe_gmm_args* args, void* stream) {
+    if (!args) return BITSMOE_EINVAL;
+    const int rc = gmm_refusal(*args);
+    return rc || args->n_rows == 0 ? rc : launch_gmm(*args, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -935,19 +943,21 @@ BITSMOE_API int bitsmoe_dense_ffn_forward(const bitsmoe_dense_ffn_args* args, vo
     g.in_type = g.out_type = a.type;
     g.rows_per_a = d.top_k;
     g.scatter = 1;
-    int rc = bitsmoe_grouped_matmul(&g, stream);
-    if (rc) return rc;
-    g.A = h;
-    g.W = a.W_down;
-    g.W_up = nullptr;
-    g.out = y;
-    g.a_stride = d.d_ff;
-    g.n_a_rows = pairs;
-    g.n_out = d.d_model;
-    g.n_in = d.d_ff;
-    g.out_type = BITSMOE_F32;
-    g.rows_per_a = 1;
-    rc = bitsmoe_grouped_matmul(&g, stream);
+    bitsmoe_gmm_args down = g;
+    down.A = h;
+    down.W = a.W_down;
+    down.W_up = nullptr;
+    down.out = y;
+    down.a_stride = d.d_ff;
+    down.n_a_rows = pairs;
+    down.n_out = d.d_model;
+    down.n_in = d.d_ff;
+    down.out_type = BITSMOE_F32;
+    down.rows_per_a = 1;
+    int rc = gmm_refusal(g);
+    if (!rc) rc = gmm_refusal(down);  // before the first launch
+    if (!rc) rc = launch_gmm(g, stream);
+    if (!rc) rc = launch_gmm(down, stream);
     if (rc) return rc;
     return launch_combine(a.topk_ids, a.gate_w, y, a.out, a.tokens, d.top_k, d.n_experts, d.d_model, (cudaStream_t)stream);
 }

@@ -1,4 +1,5 @@
-"""Sizes whose index arithmetic would leave 32 bits are refused before any launch (no GPU needed)."""
+"""Sizes whose index arithmetic would leave 32 bits, and operands of a later launch, are refused before any launch (no
+GPU needed)."""
 import struct
 
 import pytest
@@ -33,3 +34,12 @@ def test_dense_ffn_of_more_than_2_30_pairs(B, T, K):
 def test_grouped_product_of_more_than_2_30_rows(B, n):
     args = struct.pack("@7Pq10i", 256, 512, 0, 1024, 2048, 4096, 0, 16, n, n, 8, 16, 2, 1, 1, 1, 0, 0)
     assert B.lib().bitsmoe_grouped_matmul(args, None) == B.EINVAL
+
+
+@pytest.mark.parametrize("bad", [dict(wd=264), dict(d_model=1 << 20, E=4096)])
+def test_dense_ffn_refuses_the_down_product_before_the_first_launch(B, bad):
+    """A misaligned W_down, or more rows of it than a tensor map counts, is refused as such: not after the gate and up
+    products were launched (which here, without a GPU, would answer with a CUDA error)."""
+    ok = dict(d_model=64, d_ff=32, E=4, K=2, tokens=3, type=1, x=256, wg=256, wu=256, wd=256, ids=256, gw=256, off=256,
+              od=256, out=256, ws=512, st=0, nb=1 << 60, xs=1 << 20)
+    assert B.lib().bitsmoe_dense_ffn_forward(struct.pack("@6i11PQq", *{**ok, **bad}.values()), None) == B.EINVAL

@@ -8,6 +8,7 @@ library is missing the import of any call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -547,6 +548,7 @@ def topk_route(logits, topk_ids, gate_w, offsets=None, order=None, *, scoring: s
                         lt, mode, renormalise, scale, 0))
 
 
+@functools.lru_cache(maxsize=256)  # a call of the library took 0.8 us of every step's
 def q4_bytes(n_experts: int, rows: int, cols: int, group: int) -> int:
     return int(lib().bitsmoe_q4_bytes(n_experts, rows, cols, group))
 
@@ -605,7 +607,7 @@ def ffn_down_q4(dims: FfnDims, blob, group: int, Y_gate, Y_up, topk_ids, gate_w,
     ids = _dense(what, "topk_ids", topk_ids, torch.int32, (T, K), dev)
     gw = _dense(what, "gate_w", gate_w, torch.float32, (T, K), dev)
     op = _dense(what, "out", out, torch.float32, (T, d_model), dev)
-    bp = _blob(what, blob, lib().bitsmoe_q4_bytes(E, d_model, d_ff, group), dev)
+    bp = _blob(what, blob, q4_bytes(E, d_model, d_ff, group), dev)
     ws = _bytes(what, "workspace", workspace, dev, workspace_bytes)
     if dev < 0:
         _refuse(what, "the tensors are not on one GPU")

@@ -36,21 +36,6 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-template <bool F16>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float2 f = unpack2<F16>(u[j]);
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-    }
-}
-template <bool F16>
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]), pack2<F16>(v[4], v[5]), pack2<F16>(v[6], v[7]));
-}
-
 __device__ __forceinline__ void unpack4(uint2 w, int type, float (&v)[4]) {
     const float2 a = type == BITSMOE_F16 ? unpack2<true>(w.x) : unpack2<false>(w.x);
     const float2 b = type == BITSMOE_F16 ? unpack2<true>(w.y) : unpack2<false>(w.y);
@@ -78,50 +63,22 @@ __device__ __forceinline__ void store4(void* p, int type, int64_t i, const float
     }
 }
 
-// V elements (8: 16-byte aligned; 1: any) from element i of p.
+// V neighbouring elements, one by one, from element i of p on.
 template <int V>
 __device__ __forceinline__ void load_elems(const void* p, int type, int64_t i, float (&v)[V]) {
-    if constexpr (V == 8) {
-        if (type == BITSMOE_F32) {
-            const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-            const float4 a = f[0], b = f[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-            if (type == BITSMOE_F16)
-                unpack8<true>(w, v);
-            else
-                unpack8<false>(w, v);
-        }
-    } else {
 #pragma unroll
-        for (int j = 0; j < V; j++)
-            v[j] = type == BITSMOE_F32 ? static_cast<const float*>(p)[i + j]
-                                       : half_bits(static_cast<const uint16_t*>(p)[i + j], type);
-    }
+    for (int j = 0; j < V; j++)
+        v[j] = type == BITSMOE_F32 ? static_cast<const float*>(p)[i + j]
+                                   : half_bits(static_cast<const uint16_t*>(p)[i + j], type);
 }
-
 template <int V>
 __device__ __forceinline__ void store_elems(void* p, int type, int64_t i, const float (&v)[V]) {
-    if constexpr (V == 8) {
-        if (type == BITSMOE_F32) {
-            float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-            f[0] = make_float4(v[0], v[1], v[2], v[3]);
-            f[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else if (type == BITSMOE_F16) {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack8<true>(v);
-        } else {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack8<false>(v);
-        }
-    } else {
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            if (type == BITSMOE_F32)
-                static_cast<float*>(p)[i + j] = v[j];
-            else
-                static_cast<uint16_t*>(p)[i + j] = (uint16_t)to_half_bits(v[j], type);
-        }
+    for (int j = 0; j < V; j++) {
+        if (type == BITSMOE_F32)
+            static_cast<float*>(p)[i + j] = v[j];
+        else
+            static_cast<uint16_t*>(p)[i + j] = (uint16_t)to_half_bits(v[j], type);
     }
 }
 

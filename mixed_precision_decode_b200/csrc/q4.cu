@@ -182,14 +182,21 @@ __device__ __forceinline__ void q4_mma_zero(int (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
 }
 
-// SiLU(yg) * yu of 8 values (yu NULL: yg itself).
+// SiLU(yg) * yu of 8 values, 16-byte aligned (yu NULL: yg itself).
 __device__ __forceinline__ void q4_h8(const float* yg, const float* yu, int64_t i, float (&h)[8]) {
-    load_elems<8>(yg, BITSMOE_F32, i, h);
-    if (!yu) return;
-    float u[8];
-    load_elems<8>(yu, BITSMOE_F32, i, u);
+    float lo[4], hi[4];
+    load4<true>(yg, BITSMOE_F32, i, lo);
+    load4<true>(yg, BITSMOE_F32, i + 4, hi);
 #pragma unroll
-    for (int j = 0; j < 8; j++) h[j] = silu_f(h[j]) * u[j];
+    for (int j = 0; j < 4; j++) {
+        h[j] = lo[j];
+        h[4 + j] = hi[j];
+    }
+    if (!yu) return;
+    load4<true>(yu, BITSMOE_F32, i, lo);
+    load4<true>(yu, BITSMOE_F32, i + 4, hi);
+#pragma unroll
+    for (int j = 0; j < 8; j++) h[j] = silu_f(h[j]) * (j < 4 ? lo[j] : hi[j - 4]);
 }
 
 // The exponent e of a power of two above a row's largest |h| (m): |h| 2^(30 - e) < 2^30.

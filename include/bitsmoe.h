@@ -439,7 +439,9 @@ uint64_t bitsmoe_topk_route_workspace_bytes(int32_t T, int32_t n_experts, int32_
 /* The top_k experts of every token from its router logits, their gate weights, and the
  * (token, slot) pairs grouped by expert.
  * A logit of -inf closes an expert to the token; a slot without an open expert gets id
- * -1, weight 0 and no group.  A row with a NaN or +inf logit gets -1 and 0 in every
+ * -1, weight 0 and no group.  (bitsmoe_dense_ffn_forward passes over such a slot; the
+ * steps that go by the ids alone -- the spectral layer, bitsmoe_ffn_down and
+ * bitsmoe_ffn_down_q4 -- leave it out too, and report it as BITSMOE_ST_BADEXPERT.)  A row with a NaN or +inf logit gets -1 and 0 in every
  * slot and sets BITSMOE_ST_NONFINITE.  n_experts <= 8192, top_k <= min(n_experts, 1024),
  * tokens top_k <= 2^30.
  * tokens = 0 writes zero offsets. */

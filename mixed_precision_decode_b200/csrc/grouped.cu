@@ -268,10 +268,15 @@ static int launch_gmm_mv(const GmmParams& P, cudaStream_t s) {
 // The number of tiles is known on the device alone: every CTA derives it from offsets.
 //
 // Bound by the weights' bytes up to a few hundred rows per expert, then by the tensor
-// pipe.  128 experts, 2048 -> 768 gated, gathered: 128 pairs 81 us (510 MB, 6.3 TB/s), 16,384
-// pairs 153 us (870 MB, 5.7 TB/s, the tensor pipe 40% busy); 768 -> 2048 with fp32 results,
-// 16,384 pairs 104 us; 8 experts, 4096 -> 14336, 2,050 pairs 232 us (1.04 PFLOP/s, the pipe
-// 69% busy) before the power limit lowers the clocks.  Tiles of one expert stand together:
+// pipe.  A few calls / a loop of seconds, in which the board's power limit lowers the clocks:
+// 128 experts, 2048 -> 768 gated, gathered, 128 pairs 81 us (510 MB, 6.3 TB/s), 16,384 pairs
+// 153 / 181 us (870 MB, 5.7 / 4.8 TB/s, the tensor pipe 40% busy; 1.24 GHz in the loop);
+// 768 -> 2048 with fp32 results, 16,384 pairs 107 / 122 us (1.59 GHz); 8 experts, 4096 ->
+// 14336, 2,050 pairs 232 to 250 / 298 us (1.04 to 0.96 / 0.81 PFLOP/s; 1.07 GHz).  The clocks are
+// not all of the last: it does 0.70 to 0.76 TFLOP/s per MHz, the library's dense product of
+// 8192^3 1.04, and no unit is full (tensor pipe 68%, L2 45%, DRAM 55%).  Likely the weights'
+// path from L2: the pieces of one expert load the same weight tiles, each for itself.
+// Tiles of one expert stand together:
 // walking them by block of weight rows over all experts was 2 to 5% slower.
 constexpr int kGtM = 128;                        // weight rows per CTA and matrix
 constexpr int kGtK = 64;                         // K per stage: one 128-byte swizzled row

@@ -20,8 +20,9 @@
 // conversions behind them (under a branch per chunk 8,192 rows of 4,096 took 66 us
 // instead of 61.5, 4,096 rows of 8,192 107 instead of 53); h kept in 16 bits until it is
 // needed, which leaves registers for a fifth row; element widths fixed when the kernel is
-// built.  8,192 x 4,096, bf16 h and x, fp32 y, both norms and a gate per channel: 57.5 us,
-// 5.8 TB/s, 90% of a plain copy's rate.  Slower were two rows a CTA (83 us), loads through
+// built.  8,192 x 4,096, bf16 h and x, fp32 y, both norms and a gate per channel: 57.5 us in a
+// single launch (5.8 TB/s, 90% of a plain copy's rate), 62 (84%) in a loop, where the board's
+// power limit holds the SMs near 1.69 GHz.  Slower were two rows a CTA (83 us), loads through
 // a ring in shared memory by persistent CTAs (73 to 124, by its depth) and the channel
 // vectors held in registers (86 and more): they hold fewer rows, or leave the L1 cache
 // too small for the vectors.
@@ -249,7 +250,8 @@ __global__ void __launch_bounds__(WARP ? 256 : NC > 0 ? norm_threads(V, NC) : 10
 
 // Rows that start anywhere: groups of 4 elements on their natural boundary all the same, the first of which may begin
 // q = 1 to 3 elements before the row and the last end behind it; those two go element by element, and nothing outside
-// the row is read or written.  A CTA per row.
+// the row is read or written.  A CTA per row.  Bound by L1 (72% busy): the channel vectors, which start on no boundary
+// of these groups, come as single floats.
 // (Against one element per load, us: 4,000 rows x 1,999 in bf16 22.4 and 46.5, 868 x 3,251 11.9 and 18.5, 583 x 1,281 4.2
 // and 5.1; but 1,000 x 300 3.7 and 3.5, 1 x 3,251 3.7 and 3.5, 8,192 x 20 12.2 and 2.5.)
 constexpr int kShiftChunks = 4, kShiftThreads = 256, kShiftMinCols = 1024, kShiftMinRows = 128;

@@ -398,7 +398,10 @@ __device__ __forceinline__ void q4_t1_batch(const Q4Tiles<G, U>& tiles, const ui
 
 template <int G>
 __global__ void __launch_bounds__(32 * kQ4T1Warps) k_q4_t1(const Q4Params P) {
-    constexpr int U = 6, V = G > kQ4Cols ? 2 : 1;  // tiles per batch, and per step of what is left
+    // Tiles per batch, and per step of what is left.  (8 slots, 2048 rows, G = 64, batches of 2, 4, 6, 8, us: 512
+    // columns 6.40, 6.46, 6.36, 6.37; 768 columns 7.28, 7.20, 7.01, 7.19; 1,024 columns 8.12, 7.71, 7.90, 7.71; 1,408
+    // columns 11.9, 11.2, 11.1, 11.0: 6 is within 0.2 us of the best at each.)
+    constexpr int U = 6, V = G > kQ4Cols ? 2 : 1;
     extern __shared__ __align__(16) uint32_t s_h[];  // [K][tiles][4][16], then [K][groups][2], [row blocks][unit][16], ids, weights
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int ntiles = P.M.cols_p / kQ4Cols, nblk = P.M.nblk;
@@ -711,7 +714,7 @@ __global__ void __launch_bounds__(THREADS) k_q4_prep(const Q4Params P) {
 // its own in shared memory, filled by bulk copies of up to 12 tiles, a stage ahead and
 // across the borders of units (without the products this reads at HBM's rate).  Results go
 // from registers to memory, a row of y per pair and range; no CTA barrier is met.
-// 64 tokens, 128 experts, 2048 x 768, top 8: about 32 us of the step's 42 (108 MB); 56% of
+// 64 tokens, 128 experts, 2048 x 768, top 8: about 32 us of the step's 43 (108 MB); 48% of
 // the issue slots are used, most by unpacking and scaling, the MMAs take 11 us.
 constexpr int kQ4Warps = 8;
 constexpr int kQ4Threads = 32 * kQ4Warps;

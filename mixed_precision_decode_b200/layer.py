@@ -10,7 +10,6 @@ import torch
 
 from . import bitsmoe as B
 
-
 _HERE = contextlib.nullcontext()
 
 
@@ -337,7 +336,9 @@ class MoEBlock:
     finish.  w_post and alpha belong to the block that made y: the next block is told which
     one that is (made_by).  w_norm, w_post [d_model] f32, w_router [E][d_model] fp16; ffn a
     SpectralMoEFFN or an fp16 DenseMoEFFN; gate, of that y, f32 [T or 1][d_model or 1], None
-    without a y.  eps is that of the norms in this block's calls."""
+    without a y.  eps is that of the norms in this block's calls.  A token with fewer than
+    top_k open experts (logits of -inf) leaves its other slots out; over a SpectralMoEFFN
+    status then holds ST_BADEXPERT, over a DenseMoEFFN it does not."""
 
     def __init__(self, ffn: "SpectralMoEFFN | DenseMoEFFN", w_norm: torch.Tensor, w_router: torch.Tensor,
                  w_post: torch.Tensor | None = None, alpha: float = 1.0, eps: float = 1e-6, scoring: str = "softmax",

@@ -4,6 +4,7 @@ and streams; every computation is a libbitsmoe kernel."""
 from __future__ import annotations
 
 import contextlib
+import functools
 import warnings
 
 import torch
@@ -11,6 +12,7 @@ import torch
 from . import bitsmoe as B
 
 _HERE = contextlib.nullcontext()
+_current_gpu = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else lambda: -1
 
 
 def _on(stream, like: torch.Tensor):
@@ -22,16 +24,29 @@ def _on(stream, like: torch.Tensor):
     dev = like.get_device()
     if stream is not None:
         return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev))
-    return _HERE if dev < 0 or dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    return _HERE if dev < 0 or dev == _current_gpu() else torch.cuda.device(dev)
 
 
-def _workspace(kept: dict, T: int, n: int, device) -> torch.Tensor:
-    """n bytes for a call of T tokens; one token's are zeros at first and stay in `kept`."""
-    if T != 1:
-        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
-    if T not in kept:
-        kept[T] = torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
-    return kept[T]
+class _Workspaces:
+    """Workspaces of size(T) bytes for an object's calls of T tokens."""
+
+    def __init__(self, size, device, keep_one: bool):
+        self._size, self._device, self._keep_one = size, device, keep_one
+        self._bytes = {}   # of the last T's: asking the library costs a microsecond
+        self.one = None    # one token's, when it is kept
+
+    def get(self, T: int) -> torch.Tensor:
+        if T == 1 and self.one is not None:
+            return self.one
+        n = self._bytes.get(T)
+        if n is None:
+            if len(self._bytes) >= 64:
+                self._bytes.clear()
+            n = self._bytes[T] = max(self._size(T), 256)
+        if T != 1 or not self._keep_one:
+            return torch.empty(n, dtype=torch.uint8, device=self._device)
+        self.one = torch.zeros(n, dtype=torch.uint8, device=self._device)
+        return self.one
 
 
 class PackedProjection:
@@ -133,21 +148,21 @@ class SpectralMoELayer:
     def __init__(self, gate: PackedProjection, up: PackedProjection):
         assert gate.d_in == up.d_in and gate.top_k == up.top_k and gate.n_experts == up.n_experts
         self.gate, self.up = gate, up
-        self._ws = {}
+        self._ws = _Workspaces(lambda T: B.layer_workspace_bytes(gate.plan, up.plan, T), gate.blob.device, True)
         self._ios = {}
 
     def workspace(self, T: int) -> torch.Tensor:
         """A workspace for a call of T tokens.  One token's is the layer's own, made and
         zero-filled on first use: its head keeps the fused path's counters between calls.
         Any other T uses nothing that an earlier call left and gets a new one."""
-        return _workspace(self._ws, T, B.layer_workspace_bytes(self.gate.plan, self.up.plan, T), self.gate.blob.device)
+        return self._ws.get(T)
 
     def _proj_ios(self, out: dict) -> tuple:
         """The two projections' I/O descriptors for these output buffers, reused
         while a caller keeps passing the same buffers (a decode loop)."""
-        key = tuple(None if t is None else t.data_ptr()
-                    for t in (out["Y_sum_gate"], out["Y_sum_up"], out.get("Z_gate"), out.get("Z_up"),
-                              out.get("Y_experts_gate"), out.get("Y_experts_up")))
+        zg, zu, yg, yu = out.get("Z_gate"), out.get("Z_up"), out.get("Y_experts_gate"), out.get("Y_experts_up")
+        key = (out["Y_sum_gate"].data_ptr(), out["Y_sum_up"].data_ptr(), zg is not None and zg.data_ptr(),
+               zu is not None and zu.data_ptr(), yg is not None and yg.data_ptr(), yu is not None and yu.data_ptr())
         ios = self._ios.get(key)
         if ios is None:
             ios = tuple(B.proj_io(p.plan, p.blob, p.phi_t, out[f"Y_sum_{name}"], out.get(f"Z_{name}"),
@@ -176,14 +191,16 @@ class SpectralMoELayer:
                         out[f"Y_experts_{name}"] = torch.empty((T, p.top_k, p.d_out), dtype=torch.float32, device=dev)
                     if want_z:
                         out[f"Z_{name}"] = torch.empty((T, p.rank), dtype=torch.float32, device=dev)
-            ios = self._proj_ios(out)
-            ws = self.workspace(T)
-            if next_layer is None:
-                B.layer_forward(ios[0], ios[1], x, topk_ids, gate_w, T, ws, ws.numel(), status, stream)
-            else:
-                B.layer_forward_chained(ios[0], ios[1], x, topk_ids, gate_w, T, ws, ws.numel(), next_layer.gate.phi_t,
-                                        next_layer.up.phi_t, status, stream)
+            self._run(x, topk_ids, gate_w, T, out, self._ws.get(T), status, stream, next_layer)
         return out
+
+    def _run(self, x, topk_ids, gate_w, T: int, out: dict, ws, status, stream, next_layer=None):
+        ios = self._proj_ios(out)
+        if next_layer is None:
+            B.layer_forward(ios[0], ios[1], x, topk_ids, gate_w, T, ws, ws.numel(), status, stream)
+        else:
+            B.layer_forward_chained(ios[0], ios[1], x, topk_ids, gate_w, T, ws, ws.numel(), next_layer.gate.phi_t,
+                                    next_layer.up.phi_t, status, stream)
 
 
 class Q4Down:
@@ -231,16 +248,21 @@ class SpectralMoEFFN:
             assert w_down.dtype == torch.float16
             self.w_down = w_down.contiguous()
         self.dims = B.ffn_dims(g.d_in, g.d_out, g.n_experts, g.top_k)
-        self._ws = {}
+        if self.q4 is None:
+            self._ws = _Workspaces(lambda T: B.ffn_workspace_bytes(g.plan, layer.up.plan, T), g.blob.device, True)
+        else:
+            self._q4_bytes = functools.lru_cache(64)(
+                lambda T: B.ffn_down_q4_workspace_bytes(self.dims, self.q4.group, T))
+            # the layer's is free again where the down step starts; one token's is the layer's own, and stays apart
+            self._ws = _Workspaces(
+                lambda T: max(self._q4_bytes(T), 0 if T == 1 else B.layer_workspace_bytes(g.plan, layer.up.plan, T)),
+                g.blob.device, False)
 
     def workspace(self, T: int) -> torch.Tensor:
         """A workspace for a call of T tokens: with fp16 down matrices the layer's, then
         the down step's, one token's kept as SpectralMoELayer.workspace has it; with 4-bit
-        ones the down step's alone, which keeps nothing between calls."""
-        dev = self.layer.gate.blob.device
-        if self.q4 is not None:
-            return torch.empty(B.ffn_down_q4_workspace_bytes(self.dims, self.q4.group, T), dtype=torch.uint8, device=dev)
-        return _workspace(self._ws, T, B.ffn_workspace_bytes(self.layer.gate.plan, self.layer.up.plan, T), dev)
+        ones enough for either step, which keeps nothing between calls."""
+        return self._ws.get(T)
 
     def launches(self, T: int) -> int:
         """Kernels one forward launches for T tokens (the layer's, then the down step's)."""
@@ -267,12 +289,14 @@ class SpectralMoEFFN:
                 out = torch.empty((T, self.dims.d_model), dtype=torch.float32, device=x.device)
             if gate_up is None:
                 gate_up = self.gate_up_buffers(T, x.device)
-            ws = self.workspace(T)
             if self.q4 is not None:
-                self.layer.forward(x, topk_ids, gate_w, out=gate_up, status=status, stream=stream)
+                n = self._q4_bytes(T)
+                ws = self._ws.get(T) if T != 1 or n else None
+                self.layer._run(x, topk_ids, gate_w, T, gate_up, self.layer._ws.get(1) if T == 1 else ws, status, stream)
                 B.ffn_down_q4(self.dims, self.q4.blob, self.q4.group, gate_up["Y_experts_gate"], gate_up["Y_experts_up"],
-                              topk_ids, gate_w, T, out, ws, ws.numel(), status, stream)
+                              topk_ids, gate_w, T, out, ws, n, status, stream)
             else:
+                ws = self._ws.get(T)
                 ios = self.layer._proj_ios(gate_up)
                 B.ffn_forward(ios[0], ios[1], self.w_down, x, topk_ids, gate_w, T, out, ws, ws.numel(), status, stream)
         return out

@@ -30,7 +30,7 @@ def current(monkeypatch):
         yield
         now[:] = before
 
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(L, "_current_gpu", lambda: now[0])
     monkeypatch.setattr(torch.cuda, "device", lambda dev: entered(int(dev), None))
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: (0 if device is None else device, h))
     monkeypatch.setattr(torch.cuda, "stream", lambda s: entered(*s))

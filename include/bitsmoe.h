@@ -410,7 +410,7 @@ int bitsmoe_allocate_widths(const float *amps_host, const double *beta_host, con
  *   x  = h' rsqrt(mean(h'^2) + eps) w_pre
  * in fp32, each output rounded once to its type (x is formed from the fp32 h').  Rows of
  * an output must not overlap each other or another operand (h_out = h apart).
- * Any width and stride; rows on 16-byte boundaries with d a multiple of 8 are read and
+ * Any width up to 2^30 and any stride; rows on 16-byte boundaries with d a multiple of 8 are read and
  * written 16 bytes at a time.  rows = 0 is a no-op. */
 typedef struct {
     const void *h;         /* dev, rows of d elements of h_type, h_stride elements apart */
@@ -551,7 +551,7 @@ typedef struct {
     int64_t a_stride;
     int32_t n_rows;         /* rows the groups may cover: rows of out, entries of `rows`; <= 2^30 */
     int32_t n_a_rows, n_out; /* n_experts n_out < 2^31 - 256 */
-    int32_t n_in;           /* a multiple of 8 */
+    int32_t n_in;           /* a multiple of 8, <= 2^30 */
     int32_t n_experts;      /* <= BITSMOE_GMM_MAX_EXPERTS */
     int32_t in_type;        /* BITSMOE_F16 or BITSMOE_BF16: A, W and W_up */
     int32_t out_type;       /* in_type or BITSMOE_F32 */

@@ -17,6 +17,7 @@ int launch_combine(const int32_t* ids, const float* gw, float* Ye, float* Ysum, 
                    cudaStream_t s);
 
 constexpr int kGmmMaxRows = 1 << 30;  // a row's index and a tile of rows behind it are ints
+constexpr int kGmmMaxIn = 1 << 30;    // so are a k and a step of all warps behind it
 
 struct GmmParams {
     const uint16_t* a;
@@ -852,7 +853,7 @@ static int launch_gmm_seg(const GmmParams& P, cudaStream_t s) {
 using namespace bitsmoe;
 
 static int gmm_refusal(const bitsmoe_gmm_args& d) {
-    if (d.n_rows < 0 || d.n_rows > kGmmMaxRows || d.n_a_rows < 0 || d.n_out < 1 || d.n_in < 8 || d.n_in % 8 || d.n_experts < 1 ||
+    if (d.n_rows < 0 || d.n_rows > kGmmMaxRows || d.n_a_rows < 0 || d.n_out < 1 || d.n_in < 8 || d.n_in > kGmmMaxIn || d.n_in % 8 || d.n_experts < 1 ||
         d.n_experts > BITSMOE_GMM_MAX_EXPERTS || (d.in_type != BITSMOE_F16 && d.in_type != BITSMOE_BF16) ||
         (d.out_type != BITSMOE_F32 && d.out_type != d.in_type) || d.rows_per_a < 1 || d.reserved ||
         (int64_t)d.n_experts * d.n_out > 0x7fffffff - 2 * kGtM)  // a tile's last weight row is an int

@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kShiftThreads, 4) k_norm_shift(const NormParam
     }
 }
 
+constexpr int kNormMaxCols = 1 << 30;  // a column's index and a step of 1024 threads behind it are ints
 constexpr int kNormWarpRows = 8;  // rows (warps) per CTA when a row belongs to a warp
 
 template <int V, bool H32, bool Y32, bool X32>
@@ -444,7 +445,7 @@ using namespace bitsmoe;
 BITSMOE_API int bitsmoe_norm_residual(const bitsmoe_norm_args* args, void* stream) {
     if (!args) return BITSMOE_EINVAL;
     const bitsmoe_norm_args& a = *args;
-    if (a.rows < 0 || a.d < 1 || !elem_ok(a.h_type) || (a.y && !elem_ok(a.y_type)) || (a.x && !elem_ok(a.x_type)))
+    if (a.rows < 0 || a.d < 1 || a.d > kNormMaxCols || !elem_ok(a.h_type) || (a.y && !elem_ok(a.y_type)) || (a.x && !elem_ok(a.x_type)))
         return BITSMOE_EINVAL;
     if (a.rows == 0) return BITSMOE_OK;
     if (!a.h || (!a.h_out && !a.x) || (a.x && !a.w_pre) || (!a.y && (a.w_post || a.gate))) return BITSMOE_EINVAL;

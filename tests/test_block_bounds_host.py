@@ -43,3 +43,15 @@ def test_dense_ffn_refuses_the_down_product_before_the_first_launch(B, bad):
     ok = dict(d_model=64, d_ff=32, E=4, K=2, tokens=3, type=1, x=256, wg=256, wu=256, wd=256, ids=256, gw=256, off=256,
               od=256, out=256, ws=512, st=0, nb=1 << 60, xs=1 << 20)
     assert B.lib().bitsmoe_dense_ffn_forward(struct.pack("@6i11PQq", *{**ok, **bad}.values()), None) == B.EINVAL
+
+
+@pytest.mark.parametrize("d", [2 ** 30 + 1, 2 ** 31 - 1])
+def test_norm_of_more_than_2_30_columns(B, d):
+    args = struct.pack("@7P5q6i2f", 256, 512, 0, 0, 256, 1024, 2048, d, d, 0, d, d, 1, d, 0, 0, 1, 0, 1.0, 1e-6)
+    assert B.lib().bitsmoe_norm_residual(args, None) == B.EINVAL
+
+
+@pytest.mark.parametrize("k", [2 ** 30 + 8, 2 ** 31 - 8])
+def test_grouped_product_over_more_than_2_30_columns(B, k):
+    args = struct.pack("@7Pq10i", 256, 512, 0, 1024, 0, 2048, 0, k, 4, 4, 8, k, 2, 1, 1, 1, 0, 0)
+    assert B.lib().bitsmoe_grouped_matmul(args, None) == B.EINVAL

@@ -693,6 +693,8 @@ def run_ffn(args, dist):
     wl = Workload(cfg, L, max(G, L), seed_base=10_000 + 1000 * dist.rank)
     ffns = [SpectralMoEFFN(layer, synth.make_down(cfg, synth.make_generator(20_000 + 1000 * dist.rank + l, dev), dev))
             for l, layer in enumerate(wl.layers)]
+    for f in ffns:
+        f.workspace(T)  # made before any capture
     bufs = [layer.forward(wl.x[0], wl.ids[0], wl.gw[0], want_experts=True) for layer in wl.layers]
     outs = [torch.empty((T, cfg.d_in), dtype=torch.float32, device=dev) for _ in range(L)]
     torch.cuda.synchronize()

@@ -27,6 +27,10 @@ def _on(stream, like: torch.Tensor):
     return _HERE if dev < 0 or dev == _current_gpu() else torch.cuda.device(dev)
 
 
+def _capturing(t: torch.Tensor) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 class _Workspaces:
     """Workspaces of size(T) bytes for an object's calls of T tokens."""
 
@@ -45,8 +49,10 @@ class _Workspaces:
             n = self._bytes[T] = max(self._size(T), 256)
         if T != 1 or not self._keep_one:
             return torch.empty(n, dtype=torch.uint8, device=self._device)
-        self.one = torch.zeros(n, dtype=torch.uint8, device=self._device)
-        return self.one
+        ws = torch.zeros(n, dtype=torch.uint8, device=self._device)
+        if not _capturing(ws):  # else the zeros are the graph's, filled in at its replays alone
+            self.one = ws
+        return ws
 
 
 class PackedProjection:
@@ -154,6 +160,7 @@ class SpectralMoELayer:
     def workspace(self, T: int) -> torch.Tensor:
         """A workspace for a call of T tokens.  One token's is the layer's own, made and
         zero-filled on first use: its head keeps the fused path's counters between calls.
+        (First use in a stream capture: a call's own, zero-filled at every replay.)
         Any other T uses nothing that an earlier call left and gets a new one."""
         return self._ws.get(T)
 

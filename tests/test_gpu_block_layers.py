@@ -186,3 +186,60 @@ def test_overlapping_calls_of_one_object(kind, T):
     for w, ys in zip(want, got):
         for y in ys:
             assert torch.equal(y, w)
+
+
+@pytest.mark.parametrize("T", [1, 9])
+@pytest.mark.parametrize("kind", ["dense", "fp16", "q4"])
+def test_stack_captured_before_its_first_call(kind, T):
+    """A stack of new blocks captured into a graph and replayed, an eager pass before its first replay and another after:
+    all of them give the same residual stream (one token over the spectral layer: within the outputs' 2e-3 bound, the
+    order of its atomics being open)."""
+    from mixed_precision_decode_b200.layer import MoEBlock, SpectralMoEFFN, SpectralMoELayer
+    g = _gen(3 * T + len(kind))
+    ffns = [_dense(g, 6, 2, 136, 200) if kind == "dense" else _spectral(kind, 60 + b) for b in range(3)]
+    if kind != "dense":
+        ffns = [SpectralMoEFFN(SpectralMoELayer(f.layer.gate, f.layer.up), f.q4 or f.w_down) for f in ffns]
+    d, E = ffns[0].dims.d_model, ffns[0].dims.n_experts
+    blocks = [MoEBlock(f, 1 + 0.1 * _randn(g, d), _randn(g, E, d).half(), w_post=1 + 0.1 * _randn(g, d), alpha=0.5)
+              for f in ffns]
+    h0 = _randn(g, T, d)
+    h = h0.clone()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run():
+        h.copy_(h0)
+        y = before = None
+        for b in blocks:
+            y = b.forward(h, y, status=st, made_by=before)
+            before = b
+        blocks[-1].finish(h, y)
+
+    torch.empty(1, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run()
+    got = []
+    for step in (run, graph.replay, graph.replay, run, graph.replay):
+        h.zero_()
+        step()
+        torch.cuda.synchronize()
+        got.append(h.clone())
+    assert B.read_status(st) == 0 and bool(torch.isfinite(got[0]).all())
+    for other in got[1:]:
+        if T > 1 or kind == "dense":
+            assert torch.equal(other, got[0])
+        else:
+            assert float((other - got[0]).abs().max() / got[0].abs().max()) <= 2e-3
+
+
+@pytest.mark.parametrize("kind", ["dense", "fp16", "q4"])
+def test_empty_batches(kind):
+    from mixed_precision_decode_b200.layer import MoEBlock
+    g = _gen(4)
+    ffn = _dense(g, 6, 2, 136, 200) if kind == "dense" else _spectral(kind, 66)
+    d, E = ffn.dims.d_model, ffn.dims.n_experts
+    blk = MoEBlock(ffn, _randn(g, d), _randn(g, E, d).half())
+    h = _randn(g, 0, d)
+    y = blk.forward(h)
+    assert y.shape == (0, d) and blk.finish(h, blk.forward(h, y, made_by=blk)).shape == (0, d)

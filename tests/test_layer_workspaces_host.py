@@ -62,6 +62,19 @@ def test_calls_of_several_tokens_share_nothing(used, kind):
 
 
 @pytest.mark.parametrize("kind", ["layer", "fp16"])
+def test_one_tokens_state_made_in_a_capture_is_the_graphs(used, kind, monkeypatch):
+    """Zeros that are filled in when a graph is replayed must not serve a call outside it."""
+    obj = _object(kind)
+    monkeypatch.setattr(L, "_capturing", lambda t: True)
+    _call(obj, 1)
+    monkeypatch.setattr(L, "_capturing", lambda t: False)
+    _call(obj, 1)
+    _call(obj, 1)
+    (_, a, _), (_, b, _), (_, c, _) = used
+    assert a is not b and b is c
+
+
+@pytest.mark.parametrize("kind", ["layer", "fp16"])
 def test_one_tokens_state_is_kept_and_begins_as_zeros(used, kind):
     obj = _object(kind)
     for _ in range(2):

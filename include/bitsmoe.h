@@ -514,7 +514,8 @@ typedef struct {
     const int32_t *topk_ids;   /* dev [tokens][top_k] */
     const float *gate_w;       /* dev [tokens][top_k], applied as given */
     float *out;                /* dev [tokens][d_model] */
-    void *workspace;           /* dev, 256-byte aligned, no initialisation; NULL when its size is 0 */
+    void *workspace;           /* dev, 256-byte aligned, no initialisation; NULL when its size is 0.  Calls that
+                                  share it must not overlap. */
     int32_t *status;           /* dev or NULL */
     uint64_t workspace_bytes;
 } bitsmoe_q4_args;
@@ -582,7 +583,7 @@ typedef struct {
     const int32_t *offsets;    /* dev [E + 1], and */
     const int32_t *order;      /* dev [tokens top_k]: the grouping of topk_ids */
     float *out;                /* dev [tokens][d_model] */
-    void *workspace;           /* dev, 256-byte aligned, no initialisation */
+    void *workspace;           /* dev, 256-byte aligned, no initialisation.  Calls that share it must not overlap. */
     int32_t *status;           /* dev or NULL */
     uint64_t workspace_bytes;
     int64_t x_stride;
